@@ -48,7 +48,7 @@ def listed():
              sections="16,24,24", interleaved=False, inverse=False, dtype="f16", theta=500000.0),
         # A prompt with images, heads of the long-context workload.
         dict(name="rope_prompt", op="rope", tokens=16384, hq=24, hkv=4, dim=256, rot=256,
-             sections="32,48,48", interleaved=True, inverse=False, dtype="bf16", theta=10000.0),
+             sections="44,42,42", interleaved=True, inverse=False, dtype="bf16", theta=10000.0),
         # fp32, odd token count, half of each head rotated, turned back (a gradient, or keys
         # that are to be moved).
         dict(name="rope_back_f32", op="rope", tokens=2049, hq=8, hkv=4, dim=64, rot=32,
