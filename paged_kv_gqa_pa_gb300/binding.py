@@ -34,7 +34,10 @@ _TORCH_DTYPE = {PA_DTYPE_F16: torch.float16, PA_DTYPE_BF16: torch.bfloat16,
 
 EXPORTED = ("pa_plan", "pa_plan_ex", "pa_decode", "pa_decode_partitions", "pa_merge",
             "pa_get_error", "pa_get_error_ex", "pa_status_string", "pa_version",
-            "pa_decode_static")
+            "pa_decode_static",
+            # include/pa_q4.h (q4.py)
+            "pa_q4_page_bytes", "pa_q4_write", "pa_q4_read", "pa_q4_plan", "pa_q4_decode",
+            "pa_extend_tables", "pa_rope_axes")
 
 
 class pa_plan_t(ctypes.Structure):

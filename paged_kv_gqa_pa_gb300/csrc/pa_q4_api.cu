@@ -1,0 +1,211 @@
+// pa_q4_api.cu -- planning, argument checks and launch of the decode
+// attention over the 4-bit cache (include/pa_q4.h).
+#include <limits.h>
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "pa_q4_attend.cuh"
+
+namespace pa {
+
+#define PA_Q4_EXTERN(D)                                                                          \
+    extern template cudaError_t launch_q4_attend_d<D, __half>(const Q4AttendParams&, dim3,       \
+                                                              cudaStream_t);                     \
+    extern template cudaError_t launch_q4_attend_d<D, __nv_bfloat16>(const Q4AttendParams&, dim3, \
+                                                                     cudaStream_t);
+PA_Q4_EXTERN(64)
+PA_Q4_EXTERN(96)
+PA_Q4_EXTERN(128)
+PA_Q4_EXTERN(256)
+#undef PA_Q4_EXTERN
+
+constexpr int kQ4MaxBatch = 4096;
+
+// Workspace: [control block | arrival counters, groups x B | (max, sum) of the
+// partials | their outputs], each 256-byte aligned; two partials per CTA.
+struct Q4WsLayout {
+    size_t ctr_off, ctrl_bytes, ml_off, o_off, total;
+};
+
+static size_t q4_align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+static Q4WsLayout q4_ws_layout(int B, int G, int D, long long groups, int X) {
+    Q4WsLayout w;
+    const size_t rows = (size_t)groups * X * 2 * G;
+    w.ctr_off = kCtrlBytes;
+    w.ctrl_bytes = kCtrlBytes + q4_align256((size_t)groups * B * 4);
+    w.ml_off = w.ctrl_bytes;
+    w.o_off = w.ml_off + q4_align256(rows * 8);
+    w.total = w.o_off + q4_align256(rows * D * 4);
+    return w;
+}
+
+static int q4_ctas_per_sm(int D, int B) {
+    int smem = 0;
+    switch (D) {
+        case 64: smem = Q4Cfg<64>::smem(B); break;
+        case 96: smem = Q4Cfg<96>::smem(B); break;
+        case 128: smem = Q4Cfg<128>::smem(B); break;
+        default: smem = Q4Cfg<256>::smem(B); break;
+    }
+    return std::max(1, std::min(3, 228 * 1024 / (smem + 1024 + 32)));
+}
+
+// What a plan's shapes must satisfy; the automatic fields are checked by the caller.
+static int q4_check_shapes(const pa_q4_plan_t* p) {
+    if (p->batch < 0 || p->num_q_heads <= 0 || p->num_kv_heads <= 0 ||
+        p->num_q_heads % p->num_kv_heads != 0 || p->head_dim <= 0 || p->page_size <= 0 ||
+        p->num_pages <= 0 || p->max_pages_per_seq <= 0 || p->max_context_len < 0 ||
+        p->window < 0 || p->num_sms < 0)
+        return PA_ERR_INVALID_ARG;
+    if (p->dtype != PA_DTYPE_F16 && p->dtype != PA_DTYPE_BF16 && p->dtype != PA_DTYPE_F32)
+        return PA_ERR_INVALID_ARG;
+    if ((long long)p->max_context_len > (long long)p->max_pages_per_seq * p->page_size)
+        return PA_ERR_INVALID_ARG;
+    if (p->dtype == PA_DTYPE_F32 || !q4_head_dim_ok(p->head_dim) || p->page_size != kPageSize ||
+        p->batch > kQ4MaxBatch)
+        return PA_ERR_UNSUPPORTED;
+    // The batch's pages end to end are counted in 32 bits.
+    const long long span = ((long long)p->max_context_len + kPageSize - 1) / kPageSize;
+    if (span * std::max(1, p->batch) > (1ll << 30)) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+int pa_q4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+               int num_pages, int max_pages_per_seq, int max_context_len, int window,
+               int num_sms, int dtype, pa_q4_plan_t* plan) {
+    if (!plan) return PA_ERR_INVALID_ARG;
+    memset(plan, 0, sizeof(*plan));
+    pa_q4_plan_t p = {};
+    p.batch = batch;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.max_pages_per_seq = max_pages_per_seq;
+    p.max_context_len = max_context_len;
+    p.window = window;
+    p.num_sms = num_sms;
+    p.dtype = dtype;
+    const int st = q4_check_shapes(&p);
+    if (st != PA_OK) return st;
+    const int g = num_q_heads / num_kv_heads;
+    const int nchunk = (g + kMaxHeadsPerCta - 1) / kMaxHeadsPerCta;
+    if (g % nchunk != 0) return PA_ERR_UNSUPPORTED;
+    const long long groups = (long long)num_kv_heads * nchunk;
+    if (groups > 65535) return PA_ERR_UNSUPPORTED;
+    if (p.num_sms == 0) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&p.num_sms, cudaDevAttrMultiProcessorCount, dev) !=
+                cudaSuccess) {
+            cudaGetLastError();
+            return PA_ERR_CUDA;
+        }
+    }
+    p.heads_per_cta = g / nchunk;
+    // One wave of resident CTAs over all groups, but no more than the ranges
+    // of kQ4MinPages pages that the longest batch has.
+    int span = (max_context_len + kPageSize - 1) / kPageSize;
+    if (window > 0) span = std::min(span, (window - 1 + kPageSize - 1) / kPageSize + 1);
+    const long long pages = std::max(1ll, (long long)std::max(1, batch) * span);
+    const long long slots = (long long)p.num_sms * q4_ctas_per_sm(head_dim, batch);
+    long long x = std::max(1ll, slots / groups);
+    x = std::min(x, (pages + kQ4MinPages - 1) / kQ4MinPages);
+    p.ctas_per_group = (int)x;
+    p.ctas = (int)std::min<long long>(x * groups, INT_MAX);
+    const Q4WsLayout wl = q4_ws_layout(batch, p.heads_per_cta, head_dim, groups, p.ctas_per_group);
+    if (wl.ctrl_bytes > (size_t)INT_MAX) return PA_ERR_UNSUPPORTED;
+    p.workspace_bytes = wl.total;
+    p.ctrl_bytes = (int)wl.ctrl_bytes;
+    *plan = p;
+    return PA_OK;
+}
+
+int pa_q4_decode(const pa_q4_plan_t* plan, const void* q, const void* cache,
+                 const int32_t* block_tables, const int32_t* context_lens, float scale,
+                 int window, void* out, float* lse, void* workspace, void* stream) {
+    if (!plan) return PA_ERR_INVALID_ARG;
+    const int st = q4_check_shapes(plan);
+    if (st != PA_OK) return st;
+    const int g = plan->num_q_heads / plan->num_kv_heads;
+    const int G = plan->heads_per_cta, X = plan->ctas_per_group, D = plan->head_dim;
+    if (G < 1 || G > kMaxHeadsPerCta || g % G != 0 || X < 1 || X > (1 << 20) ||
+        window != plan->window || plan->test_stall_bytes < 0 || plan->test_stall_bytes > 4096)
+        return PA_ERR_INVALID_ARG;
+    const long long groups = (long long)plan->num_kv_heads * (g / G);
+    if (groups > 65535) return PA_ERR_UNSUPPORTED;
+    const Q4WsLayout wl = q4_ws_layout(plan->batch, G, D, groups, X);
+    if (plan->workspace_bytes < wl.total || plan->ctrl_bytes < 0 ||
+        (size_t)plan->ctrl_bytes < wl.ctrl_bytes)
+        return PA_ERR_INVALID_ARG;
+    if (!workspace) return PA_ERR_WORKSPACE;
+    if ((uintptr_t)workspace & 15u) return PA_ERR_INVALID_ARG;
+    if (plan->batch == 0) return PA_OK;
+    if (!q || !cache || !block_tables || !context_lens || !out || !lse) return PA_ERR_INVALID_ARG;
+    if (((uintptr_t)q & 15u) || ((uintptr_t)cache & 15u) || ((uintptr_t)out & 15u))
+        return PA_ERR_INVALID_ARG;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    Q4AttendParams p;
+    p.q = q;
+    p.cache = static_cast<const unsigned char*>(cache);
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.out = out;
+    p.lse = lse;
+    p.ws_o = reinterpret_cast<float*>(ws + wl.o_off);
+    p.ws_ml = reinterpret_cast<float*>(ws + wl.ml_off);
+    p.counters = reinterpret_cast<unsigned*>(ws + wl.ctr_off);
+    p.err = reinterpret_cast<unsigned*>(ws);
+    p.B = plan->batch;
+    p.Hq = plan->num_q_heads;
+    p.Hkv = plan->num_kv_heads;
+    p.g = g;
+    p.num_pages = plan->num_pages;
+    p.maxp = plan->max_pages_per_seq;
+    p.max_ctx = plan->max_context_len;
+    p.window = plan->window;
+    p.nchunk = g / G;
+    p.G = G;
+    p.X = X;
+    p.stall_tx = plan->test_stall_bytes;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    const dim3 grid(X, (unsigned)groups);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf = plan->dtype == PA_DTYPE_BF16;
+    cudaError_t e;
+    switch (D) {
+        case 64:
+            e = bf ? launch_q4_attend_d<64, __nv_bfloat16>(p, grid, s)
+                   : launch_q4_attend_d<64, __half>(p, grid, s);
+            break;
+        case 96:
+            e = bf ? launch_q4_attend_d<96, __nv_bfloat16>(p, grid, s)
+                   : launch_q4_attend_d<96, __half>(p, grid, s);
+            break;
+        case 128:
+            e = bf ? launch_q4_attend_d<128, __nv_bfloat16>(p, grid, s)
+                   : launch_q4_attend_d<128, __half>(p, grid, s);
+            break;
+        default:
+            e = bf ? launch_q4_attend_d<256, __nv_bfloat16>(p, grid, s)
+                   : launch_q4_attend_d<256, __half>(p, grid, s);
+            break;
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return PA_ERR_CUDA;
+    }
+    return PA_OK;
+}
+
+}  // extern "C"

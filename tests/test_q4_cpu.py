@@ -1,0 +1,265 @@
+"""Host-side tests of include/pa_q4.h (no GPU): the reference the GPU tests use
+is checked against properties of the definitions, plans and argument checks
+return before anything is launched, and the ctypes mirror follows the header."""
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_gqa_pa_gb300 as pa
+import q4_reference as ref
+from paged_kv_gqa_pa_gb300 import binding, q4
+from paged_kv_gqa_pa_gb300 import build as pa_build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    pa_build.build()
+    return q4._lib()
+
+
+def test_plan_struct_layout_matches_header():
+    text = open(os.path.join(ROOT, "include", "pa_q4.h")).read()
+    body = re.search(r"typedef struct pa_q4_plan \{(.*?)\} pa_q4_plan_t;", text, flags=re.S).group(1)
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    fields = re.findall(r"\b(?:int|size_t|float)\s+([a-z_0-9]+)\s*;", body)
+    assert fields == [f for f, _ in q4.pa_q4_plan_t._fields_]
+    assert q4.pa_q4_plan_t.workspace_bytes.offset == 56
+    assert ctypes.sizeof(q4.pa_q4_plan_t) == 72
+
+
+def test_page_bytes():
+    assert [pa.pa_q4_page_bytes(d) for d in (64, 96, 128, 256)] == [1280, 1920, 2560, 5120]
+    assert [pa.pa_q4_page_bytes(d) for d in (0, -64, 32, 80, 512)] == [0] * 5
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+def test_layout_covers_the_block_once_and_tokens_own_their_bytes(D):
+    owner = {}
+    nib = set()
+    for r in range(16):
+        for d in range(D):
+            for place in (ref.k_place, ref.v_place):
+                at, sh = place(D, r, d)
+                assert (at, sh) not in nib and 0 <= at < 16 * D
+                nib.add((at, sh))
+                assert owner.setdefault(at, r) == r
+        for n in range(D // 32):
+            for cell in (ref.k_cell, ref.v_cell):
+                for at in cell(D, r, n):
+                    assert at % 2 == 0 and 16 * D <= at < 20 * D
+                    assert owner.setdefault(at, r) == r and owner.setdefault(at + 1, r) == r
+    assert len(nib) == 32 * D and len(owner) == 20 * D
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_quantisation_error_is_about_half_a_step(dtype):
+    g = np.random.default_rng(1)
+    grid = {"f16": 1 / 64, "bf16": 1 / 8}[dtype]
+    for _ in range(200):
+        x = ref.rn(g.standard_normal(32) * 10.0 ** g.uniform(-2, 2), dtype)
+        c, s, z = ref.quantise(x, dtype)
+        assert x.min() < 0 < x.max()
+        got = ref.values(c, s, z, dtype)
+        # half a step, the grid's shift, and the value's rounding
+        assert (np.abs(got - x) <= s[0] * (0.5 + grid) + ref.HALF_STEP[dtype] * np.abs(got)).all()
+
+
+def test_quantisation_corners():
+    for dtype in ("f16", "bf16"):
+        c, s, z = ref.quantise(np.full(32, 3.5), dtype)       # constant: exact
+        assert s[0] == 0 and (ref.values(c, s, z, dtype) == 3.5).all()
+        x = np.zeros(32)
+        x[3] = np.nan
+        assert np.isnan(ref.values(*ref.quantise(x, dtype), dtype)).all()
+        x[3] = np.inf                                           # saturates at the limit
+        got = ref.values(*ref.quantise(x, dtype), dtype)
+        assert np.isfinite(got).all() and got[3] == got.max() > 0.9 * ref.LIMIT[dtype]
+
+
+def _plan(**kw):
+    a = dict(batch=2, num_q_heads=8, num_kv_heads=2, head_dim=128, page_size=16, num_pages=64,
+             max_pages_per_seq=16, max_context_len=256, window=0, num_sms=152, dtype=0)
+    a.update(kw)
+    return pa.pa_q4_plan(**a)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(num_q_heads=7), binding.PA_ERR_INVALID_ARG),
+    (dict(num_kv_heads=0), binding.PA_ERR_INVALID_ARG),
+    (dict(batch=-1), binding.PA_ERR_INVALID_ARG),
+    (dict(max_context_len=257), binding.PA_ERR_INVALID_ARG),
+    (dict(max_context_len=-1), binding.PA_ERR_INVALID_ARG),
+    (dict(window=-1), binding.PA_ERR_INVALID_ARG),
+    (dict(num_pages=0), binding.PA_ERR_INVALID_ARG),
+    (dict(dtype=5), binding.PA_ERR_INVALID_ARG),
+    (dict(num_sms=-1), binding.PA_ERR_INVALID_ARG),
+    (dict(dtype=binding.PA_DTYPE_F32), binding.PA_ERR_UNSUPPORTED),
+    (dict(head_dim=80), binding.PA_ERR_UNSUPPORTED),
+    (dict(page_size=32, max_pages_per_seq=8), binding.PA_ERR_UNSUPPORTED),
+    (dict(batch=4097), binding.PA_ERR_UNSUPPORTED),
+    (dict(num_q_heads=22, num_kv_heads=2), binding.PA_ERR_UNSUPPORTED),  # g = 11
+    (dict(batch=4096, max_pages_per_seq=1 << 20, max_context_len=1 << 24),
+     binding.PA_ERR_UNSUPPORTED),
+])
+def test_plan_rejects(kw, status):
+    with pytest.raises(pa.PAError) as e:
+        _plan(**kw)
+    assert e.value.status == status
+
+
+def test_plan_fields():
+    p = _plan(batch=64, num_q_heads=32, num_kv_heads=8, max_context_len=4096,
+              max_pages_per_seq=256, num_pages=20000)
+    assert p.heads_per_cta == 4 and p.ctas == p.ctas_per_group * 8 <= 3 * 152
+    # two partials per CTA: o, maximum and sum of its heads
+    assert p.workspace_bytes >= p.ctrl_bytes + p.ctas * 2 * 4 * (128 + 2) * 4
+    assert p.ctrl_bytes >= 256 + 8 * 64 * 4
+    # sixteen query heads per KV head: two chunks
+    p = _plan(num_q_heads=32, num_kv_heads=2)
+    assert p.heads_per_cta == 8 and p.ctas == p.ctas_per_group * 4
+    # no more CTAs than ranges of 8 pages
+    assert _plan(batch=1, max_context_len=100).ctas_per_group == 1
+    assert _plan(batch=0).ctas_per_group >= 1
+
+
+FAKE = 1 << 20  # aligned, never dereferenced: every call below is refused on the host
+
+
+def test_decode_checks_return_before_launch(lib):
+    plan = _plan()
+    base = [ctypes.byref(plan), FAKE, FAKE, FAKE, FAKE, 1.0, 0, FAKE, FAKE, FAKE, None]
+    IA, WS = binding.PA_ERR_INVALID_ARG, binding.PA_ERR_WORKSPACE
+
+    def call(**at):
+        a = list(base)
+        for i, v in at.items():
+            a[int(i[1:])] = v
+        return lib.pa_q4_decode(*a)
+
+    assert call(_0=None) == IA
+    for i in (1, 2, 3, 4, 7, 8):
+        assert call(**{f"_{i}": None}) == IA
+    for i in (1, 2, 7, 9):
+        assert call(**{f"_{i}": FAKE + 8}) == IA
+    assert call(_9=None) == WS
+    assert call(_6=5) == IA  # another window than the plan's
+    for field, value, st in [("heads_per_cta", 3, IA), ("heads_per_cta", 0, IA),
+                             ("ctas_per_group", 0, IA), ("workspace_bytes", 256, IA),
+                             ("ctrl_bytes", 256, IA), ("test_stall_bytes", 5000, IA),
+                             ("num_q_heads", 9, IA), ("head_dim", 100, binding.PA_ERR_UNSUPPORTED),
+                             ("max_context_len", 1 << 20, IA),
+                             ("ctas_per_group", plan.ctas_per_group + 1, IA)]:
+        bad = q4.pa_q4_plan_t.from_buffer_copy(plan)
+        setattr(bad, field, value)
+        assert call(_0=ctypes.byref(bad)) == st, field
+    empty = _plan(batch=0)
+    assert call(_0=ctypes.byref(empty), _1=None, _2=None) == binding.PA_OK
+
+
+@pytest.mark.parametrize("fn", ["pa_q4_write", "pa_q4_read"])
+def test_cache_call_checks_return_before_launch(lib, fn):
+    IA, UN = binding.PA_ERR_INVALID_ARG, binding.PA_ERR_UNSUPPORTED
+
+    def call(n=4, hkv=2, D=128, ps=16, pages=8, dtype=0, k=FAKE, ks=256, v=FAKE, vs=256,
+             slots=FAKE, cache=FAKE, err=None):
+        if fn == "pa_q4_write":
+            return lib.pa_q4_write(n, hkv, D, ps, pages, dtype, k, ks, v, vs, slots, cache, err,
+                                   None)
+        return lib.pa_q4_read(n, hkv, D, ps, pages, dtype, cache, slots, k, ks, v, vs, err, None)
+
+    assert call(n=0, k=None, v=None, slots=None, cache=None) == binding.PA_OK
+    for kw in (dict(n=-1), dict(hkv=0), dict(pages=0), dict(dtype=7), dict(ks=255), dict(vs=260),
+               dict(ks=-256), dict(k=None), dict(v=None), dict(slots=None), dict(cache=None),
+               dict(k=FAKE + 8), dict(v=FAKE + 2), dict(cache=FAKE + 4), dict(slots=FAKE + 4),
+               dict(err=FAKE + 2), dict(ks=1 << 50)):
+        assert call(**kw) == IA, kw
+    for kw in (dict(dtype=2), dict(D=80), dict(ps=8), dict(hkv=40000, ks=1 << 30, vs=1 << 30)):
+        assert call(**kw) == UN, kw
+
+
+def test_tables_checks_return_before_launch(lib):
+    IA, UN = binding.PA_ERR_INVALID_ARG, binding.PA_ERR_UNSUPPORTED
+    names = ["past", "new", "free", "bt", "lens", "starts", "slots", "pos", "taken", "err"]
+    ptr = {n: FAKE + 64 * i for i, n in enumerate(names)}
+
+    def call(B=2, maxp=4, ps=16, pages=8, nfree=3, cap=5, **kw):
+        p = dict(ptr, **kw)
+        return lib.pa_extend_tables(B, maxp, ps, pages, nfree, cap, *[p[n] for n in names], None)
+
+    for kw in (dict(B=-1), dict(maxp=0), dict(pages=0), dict(nfree=-1), dict(cap=-1)):
+        assert call(**kw) == IA, kw
+    for n in names[:-1]:
+        assert call(**{n: None}) == IA, n
+    for n in names:
+        assert call(**{n: FAKE + 2}) == IA, n
+    assert call(slots=FAKE + 4) == IA
+    assert call(lens=ptr["past"]) == IA and call(starts=ptr["new"]) == IA
+    assert call(B=8193) == UN and call(ps=8) == UN and call(maxp=1 << 27) == UN
+
+
+def test_rope_checks_return_before_launch(lib):
+    IA, UN = binding.PA_ERR_INVALID_ARG, binding.PA_ERR_UNSUPPORTED
+
+    def call(n=4, hq=4, hk=2, D=128, R=128, sections=(16, 24, 24), axes=None, inter=0, inv=0,
+             theta=1e4, dtype=0, q=FAKE, qs=512, k=FAKE, ks=256, pos=FAKE, qo=FAKE, qos=512,
+             ko=FAKE, kos=256):
+        arr = (ctypes.c_int * max(1, len(sections)))(*sections)
+        return lib.pa_rope_axes(n, hq, hk, D, R, len(sections) if axes is None else axes, arr,
+                                inter, inv, theta, dtype, q, qs, k, ks, pos, qo, qos, ko, kos,
+                                None)
+
+    assert call(n=0) == binding.PA_OK
+    assert call(hq=0, hk=0) == binding.PA_OK
+    for kw in (dict(n=-1), dict(hq=-1), dict(R=0), dict(R=144), dict(sections=(64, 1)),
+               dict(sections=(65, -1)), dict(axes=0), dict(sections=(13, 13, 13, 13, 12)),
+               dict(theta=0.0), dict(theta=float("nan")), dict(theta=float("inf")),
+               dict(dtype=3), dict(inter=2), dict(inv=-1), dict(q=None), dict(ko=None),
+               dict(pos=None), dict(q=FAKE + 8), dict(ko=FAKE + 2), dict(qs=508), dict(kos=264 - 4),
+               dict(pos=FAKE + 2), dict(qos=520),  # in place with another stride
+               dict(sections=(10, 44, 10), inter=1)):
+        assert call(**kw) == IA, kw
+    for kw in (dict(D=120, R=112, sections=(56,)), dict(D=512), dict(R=24, sections=(12,))):
+        assert call(**kw) == UN, kw
+
+
+def test_binding_refuses_host_tensors_and_wrong_arguments():
+    k = torch.zeros(2, 1, 64, dtype=torch.float16)
+    slots = torch.zeros(2, dtype=torch.int64)
+    cache = torch.zeros(1, 1, 1280, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="CUDA"):
+        pa.pa_q4_write(k, k, slots, cache)
+    with pytest.raises(ValueError, match="CUDA"):
+        pa.pa_q4_read(cache, slots, k, k)
+    with pytest.raises(TypeError):
+        pa.pa_q4_write(None, k, slots, cache)
+    with pytest.raises(ValueError, match="CUDA"):
+        pa.pa_rope_axes(k, k, torch.zeros(1, 2, dtype=torch.int32), (32,), 1e4)
+    with pytest.raises(ValueError, match="q or k"):
+        pa.pa_rope_axes(None, None, None, (32,), 1e4)
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        pa.pa_extend_tables(i, i, i, 4, i.view(1, 2), i, i, slots, i, i)
+    plan = _plan()
+    with pytest.raises(ValueError, match="CUDA"):
+        pa.pa_q4_decode(plan, k, cache, i, i, 1.0, 0, k, k, cache)
+    with pytest.raises(ValueError):
+        pa.new_q4_cache(1, 1, 80, "cpu")
+    assert pa.new_q4_cache(3, 2, 96, "cpu").shape == (3, 2, 1920)
+
+
+def test_reference_tables_by_hand():
+    # 20 tokens held, 13 more: a third page; then an idle request; then a new one.
+    bt = np.full((3, 4), -1, np.int32)
+    bt[0, :2] = [7, 5]
+    bt[1, :1] = [9]
+    got = ref.extend_tables([20, 16, 0], [13, 0, 2], [3, 1, 4], 10, bt, 17)
+    assert got[0].tolist() == [[7, 5, 3, -1], [9, -1, -1, -1], [1, -1, -1, -1]]
+    assert got[1].tolist() == [33, 16, 2] and got[2].tolist() == [0, 13, 13, 15]
+    assert got[3].tolist() == [5 * 16 + 4 + i for i in range(12)] + [48, 16, 17, -1, -1]
+    assert got[4].tolist() == list(range(20, 33)) + [0, 1, 0, 0] and got[5:] == (2, 0)
