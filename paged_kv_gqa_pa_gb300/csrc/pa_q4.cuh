@@ -55,6 +55,14 @@ struct Q4Layout {
     }
 };
 
+// (x & mask) | bits as one lop3: written with & and | the compiler keeps both
+// constants immediate and spends two.
+__device__ __forceinline__ uint32_t q4_join(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
+    return d;
+}
+
 // Element-type specifics.  A code c becomes the 16-bit float 16 + c: 16 has a
 // zero mantissa, and its unit in the last place is 2^-6 (fp16) or 2^-3
 // (bf16), so c is shifted to bit 6 (3) and joined to 16's bits.
@@ -68,7 +76,7 @@ struct Q4Type<__half> {
     template <int P>
     __device__ static __forceinline__ uint32_t code16(uint32_t w) {
         const uint32_t x = P == 0 ? w << 6 : (P == 1 ? w << 2 : (P == 2 ? w >> 2 : w >> 6));
-        return (x & 0x03C003C0u) | 0x4C004C00u;
+        return q4_join(x, 0x03C003C0u, 0x4C004C00u);
     }
     __device__ static __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
         uint32_t d;
@@ -78,6 +86,11 @@ struct Q4Type<__half> {
     __device__ static __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
         uint32_t d;
         asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    __device__ static __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
         return d;
     }
     __device__ static __forceinline__ float to_float(uint32_t bits) {
@@ -104,7 +117,7 @@ struct Q4Type<__nv_bfloat16> {
     template <int P>
     __device__ static __forceinline__ uint32_t code16(uint32_t w) {
         const uint32_t x = P == 0 ? w << 3 : (P == 1 ? w >> 1 : (P == 2 ? w >> 5 : w >> 9));
-        return (x & 0x00780078u) | 0x41804180u;
+        return q4_join(x, 0x00780078u, 0x41804180u);
     }
     __device__ static __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
         uint32_t d;
@@ -114,6 +127,11 @@ struct Q4Type<__nv_bfloat16> {
     __device__ static __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
         uint32_t d;
         asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    __device__ static __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
         return d;
     }
     __device__ static __forceinline__ float to_float(uint32_t bits) {

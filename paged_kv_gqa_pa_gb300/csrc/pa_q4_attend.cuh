@@ -34,6 +34,8 @@
 #include <math.h>
 
 #include <atomic>
+#include <climits>
+#include <type_traits>
 
 #include "pa_q4.cuh"
 
@@ -61,16 +63,22 @@ struct Q4AttendParams {
 
 template <int D>
 struct Q4Cfg {
-    static constexpr int kStages = D == 256 ? 2 : (D == 128 ? 5 : 6);
-    static constexpr int kRingBytes = kWarps * kStages * Q4Layout<D>::kPageBytes;
-    // The warps' O meet in shared memory 128 dims at a time.
-    static constexpr int kRoundDims = D < 128 ? D : 128;
+    // Pages of a ring slot: two where a page is little work (what a page costs
+    // beside its elements -- the wait, the vote, the request -- is then paid
+    // once for two, and two chains of mma overlap), one at D 256.
+    static constexpr int kPair = D == 256 ? 1 : 2;
+    static constexpr int kSlotBytes = kPair * Q4Layout<D>::kPageBytes;
+    static constexpr int kStages = D == 64 ? 6 : (D == 96 ? 4 : 3);
+    static constexpr int kRingBytes = kWarps * kStages * kSlotBytes;
+    // The warps' O meet in shared memory so many dims at a time.
+    static constexpr int kRoundDims = D == 96 ? 32 : 64;
     static constexpr int kRounds = D / kRoundDims;
     static constexpr int kXStride = kRoundDims + 4;
     static constexpr int kXBytes = kWarps * kMaxHeadsPerCta * kXStride * 4;
     static constexpr int kSmemBytes = kRingBytes + kXBytes + kQ4StagedPages * 4 +
                                       kWarps * kMaxHeadsPerCta * 3 * 4 + kWarps * kStages * 8;
     static constexpr int kMinBlocks = 3;
+    static_assert(kMinBlocks * (kSmemBytes + 1024 + 128) <= 228 * 1024, "CTAs per SM");
     // (the sums over the batch, B + 1 words, follow)
     static int smem(int B) { return kSmemBytes + (B + 1) * 4; }
 };
@@ -189,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     const int kvh = blockIdx.y / p.nchunk;
     const int h0 = kvh * p.g + (blockIdx.y % p.nchunk) * G;
     const uint32_t bar_w = smem_u32(bars) + warp * NS * 8;
-    unsigned char* ring_w = ring + warp * NS * PB;
+    unsigned char* ring_w = ring + warp * NS * Cfg::kSlotBytes;
     const uint32_t ring_u = smem_u32(ring_w);
 
     allow_dependent_launch();
@@ -301,66 +309,87 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         bad = dead;
     };
 
-    // ---- One page in shared memory.
-    auto page = [&](const unsigned char* blk, int tok0) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        const bool whole = tok0 >= seq_start && tok0 + kPageSize <= seq_L;
+    // ---- N consecutive pages in shared memory; MASK: some of their tokens may
+    // lie outside the attended range (their cells may hold anything).
+    auto pages = [&](const unsigned char* blk0, int tok0, auto n_pages, auto mask) {
+        constexpr int N = decltype(n_pages)::value;
+        constexpr bool MASK = decltype(mask)::value;
+        float s[N][4];
         // K: tokens g and g + 8 of this lane's dims.
 #pragma unroll
-        for (int sl = 0; sl < W / V; ++sl) {  // runs of V words that one read takes
-            uint32_t ka[V], kb[V];
-            uint32_t pa_, pb_;  // (s, z) of the run's group
-            if constexpr (D == 96) {
-                q4_lds<V>(ka, blk + g * (D / 2) + 16 * sl + 4 * t);
-                q4_lds<V>(kb, blk + (g + 8) * (D / 2) + 16 * sl + 4 * t);
-                pa_ = *reinterpret_cast<const uint32_t*>(blk + L::k_params(0, sl) + g * 12);
-                pb_ = *reinterpret_cast<const uint32_t*>(blk + L::k_params(8, sl) + g * 12);
-            } else {
-                const unsigned char* row = blk + sl * (8 * L::kSlice) + lane * (4 * V);
-                q4_lds<V>(ka, row);
-                q4_lds<V>(kb, row + 8 * (L::kSlice / 2));
-                const int n = D == 64 ? t >> 1 : t;
-                const unsigned char* par = blk + L::kKParams + sl * (kPageSize * 4 * L::kSliceGroups);
-                pa_ = *reinterpret_cast<const uint32_t*>(par + (g * L::kSliceGroups + n) * 4);
-                pb_ = *reinterpret_cast<const uint32_t*>(par + ((g + 8) * L::kSliceGroups + n) * 4);
-            }
-            const uint32_t sa = __byte_perm(pa_, pa_, 0x1010), za = __byte_perm(pa_, pa_, 0x3232);
-            const uint32_t sb = __byte_perm(pb_, pb_, 0x1010), zb = __byte_perm(pb_, pb_, 0x3232);
+        for (int j = 0; j < N; ++j) {
+            const unsigned char* blk = blk0 + j * PB;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int w = sl * V + i;
-                M::mma(s, Q::fma2(sa, Q::template code16<0>(ka[i]), za),
-                       Q::fma2(sb, Q::template code16<0>(kb[i]), zb),
-                       Q::fma2(sa, Q::template code16<1>(ka[i]), za),
-                       Q::fma2(sb, Q::template code16<1>(kb[i]), zb), qf[w][0], qf[w][1]);
-                M::mma(s, Q::fma2(sa, Q::template code16<2>(ka[i]), za),
-                       Q::fma2(sb, Q::template code16<2>(kb[i]), zb),
-                       Q::fma2(sa, Q::template code16<3>(ka[i]), za),
-                       Q::fma2(sb, Q::template code16<3>(kb[i]), zb), qf[w][2], qf[w][3]);
+            for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
+#pragma unroll
+            for (int sl = 0; sl < W / V; ++sl) {  // runs of V words that one read takes
+                uint32_t ka[V], kb[V];
+                uint32_t pa_, pb_;  // (s, z) of the run's group
+                if constexpr (D == 96) {
+                    q4_lds<V>(ka, blk + g * (D / 2) + 16 * sl + 4 * t);
+                    q4_lds<V>(kb, blk + (g + 8) * (D / 2) + 16 * sl + 4 * t);
+                    pa_ = *reinterpret_cast<const uint32_t*>(blk + L::k_params(0, sl) + g * 12);
+                    pb_ = *reinterpret_cast<const uint32_t*>(blk + L::k_params(8, sl) + g * 12);
+                } else {
+                    const unsigned char* row = blk + sl * (8 * L::kSlice) + lane * (4 * V);
+                    q4_lds<V>(ka, row);
+                    q4_lds<V>(kb, row + 8 * (L::kSlice / 2));
+                    const int n = D == 64 ? t >> 1 : t;
+                    const unsigned char* par =
+                        blk + L::kKParams + sl * (kPageSize * 4 * L::kSliceGroups) +
+                        (g * L::kSliceGroups + n) * 4;
+                    pa_ = *reinterpret_cast<const uint32_t*>(par);
+                    pb_ = *reinterpret_cast<const uint32_t*>(par + 8 * L::kSliceGroups * 4);
+                }
+                const uint32_t sa = __byte_perm(pa_, pa_, 0x1010), za = __byte_perm(pa_, pa_, 0x3232);
+                const uint32_t sb = __byte_perm(pb_, pb_, 0x1010), zb = __byte_perm(pb_, pb_, 0x3232);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int w = sl * V + i;
+                    M::mma(s[j], Q::fma2(sa, Q::template code16<0>(ka[i]), za),
+                           Q::fma2(sb, Q::template code16<0>(kb[i]), zb),
+                           Q::fma2(sa, Q::template code16<1>(ka[i]), za),
+                           Q::fma2(sb, Q::template code16<1>(kb[i]), zb), qf[w][0], qf[w][1]);
+                    M::mma(s[j], Q::fma2(sa, Q::template code16<2>(ka[i]), za),
+                           Q::fma2(sb, Q::template code16<2>(kb[i]), zb),
+                           Q::fma2(sa, Q::template code16<3>(ka[i]), za),
+                           Q::fma2(sb, Q::template code16<3>(kb[i]), zb), qf[w][2], qf[w][3]);
+                }
             }
         }
-        if (!whole) {  // cells outside the attended range may hold anything
-            const int ta = tok0 + g, tb = ta + 8;
-            if (ta < seq_start || ta >= seq_L) s[0] = s[1] = -INFINITY;
-            if (tb < seq_start || tb >= seq_L) s[2] = s[3] = -INFINITY;
-            // (a scale of 0 or below must not turn the mask around)
-        }
+        // e: the scores in the log2 domain, above the running maximum.  `out`
+        // marks tokens g and g + 8 that are not attended.
         const float sc = p.scale_log2;
-        float d[4];
-        if (whole) {
-            d[0] = fmaf(s[0], sc, -m0), d[1] = fmaf(s[1], sc, -m1);
-            d[2] = fmaf(s[2], sc, -m0), d[3] = fmaf(s[3], sc, -m1);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                d[i] = s[i] == -INFINITY ? -INFINITY : fmaf(s[i], sc, i & 1 ? -m1 : -m0);
+        bool out_a = false, out_b = false;
+        if constexpr (MASK) {
+            static_assert(!MASK || N == 1, "masked pages go one at a time");
+            const int ta = tok0 + g, tb = ta + 8;
+            out_a = ta < seq_start || ta >= seq_L;
+            out_b = tb < seq_start || tb >= seq_L;
         }
-        const bool raise = fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])) > 8.f;
-        if (__any_sync(0xffffffffu, raise)) {
+        float e[N][4];
+        float top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                d[i] = (!whole && s[i] == -INFINITY) ? -INFINITY : s[i] * sc;
-            float x0 = fmaxf(d[0], d[2]), x1 = fmaxf(d[1], d[3]);
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                e[j][i] = fmaf(s[j][i], sc, i & 1 ? -m1 : -m0);
+                if (MASK && (i < 2 ? out_a : out_b)) e[j][i] = -INFINITY;
+                top = fmaxf(top, e[j][i]);
+            }
+        if (__any_sync(0xffffffffu, top > 8.f)) {
+            float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    e[j][i] = s[j][i] * sc;
+                    if (MASK && (i < 2 ? out_a : out_b)) e[j][i] = -INFINITY;
+                    if (i & 1)
+                        x1 = fmaxf(x1, e[j][i]);
+                    else
+                        x0 = fmaxf(x0, e[j][i]);
+                }
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1) {
                 x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, k));
@@ -384,61 +413,71 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
                     acc[w][u][2] *= f0;
                     acc[w][u][3] *= f1;
                 }
-            d[0] -= m0, d[1] -= m1, d[2] -= m0, d[3] -= m1;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e[j][i] -= i & 1 ? m1 : m0;
         }
         // Weights; P^T's fragments are S^T's, each 8 x 8 block transposed.
-        float e[4];
+        uint32_t b0[N], b1[N];
+        [[maybe_unused]] uint32_t r0[N], r1[N];  // the rest of a split P
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = ex2(d[i]);
-        l0 += e[0] + e[2];
-        l1 += e[1] + e[3];
-        const uint32_t ha = M::pack(e[0], e[1]), hb = M::pack(e[2], e[3]);
-        const uint32_t b0 = q4_movmatrix(ha), b1 = q4_movmatrix(hb);
-        uint32_t r0 = 0, r1 = 0;
-        if constexpr (M::kSplitP) {
-            const float2 fa = M::unpack(ha), fb = M::unpack(hb);
-            r0 = q4_movmatrix(M::pack(e[0] - fa.x, e[1] - fa.y));
-            r1 = q4_movmatrix(M::pack(e[2] - fb.x, e[3] - fb.y));
+        for (int j = 0; j < N; ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[j][i] = ex2(e[j][i]);
+            l0 += e[j][0] + e[j][2];
+            l1 += e[j][1] + e[j][3];
+            const uint32_t ha = M::pack(e[j][0], e[j][1]), hb = M::pack(e[j][2], e[j][3]);
+            b0[j] = q4_movmatrix(ha);
+            b1[j] = q4_movmatrix(hb);
+            M::mma(lacc, M::kOnes, M::kOnes, M::kOnes, M::kOnes, b0[j], b1[j]);
+            if constexpr (M::kSplitP) {
+                const float2 fa = M::unpack(ha), fb = M::unpack(hb);
+                r0[j] = q4_movmatrix(M::pack(e[j][0] - fa.x, e[j][1] - fa.y));
+                r1[j] = q4_movmatrix(M::pack(e[j][2] - fb.x, e[j][3] - fb.y));
+                M::mma(lacc, M::kOnes, M::kOnes, M::kOnes, M::kOnes, r0[j], r1[j]);
+            }
         }
-        M::mma(lacc, M::kOnes, M::kOnes, M::kOnes, M::kOnes, b0, b1);
-        if constexpr (M::kSplitP)
-            M::mma(lacc, M::kOnes, M::kOnes, M::kOnes, M::kOnes, r0, r1);
         // V: token pairs t and t + 4 (tokens 2t, 2t + 1, 2t + 8, 2t + 9).  A token
         // that is not attended gets scale and offset 0: 0 * NaN would be NaN.
         uint32_t keep_a = 0xffffffffu, keep_b = 0xffffffffu;
-        if (!whole) {
+        if constexpr (MASK) {
             auto in = [&](int k) { return k >= seq_start && k < seq_L; };
             const int k0 = tok0 + 2 * t;
             keep_a = (in(k0) ? 0xffffu : 0u) | (in(k0 + 1) ? 0xffff0000u : 0u);
             keep_b = (in(k0 + 8) ? 0xffffu : 0u) | (in(k0 + 9) ? 0xffff0000u : 0u);
         }
 #pragma unroll
-        for (int sl = 0; sl < W / V; ++sl) {
-            uint32_t va[V], vb[V], pa2[2], pb2[2];
-            const unsigned char* at = blk + L::kVCodes + sl * (128 * V) + lane * (4 * V);
-            q4_lds<V>(va, at);
-            q4_lds<V>(vb, at + 4 * D);
-            const int n = D == 96 ? sl : (D == 64 ? g >> 2 : (D == 128 ? g >> 1 : g));
-            const unsigned char* par = blk + L::kVParams + (t * L::kGroups + n) * 8;
-            q4_lds<2>(pa2, par);
-            q4_lds<2>(pb2, par + 4 * L::kGroups * 8);
-            const uint32_t sa = pa2[0] & keep_a, za = pa2[1] & keep_a;
-            const uint32_t sb = pb2[0] & keep_b, zb = pb2[1] & keep_b;
+        for (int j = 0; j < N; ++j) {
+            const unsigned char* blk = blk0 + j * PB;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int w = sl * V + i;
-                const uint32_t a00 = Q::fma2(sa, Q::template code16<0>(va[i]), za);
-                const uint32_t a01 = Q::fma2(sa, Q::template code16<1>(va[i]), za);
-                const uint32_t a02 = Q::fma2(sb, Q::template code16<0>(vb[i]), zb);
-                const uint32_t a03 = Q::fma2(sb, Q::template code16<1>(vb[i]), zb);
-                M::mma(acc[w][0], a00, a01, a02, a03, b0, b1);
-                if constexpr (M::kSplitP) M::mma(acc[w][0], a00, a01, a02, a03, r0, r1);
-                const uint32_t a10 = Q::fma2(sa, Q::template code16<2>(va[i]), za);
-                const uint32_t a11 = Q::fma2(sa, Q::template code16<3>(va[i]), za);
-                const uint32_t a12 = Q::fma2(sb, Q::template code16<2>(vb[i]), zb);
-                const uint32_t a13 = Q::fma2(sb, Q::template code16<3>(vb[i]), zb);
-                M::mma(acc[w][1], a10, a11, a12, a13, b0, b1);
-                if constexpr (M::kSplitP) M::mma(acc[w][1], a10, a11, a12, a13, r0, r1);
+            for (int sl = 0; sl < W / V; ++sl) {
+                uint32_t va[V], vb[V], pa2[2], pb2[2];
+                const unsigned char* at = blk + L::kVCodes + sl * (128 * V) + lane * (4 * V);
+                q4_lds<V>(va, at);
+                q4_lds<V>(vb, at + 4 * D);
+                const int n = D == 96 ? sl : (D == 64 ? g >> 2 : (D == 128 ? g >> 1 : g));
+                const unsigned char* par = blk + L::kVParams + (t * L::kGroups + n) * 8;
+                q4_lds<2>(pa2, par);
+                q4_lds<2>(pb2, par + 4 * L::kGroups * 8);
+                const uint32_t sa = pa2[0] & keep_a, za = pa2[1] & keep_a;
+                const uint32_t sb = pb2[0] & keep_b, zb = pb2[1] & keep_b;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int w = sl * V + i;
+                    const uint32_t a00 = Q::fma2(sa, Q::template code16<0>(va[i]), za);
+                    const uint32_t a01 = Q::fma2(sa, Q::template code16<1>(va[i]), za);
+                    const uint32_t a02 = Q::fma2(sb, Q::template code16<0>(vb[i]), zb);
+                    const uint32_t a03 = Q::fma2(sb, Q::template code16<1>(vb[i]), zb);
+                    M::mma(acc[w][0], a00, a01, a02, a03, b0[j], b1[j]);
+                    if constexpr (M::kSplitP) M::mma(acc[w][0], a00, a01, a02, a03, r0[j], r1[j]);
+                    const uint32_t a10 = Q::fma2(sa, Q::template code16<2>(va[i]), za);
+                    const uint32_t a11 = Q::fma2(sa, Q::template code16<3>(va[i]), za);
+                    const uint32_t a12 = Q::fma2(sb, Q::template code16<2>(vb[i]), zb);
+                    const uint32_t a13 = Q::fma2(sb, Q::template code16<3>(vb[i]), zb);
+                    M::mma(acc[w][1], a10, a11, a12, a13, b0[j], b1[j]);
+                    if constexpr (M::kSplitP) M::mma(acc[w][1], a10, a11, a12, a13, r0[j], r1[j]);
+                }
             }
         }
     };
@@ -467,12 +506,10 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         for (int rd = 0; rd < Cfg::kRounds; ++rd) {
             constexpr int RD = Cfg::kRoundDims;
             if (rd > 0) __syncthreads();
-            // A lane's dims of round rd: with two rounds those of columns
-            // 4 rd .. 4 rd + 3 (columns own runs of D / 8 dims).
-            if (Cfg::kRounds == 1 || g / 4 == rd) {
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const int dim = q4_v_dim<D>(g, w) - rd * RD;
+            for (int w = 0; w < W; ++w) {
+                const int dim = q4_v_dim<D>(g, w) - rd * RD;
+                if (Cfg::kRounds == 1 || (dim >= 0 && dim < RD)) {
                     float* x = xbuf + (warp * kMaxHeadsPerCta + 2 * t) * Cfg::kXStride + dim;
                     if (2 * t < G)
                         *reinterpret_cast<float4*>(x) =
@@ -583,13 +620,21 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         }
     };
 
-    // ---- The range, kQ4StagedPages at a time.  The warp's pages are those at
-    // warp, warp + 4, ... of a stretch, in ring slots taken round.
-    int issued = 0, taken = 0;  // copies of this warp, over the whole range
+    // ---- The range, kQ4StagedPages at a time.  Slots of kPair pages go to the
+    // warps in turn; a warp's copies take its ring slots round.
+    constexpr int NP = Cfg::kPair;
+    constexpr int SB = Cfg::kSlotBytes;
+    using One = std::integral_constant<int, 1>;
+    using Slot = std::integral_constant<int, NP>;
+    int in_slot = 0, out_slot = 0;    // ring slots of the next copy and of the next page
+    uint32_t out_phase = 0;
+    int pending = 0;                  // slots requested and not yet waited for
+    int stall = p.stall_tx;
     begin_sequence();
     for (int c0 = lo; c0 < hi; c0 += kQ4StagedPages) {
         const int c1 = min(hi, c0 + kQ4StagedPages);
         __syncthreads();  // the previous stretch's ids have been used
+        bool bad_id = false;
         for (int f = c0 + threadIdx.x; f < c1; f += kThreads) {
             int a = 0, z = p.B - 1;  // the sequence of page f
             while (a < z) {
@@ -607,54 +652,72 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
             int id = p.block_tables[(size_t)a * p.maxp + first_page + (f - s_base[a])];
             if (id < 0 || id >= p.num_pages) {
                 id = -1;
-                atomicOr(p.err, PA_DEVERR_BAD_PAGE);
+                bad_id = true;
             }
             s_pid[f - c0] = id;
         }
-        __syncthreads();
-        const int n = c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;  // this warp's pages
-        int next = 0;  // pages of the stretch requested so far
-        auto request = [&]() {  // (lane 0)
-            const int id = s_pid[warp + next * kWarps];
-            const uint32_t slot = issued % NS;
-            const uint32_t bar = bar_w + slot * 8;
-            if (id < 0) {
-                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-            } else {
-                mbar_arrive_expect_tx(bar, PB + (issued == 0 ? p.stall_tx : 0));
-                bulk_g2s(ring_u + slot * PB,
+        if (bad_id) atomicOr(p.err, PA_DEVERR_BAD_PAGE);
+        // With a bad id in the stretch its pages are looked at one by one.
+        const bool careful = __syncthreads_or(bad_id);
+
+        int ask = NP * warp;  // first page (from c0) of the next slot to request
+        auto request = [&]() {
+            int id = -1;
+            if (lane < NP && ask + lane < c1 - c0) id = s_pid[ask + lane];
+            const uint32_t n_ids = __popc(__ballot_sync(0xffffffffu, id >= 0));
+            const uint32_t bar = bar_w + in_slot * 8;
+            if (lane == 0) mbar_arrive_expect_tx(bar, n_ids * PB + stall);
+            __syncwarp();
+            if (id >= 0)
+                bulk_g2s(ring_u + in_slot * SB + lane * PB,
                          p.cache + ((size_t)id * p.Hkv + kvh) * (size_t)PB, PB, bar);
-            }
+            stall = 0;
+            ask += NP * kWarps;
+            in_slot = in_slot + 1 == NS ? 0 : in_slot + 1;
+            ++pending;
         };
-        while (next < min(n, NS) && !dead) {
-            if (lane == 0) request();
-            ++next;
-            ++issued;
-        }
-        int i = 0;  // pages of the stretch consumed
+        if (!dead)
+            for (int i = 0; i < NS && ask < c1 - c0; ++i) request();
+
+        int f = dead ? c1 : c0 + NP * warp;  // next page of this warp
         while (true) {
             const int seg_end = min(c1, s_base[b + 1]);
-            for (; i < n && c0 + warp + i * kWarps < seg_end; ++i) {
-                if (dead) continue;
-                const int slot = taken % NS;
-                if (!mbar_wait_bounded(bar_w + slot * 8, (taken / NS) & 1)) dead = true;
-                dead = __any_sync(0xffffffffu, dead);
-                if (dead) {
-                    if (lane == 0) atomicOr(p.err, PA_DEVERR_TIMEOUT);
-                    bad = true;
-                    continue;
+            // Pages that are attended whole lie in [whole0, whole1).
+            const int base = s_base[b] - seq_page0;  // page of token 0
+            const int whole0 = careful ? INT_MAX : base + (seq_start + kPageSize - 1) / kPageSize;
+            const int whole1 = min(seg_end, base + seq_L / kPageSize);
+            while (f < seg_end) {
+                const int sub = (f - c0) & (NP - 1);
+                if (sub == 0) {
+                    const bool ok = mbar_wait_bounded(bar_w + out_slot * 8, out_phase);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        if (lane == 0) atomicOr(p.err, PA_DEVERR_TIMEOUT);
+                        dead = bad = true;
+                        f = c1;
+                        break;
+                    }
+                    --pending;
                 }
-                ++taken;
-                const int f = c0 + warp + i * kWarps;
-                if (s_pid[f - c0] < 0)
-                    bad = true;
-                else
-                    page(ring_w + slot * PB, (seq_page0 + f - s_base[b]) * kPageSize);
-                __syncwarp();  // every lane has read the slot
-                if (next < n) {
-                    if (lane == 0) request();
-                    ++next;
-                    ++issued;
+                const unsigned char* blk = ring_w + out_slot * SB + sub * PB;
+                const int tok0 = (f - base) * kPageSize;
+                if (sub == 0 && f >= whole0 && f + NP <= whole1) {
+                    pages(blk, tok0, Slot{}, std::false_type{});
+                    f += NP;
+                } else {
+                    if (careful && s_pid[f - c0] < 0)
+                        bad = true;
+                    else
+                        pages(blk, tok0, One{}, std::true_type{});
+                    ++f;
+                }
+                if (((f - c0) & (NP - 1)) == 0 || f == c1) {  // the slot is used up
+                    f += NP * (kWarps - 1);
+                    __syncwarp();  // every lane has read it
+                    if (ask < c1 - c0) request();
+                    if (++out_slot == NS) {
+                        out_slot = 0;
+                        out_phase ^= 1;
+                    }
                 }
             }
             if (s_base[b + 1] > c1) break;  // goes on in the next stretch or CTA
@@ -667,8 +730,14 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         }
     }
     if (b < p.B && s_base[b] < hi && s_base[b + 1] > hi) end_sequence();
-    if (dead) {  // copies still on their way must not outlive the CTA's shared memory
-        for (; taken < issued; ++taken) mbar_wait_bounded(bar_w + (taken % NS) * 8, (taken / NS) & 1);
+    // After a timeout: copies still on their way must not outlive the CTA's
+    // shared memory.
+    for (; dead && pending > 0; --pending) {
+        mbar_wait_bounded(bar_w + out_slot * 8, out_phase);
+        if (++out_slot == NS) {
+            out_slot = 0;
+            out_phase ^= 1;
+        }
     }
 }
 

@@ -1,11 +1,14 @@
 // pa_q4_cache.cu -- rows of K and V into the 4-bit paged cache and back
 // (pa_q4_write, pa_q4_read of include/pa_q4.h).
 //
-// Both kernels are bound by memory: a row of D elements is read (2 D bytes)
-// and leaves as 0.625 D bytes of codes and parameters, or the reverse.  A
-// thread has 8 consecutive dims (16 bytes) of a row, so the four lanes of an
-// aligned quad hold a group of 32 dims, and D / 8 consecutive lanes a row.
-// blockIdx.y is K or V of a KV head; along x the rows follow each other.
+// A row of D elements (2 D bytes) is read and leaves as 0.625 D bytes of codes
+// and parameters, or the reverse.  A thread has 8 consecutive dims (16 bytes)
+// of a token and goes through its share of the KV heads, K and V, so that the
+// slot and the addresses are worked out once; the four lanes of an aligned
+// quad hold a group of 32 dims, and D / 8 consecutive lanes a row.  The next
+// head's rows are requested before the present ones are worked on.
+#include <algorithm>
+
 #include "pa_q4.cuh"
 
 namespace pa {
@@ -21,160 +24,238 @@ struct Q4CacheParams {
     long long v_stride;
     unsigned* err;
     int n, Hkv;
+    int heads;             // KV heads a thread serves (blockIdx.y: which)
     long long num_slots;   // num_pages * 16
 };
 
-// Quantise the 8 elements of a lane (the quad's 32 form the group).  The
-// codes, scale and offset are those of exact arithmetic: where an fp32
-// result lies close to a rounding border the step is repeated in fp64.
+// The fp64 steps, taken where an fp32 quotient lies close to a rounding border
+// of T or 1 / s overflows.  Out of line: inlined, their conversions ran for
+// every element and kept the fp64 pipe 78 % busy (16384 bf16 rows of 4 x 256:
+// 74 us).
 template <typename T>
-__device__ __forceinline__ void quantise8(const uint32_t (&x)[4], uint32_t (&code)[2], uint32_t& s16,
+__device__ __noinline__ uint32_t exact_scale(float mx, float mn) {
+    return Q4Type<T>::from_double(((double)mx - (double)mn) / 15.0);
+}
+
+__device__ __noinline__ float exact_code(float x, float z, float s) {
+    return (float)rint(((double)x - (double)z) / (double)s);
+}
+
+// Quantise the 8 elements of a lane (the quad's 32 form the group): codes of
+// dims 4 i .. 4 i + 3 in the low half of code[i], first dim lowest.
+//
+// With d = x - z the code is rint(d / s) - 16.  v = fma(d, 1 / s, 1.5 2^23)
+// rounds the quotient to an integer r in one step, wrong only where d / s lies
+// within 2^-16 of the middle between two integers; there the residual
+// d - r s, which is exact, decides.  Such middles are common, not rare: values
+// and scales of T are coarse, so about one bf16 element in 300 is an exact tie.
+template <typename T>
+__device__ __forceinline__ void quantise8(const uint4& raw, uint32_t (&code)[2], uint32_t& s16,
                                           uint32_t& z16) {
     using Q = Q4Type<T>;
+    constexpr float kMagic = 12582912.f;  // 1.5 2^23
+    const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
     // (max, -min) of the quad as one packed pair, NaN kept.
-    constexpr uint32_t kSign = 0x80008000u;
-    uint32_t hi = Q::max2_nan(Q::max2_nan(x[0], x[1]), Q::max2_nan(x[2], x[3]));
-    uint32_t lo = Q::max2_nan(Q::max2_nan(x[0] ^ kSign, x[1] ^ kSign),
-                              Q::max2_nan(x[2] ^ kSign, x[3] ^ kSign));
+    const uint32_t hi = Q::max2_nan(Q::max2_nan(x[0], x[1]), Q::max2_nan(x[2], x[3]));
+    const uint32_t lo =
+        Q::min2_nan(Q::min2_nan(x[0], x[1]), Q::min2_nan(x[2], x[3])) ^ 0x80008000u;
     uint32_t ext = Q::max2_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
     ext = Q::max2_nan(ext, __shfl_xor_sync(0xffffffffu, ext, 1));
     ext = Q::max2_nan(ext, __shfl_xor_sync(0xffffffffu, ext, 2));
     float mx = Q::to_float(ext & 0xffffu);
     float mn = -Q::to_float(ext >> 16);
-    if (mx != mx || mn != mn) {
-        s16 = 0;
-        z16 = 0x7FFFu;  // NaN in fp16 and bf16
-        code[0] = code[1] = 0;
-        return;
-    }
+    const bool nan = mx != mx || mn != mn;
     mx = fminf(fmaxf(mx, -Q::kLimit), Q::kLimit);
     mn = fminf(fmaxf(mn, -Q::kLimit), Q::kLimit);
     const float qs = __fdiv_rn(mx - mn, 15.f);
-    s16 = Q::near_tie(qs) ? Q::from_double(((double)mx - (double)mn) / 15.0) : Q::from_float(qs);
+    s16 = Q::from_float(qs);
+    if (Q::near_tie(qs)) s16 = exact_scale<T>(mx, mn);
     // z = RN_T(mn - 16 s): mn is a value of T, so this is one fma of T.
     z16 = Q::fma2(Q::from_float(-16.f), s16, Q::from_float(mn)) & 0xffffu;
     const float s = Q::to_float(s16), z = Q::to_float(z16);
-    code[0] = code[1] = 0;
-    if (s16 == 0) return;
-    const float inv = __frcp_rn(s);
-    // (1 / s overflows for the smallest bf16 scales: those go by fp64)
-    const bool tiny = s < 1e-37f;
+    const float inv = __frcp_rn(s);  // (s = 0: inf; the codes are dropped below)
+    float v[8];
+    float worst = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float xv = Q::to_float(i & 1 ? x[i / 2] >> 16 : x[i / 2] & 0xffffu);
-        // u = 16 + c before rounding; its error is below 2^-17 for u <= 32
-        // (the subtraction, 1 / s and the product: 3 * 2^-24 * 32).
-        const float u = (xv - z) * inv;
-        float r = rintf(u);
-        if (tiny || fabsf(fabsf(u - r) - 0.5f) < 1.52587890625e-05f)
-            r = (float)rint(((double)xv - (double)z) / (double)s);
-        const float c = fminf(fmaxf(r - 16.f, 0.f), 15.f);
-        code[i / 4] |= (uint32_t)(int)c << (4 * (i % 4));
+        const float d = Q::to_float(i & 1 ? x[i / 2] >> 16 : x[i / 2] & 0xffffu) - z;
+        v[i] = fmaf(d, inv, kMagic);
+        worst = fmaxf(worst, fabsf(fmaf(kMagic - v[i], s, d)));
+    }
+    const float half = 0.5f * s;
+    if ((worst > half * 0.99996f || s < 1e-37f) && s16 != 0) {
+        if (s < 1e-37f) {  // (only bf16 scales get here)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = kMagic +
+                       exact_code(Q::to_float(i & 1 ? x[i / 2] >> 16 : x[i / 2] & 0xffffu), z, s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float xv = Q::to_float(i & 1 ? x[i / 2] >> 16 : x[i / 2] & 0xffffu);
+                const float d = xv - z;
+                const float back = d - xv;  // what d lost: x - z = d + e
+                const float e = (xv - (d - back)) - (z + back);
+                const float res = fmaf(kMagic - v[i], s, d);
+                const float over = (fabsf(res) - half) + copysignf(1.f, res) * e;
+                if (over > 0.f || (over == 0.f && (__float_as_uint(v[i]) & 1u)))
+                    v[i] += copysignf(1.f, res);
+            }
+        }
+    }
+    // The bits of kMagic + 16 + c, each moved to its place and added up; what
+    // all eight constants add up to is taken off again.
+    constexpr uint32_t kOne = 0x4B400010u;
+    constexpr uint32_t kSum = kOne + (kOne << 4) + (kOne << 8) + (kOne << 12);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t sum = 0u - kSum;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float c = fminf(fmaxf(v[4 * k + i], kMagic + 16.f), kMagic + 31.f);
+            sum += __float_as_uint(c) << (4 * i);
+        }
+        code[k] = nan || s16 == 0 ? 0u : sum;
+    }
+    if (nan) {
+        s16 = 0;
+        z16 = 0x7FFFu;  // NaN in fp16 and bf16
     }
 }
+
+// Byte offsets of a thread's cells in a page block, and where its rows lie.
+template <int D>
+struct Q4Lane {
+    using L = Q4Layout<D>;
+    static constexpr int kLanes = D / 8;  // of a row
+    long long tok;
+    int c8;            // first dim
+    long long slot;    // -1: left out (or no token)
+    bool bad;
+    size_t block0;     // byte offset of KV head 0's block of the slot's page
+    int k_codes, v_codes0, v_codes1, k_par, v_par;
+
+    __device__ __forceinline__ explicit Q4Lane(const Q4CacheParams& p) {
+        const long long idx = (long long)blockIdx.x * kQ4Threads + threadIdx.x;
+        tok = idx / kLanes;
+        c8 = (int)(idx % kLanes) * 8;
+        slot = tok < p.n ? p.slots[tok] : -1;
+        bad = slot < -1 || slot >= p.num_slots;
+        if (bad) slot = -1;
+        if (bad && p.err && blockIdx.y == 0 && c8 == 0) atomicOr(p.err, PA_DEVERR_BAD_SLOT);
+        const int r = slot < 0 ? 0 : (int)(slot % kPageSize);
+        block0 = slot < 0 ? 0
+                          : (size_t)(slot / kPageSize) * p.Hkv * (size_t)L::kPageBytes;
+        k_codes = L::k_codes(r, c8);
+        v_codes0 = L::v_codes(r, c8);
+        v_codes1 = L::v_codes(r, c8 + 4);
+        k_par = L::k_params(r, c8 / kQ4Group);
+        v_par = L::v_params(r, c8 / kQ4Group);
+    }
+};
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kQ4Threads) q4_write_kernel(const Q4CacheParams p) {
     using L = Q4Layout<D>;
-    constexpr int LPR = D / 8;  // lanes per row
     allow_dependent_launch();
     wait_for_prerequisite_grid();
-    const int head = blockIdx.y >> 1;
-    const bool is_v = blockIdx.y & 1;
-    const long long idx = (long long)blockIdx.x * kQ4Threads + threadIdx.x;
-    const long long tok = idx / LPR;
-    const int c8 = (int)(idx % LPR) * 8;
-    long long slot = -1;
-    uint32_t x[4] = {0, 0, 0, 0};
-    if (tok < p.n) {
-        slot = p.slots[tok];
-        const unsigned char* row =
-            (is_v ? p.v + tok * p.v_stride : p.k + tok * p.k_stride) + ((size_t)head * D + c8) * 2;
-        const uint4 raw = *reinterpret_cast<const uint4*>(row);
-        x[0] = raw.x, x[1] = raw.y, x[2] = raw.z, x[3] = raw.w;
-    }
-    uint32_t code[2], s16, z16;
-    quantise8<T>(x, code, s16, z16);  // (every lane takes part in the quad's shuffles)
-    if (slot < 0 || slot >= p.num_slots) {
-        if (p.err && slot != -1 && blockIdx.y == 0 && c8 == 0) atomicOr(p.err, PA_DEVERR_BAD_SLOT);
-        return;
-    }
-    unsigned char* block =
-        p.cache + ((size_t)(slot / kPageSize) * p.Hkv + head) * (size_t)L::kPageBytes;
-    const int r = (int)(slot % kPageSize);
-    if (!is_v) {
-        *reinterpret_cast<uint32_t*>(block + L::k_codes(r, c8)) = code[0] | (code[1] << 16);
-        if ((c8 & (kQ4Group - 1)) == 0)
-            *reinterpret_cast<uint32_t*>(block + L::k_params(r, c8 / kQ4Group)) = s16 | (z16 << 16);
-    } else {
-        *reinterpret_cast<uint16_t*>(block + L::v_codes(r, c8)) = (uint16_t)code[0];
-        *reinterpret_cast<uint16_t*>(block + L::v_codes(r, c8 + 4)) = (uint16_t)code[1];
-        if ((c8 & (kQ4Group - 1)) == 0) {
-            unsigned char* cell = block + L::v_params(r, c8 / kQ4Group);
-            *reinterpret_cast<uint16_t*>(cell) = (uint16_t)s16;
-            *reinterpret_cast<uint16_t*>(cell + 4) = (uint16_t)z16;
+    const Q4Lane<D> ln(p);
+    const bool has = ln.tok < p.n, keep = ln.slot >= 0;
+    const int h0 = blockIdx.y * p.heads, h1 = min(p.Hkv, h0 + p.heads);
+    const bool first = (ln.c8 & (kQ4Group - 1)) == 0;  // the quad's lane that stores s and z
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    const unsigned char* kr = p.k + ln.tok * p.k_stride + ((size_t)h0 * D + ln.c8) * 2;
+    const unsigned char* vr = p.v + ln.tok * p.v_stride + ((size_t)h0 * D + ln.c8) * 2;
+    unsigned char* block = p.cache + ln.block0 + (size_t)h0 * L::kPageBytes;
+    uint4 k = has ? *reinterpret_cast<const uint4*>(kr) : none;
+    uint4 v = has ? *reinterpret_cast<const uint4*>(vr) : none;
+    for (int h = h0; h < h1; ++h) {
+        uint4 k_next = none, v_next = none;
+        if (has && h + 1 < h1) {
+            k_next = *reinterpret_cast<const uint4*>(kr += 2 * D);
+            v_next = *reinterpret_cast<const uint4*>(vr += 2 * D);
         }
+        uint32_t code[2], s16, z16;
+        quantise8<T>(k, code, s16, z16);  // (every lane takes part in the quad's shuffles)
+        if (keep) {
+            *reinterpret_cast<uint32_t*>(block + ln.k_codes) = code[0] | (code[1] << 16);
+            if (first) *reinterpret_cast<uint32_t*>(block + ln.k_par) = s16 | (z16 << 16);
+        }
+        quantise8<T>(v, code, s16, z16);
+        if (keep) {
+            *reinterpret_cast<uint16_t*>(block + ln.v_codes0) = (uint16_t)code[0];
+            *reinterpret_cast<uint16_t*>(block + ln.v_codes1) = (uint16_t)code[1];
+            if (first) {
+                *reinterpret_cast<uint16_t*>(block + ln.v_par) = (uint16_t)s16;
+                *reinterpret_cast<uint16_t*>(block + ln.v_par + 4) = (uint16_t)z16;
+            }
+        }
+        block += L::kPageBytes;
+        k = k_next;
+        v = v_next;
     }
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(const Q4CacheParams p) {
-    using L = Q4Layout<D>;
+// The 8 values of two words of codes (dims 4 i .. 4 i + 3 in word half i).
+template <typename T>
+__device__ __forceinline__ uint4 dequantise8(uint32_t codes, uint32_t s16, uint32_t z16) {
     using Q = Q4Type<T>;
-    constexpr int LPR = D / 8;
-    allow_dependent_launch();
-    wait_for_prerequisite_grid();
-    const int head = blockIdx.y >> 1;
-    const bool is_v = blockIdx.y & 1;
-    const long long idx = (long long)blockIdx.x * kQ4Threads + threadIdx.x;
-    const long long tok = idx / LPR;
-    const int c8 = (int)(idx % LPR) * 8;
-    if (tok >= p.n) return;
-    const long long slot = p.slots[tok];
-    uint32_t codes = 0, s16 = 0, z16 = 0;
-    if (slot >= 0 && slot < p.num_slots) {
-        const unsigned char* block =
-            p.cache + ((size_t)(slot / kPageSize) * p.Hkv + head) * (size_t)L::kPageBytes;
-        const int r = (int)(slot % kPageSize);
-        if (!is_v) {
-            codes = *reinterpret_cast<const uint32_t*>(block + L::k_codes(r, c8));
-            const uint32_t sz =
-                *reinterpret_cast<const uint32_t*>(block + L::k_params(r, c8 / kQ4Group));
-            s16 = sz & 0xffffu;
-            z16 = sz >> 16;
-        } else {
-            codes = *reinterpret_cast<const uint16_t*>(block + L::v_codes(r, c8)) |
-                    ((uint32_t) * reinterpret_cast<const uint16_t*>(block + L::v_codes(r, c8 + 4))
-                     << 16);
-            const unsigned char* cell = block + L::v_params(r, c8 / kQ4Group);
-            s16 = *reinterpret_cast<const uint16_t*>(cell);
-            z16 = *reinterpret_cast<const uint16_t*>(cell + 4);
-        }
-    } else if (slot != -1) {
-        z16 = 0x7FFFu;
-        if (p.err && blockIdx.y == 0 && c8 == 0) atomicOr(p.err, PA_DEVERR_BAD_SLOT);
-    }
     const uint32_t s2 = s16 * 0x10001u, z2 = z16 * 0x10001u;
     // The pair at bits 4 P of both halves is dims (P, P + 4).
     const uint32_t y0 = Q::fma2(s2, Q::template code16<0>(codes), z2);
     const uint32_t y1 = Q::fma2(s2, Q::template code16<1>(codes), z2);
     const uint32_t y2 = Q::fma2(s2, Q::template code16<2>(codes), z2);
     const uint32_t y3 = Q::fma2(s2, Q::template code16<3>(codes), z2);
-    uint4 o;
-    o.x = __byte_perm(y0, y1, 0x5410);
-    o.y = __byte_perm(y2, y3, 0x5410);
-    o.z = __byte_perm(y0, y1, 0x7632);
-    o.w = __byte_perm(y2, y3, 0x7632);
-    unsigned char* row =
-        (is_v ? p.v + tok * p.v_stride : p.k + tok * p.k_stride) + ((size_t)head * D + c8) * 2;
-    *reinterpret_cast<uint4*>(row) = o;
+    return make_uint4(__byte_perm(y0, y1, 0x5410), __byte_perm(y2, y3, 0x5410),
+                      __byte_perm(y0, y1, 0x7632), __byte_perm(y2, y3, 0x7632));
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(const Q4CacheParams p) {
+    using L = Q4Layout<D>;
+    allow_dependent_launch();
+    wait_for_prerequisite_grid();
+    const Q4Lane<D> ln(p);
+    if (ln.tok >= p.n) return;
+    const bool keep = ln.slot >= 0;
+    const int h0 = blockIdx.y * p.heads, h1 = min(p.Hkv, h0 + p.heads);
+    unsigned char* kr = p.k + ln.tok * p.k_stride + ((size_t)h0 * D + ln.c8) * 2;
+    unsigned char* vr = p.v + ln.tok * p.v_stride + ((size_t)h0 * D + ln.c8) * 2;
+    const unsigned char* block = p.cache + ln.block0 + (size_t)h0 * L::kPageBytes;
+    const uint32_t fill = ln.bad ? 0x7FFFu : 0u;  // the offset of a row that is not there
+    struct Cells {
+        uint32_t kc, kp, v0, v1, vs, vz;
+    };
+    auto fetch = [&](const unsigned char* b) {
+        Cells c = {0, fill << 16, 0, 0, 0, fill};
+        if (keep) {
+            c.kc = *reinterpret_cast<const uint32_t*>(b + ln.k_codes);
+            c.kp = *reinterpret_cast<const uint32_t*>(b + ln.k_par);
+            c.v0 = *reinterpret_cast<const uint16_t*>(b + ln.v_codes0);
+            c.v1 = *reinterpret_cast<const uint16_t*>(b + ln.v_codes1);
+            c.vs = *reinterpret_cast<const uint16_t*>(b + ln.v_par);
+            c.vz = *reinterpret_cast<const uint16_t*>(b + ln.v_par + 4);
+        }
+        return c;
+    };
+    Cells c = fetch(block);
+    for (int h = h0; h < h1; ++h) {
+        Cells next = c;
+        if (h + 1 < h1) next = fetch(block += L::kPageBytes);
+        *reinterpret_cast<uint4*>(kr) = dequantise8<T>(c.kc, c.kp & 0xffffu, c.kp >> 16);
+        *reinterpret_cast<uint4*>(vr) = dequantise8<T>(c.v0 | (c.v1 << 16), c.vs, c.vz);
+        kr += 2 * D;
+        vr += 2 * D;
+        c = next;
+    }
 }
 
 template <typename T>
 static cudaError_t launch_q4_cache(bool write, int D, const Q4CacheParams& p, cudaStream_t stream) {
     const long long lanes = (long long)p.n * (D / 8);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((lanes + kQ4Threads - 1) / kQ4Threads), 2 * p.Hkv);
+    cfg.gridDim = dim3((unsigned)((lanes + kQ4Threads - 1) / kQ4Threads),
+                       (p.Hkv + p.heads - 1) / p.heads);
     cfg.blockDim = dim3(kQ4Threads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -229,6 +310,10 @@ static int q4_cache_call(bool write, int num_tokens, int num_kv_heads, int head_
     p.n = num_tokens;
     p.Hkv = num_kv_heads;
     p.num_slots = (long long)num_pages * kPageSize;
+    // All heads of a token in one thread where the tokens alone make a few
+    // waves of CTAs, else as many threads as there are heads.
+    const long long ctas = ((long long)num_tokens * (head_dim / 8) + kQ4Threads - 1) / kQ4Threads;
+    p.heads = (int)std::max(1ll, std::min<long long>(num_kv_heads, ctas / 512));
     const cudaError_t e =
         dtype == PA_DTYPE_BF16
             ? launch_q4_cache<__nv_bfloat16>(write, head_dim, p, static_cast<cudaStream_t>(stream))

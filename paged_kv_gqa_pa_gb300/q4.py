@@ -12,7 +12,6 @@ with.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -25,7 +24,6 @@ PA_DEVERR_NO_PAGES = 16
 PAGE_SIZE = 16
 _DTYPE = {torch.float16: PA_DTYPE_F16, torch.bfloat16: PA_DTYPE_BF16, torch.float32: PA_DTYPE_F32}
 _TORCH = {v: k for k, v in _DTYPE.items()}
-_NO_GUARD = contextlib.nullcontext()
 
 
 class pa_q4_plan_t(ctypes.Structure):
@@ -84,17 +82,22 @@ def _lib():
 
 
 def _check(t, name, dtype, shape, dev):
-    """A contiguous CUDA tensor of this dtype, shape and device."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    """Address of a contiguous CUDA tensor of this dtype, shape and device.
+
+    (A small step's host time is these checks and the launch, about 0.35 us a
+    tensor: the usual case takes one expression, the message is found after.)"""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev and
+                t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    _check_device(t, name, dev)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    _check_device(t, name, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _check_device(t, name, dev):
@@ -104,22 +107,23 @@ def _check_device(t, name, dev):
         raise ValueError(f"{name} is on device {t.get_device()}, expected {dev}")
 
 
-def _rows(t, name, dtype, n, heads, dim, dev):
-    """(pointer, token stride) of rows [n, heads, dim] whose heads lie side by side
-    (columns of wider rows are accepted)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+def _rows(t, name, dtype, shape, dev):
+    """(address, token stride) of rows of shape (tokens, heads, dim) whose heads lie side by
+    side (columns of wider rows are accepted)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            n, heads, dim = shape
+            st, sh, sd = t.stride()
+            if sd == 1 and (sh == dim or heads == 1) or t.is_contiguous():
+                return t.data_ptr(), (st if n > 1 else heads * dim)
+            raise ValueError(f"{name}: the heads of a token must lie side by side "
+                             f"(stride {t.stride()})")
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must have shape {(n, heads, dim)}, got {tuple(t.shape)}")
     _check_device(t, name, dev)
-    st, sh, sd = t.stride()
-    if n == 0:
-        return t.data_ptr(), heads * dim
-    if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
-        raise ValueError(f"{name}: the heads of a token must lie side by side (stride {t.stride()})")
-    return t.data_ptr(), (st if n > 1 else heads * dim)
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _device_of(t, name):
@@ -130,9 +134,15 @@ def _device_of(t, name):
     return t.get_device()
 
 
+# The current stream's handle without a Stream object around it (1 us less).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, dev):
     """cudaStream_t as an int: the device's current stream by default."""
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(dev)
         return torch.cuda.current_stream(dev).cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         if stream.device_index != dev:
@@ -141,9 +151,15 @@ def _stream(stream, dev):
     return int(stream)
 
 
-def _guard(dev):
-    """The tensors' device as the current one while the library launches."""
-    return _NO_GUARD if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+def _call(fn, dev, args):
+    """fn(*args) with the tensors' device as the current one while it launches."""
+    if torch.cuda.current_device() == dev:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status != PA_OK:
+        raise PAError(fn.__name__, status)
 
 
 def _error_ptr(t, dev):
@@ -154,11 +170,6 @@ def _error_ptr(t, dev):
     if t.numel() * t.element_size() < 4 or not t.is_contiguous():
         raise ValueError("device_error must hold 4 contiguous bytes")
     return t.data_ptr()
-
-
-def _done(fn, status):
-    if status != PA_OK:
-        raise PAError(fn, status)
 
 
 def pa_q4_page_bytes(head_dim: int) -> int:
@@ -189,40 +200,35 @@ def _cache_dims(cache, dev, head_dim):
     return cache.shape[0], cache.shape[1]
 
 
-def _cache_call(fn, k, v, slots, cache, device_error, stream):
+def _cache_args(k, v, slots, cache):
     dev = _device_of(k, "k")
     if k.dim() != 3:
         raise ValueError(f"k must have shape (tokens, Hkv, D), got {tuple(k.shape)}")
-    n, heads, dim = k.shape
+    n, _, dim = k.shape
     et = k.dtype
     if et not in _DTYPE:
         raise TypeError(f"k must be fp16 or bf16, got {et}")
     pages, hkv = _cache_dims(cache, dev, dim)
-    kp, ks = _rows(k, "k", et, n, hkv, dim, dev)
-    vp, vs = _rows(v, "v", et, n, hkv, dim, dev)
-    return (dev, n, hkv, dim, PAGE_SIZE, pages, _DTYPE[et], kp, ks, vp, vs,
-            _check(slots, "slots", torch.int64, (n,), dev), cache.data_ptr(),
-            _error_ptr(device_error, dev), _stream(stream, dev))
+    shape = (n, hkv, dim)
+    return (dev, (n, hkv, dim, PAGE_SIZE, pages, _DTYPE[et]), _rows(k, "k", et, shape, dev),
+            _rows(v, "v", et, shape, dev), _check(slots, "slots", torch.int64, (n,), dev),
+            cache.data_ptr())
 
 
 def pa_q4_write(k, v, slots, cache, device_error=None, stream=None) -> None:
     """Quantise rows k, v [tokens, Hkv, D] (fp16 or bf16, columns of wider rows allowed)
     into the cache at `slots` (int64 [tokens], distinct; -1: left out)."""
-    dev, n, hkv, dim, ps, pages, et, kp, ks, vp, vs, sl, cp, err, st = _cache_call(
-        "pa_q4_write", k, v, slots, cache, device_error, stream)
-    with _guard(dev):
-        _done("pa_q4_write", _lib().pa_q4_write(n, hkv, dim, ps, pages, et, kp, ks, vp, vs, sl,
-                                                cp, err, st))
+    dev, sizes, kr, vr, sl, cp = _cache_args(k, v, slots, cache)
+    _call(_lib().pa_q4_write, dev, (*sizes, *kr, *vr, sl, cp, _error_ptr(device_error, dev),
+                                    _stream(stream, dev)))
 
 
 def pa_q4_read(cache, slots, k_out, v_out, device_error=None, stream=None) -> None:
     """Rows the cache stands for at `slots`, into k_out, v_out [tokens, Hkv, D]
     (slot -1: zeros)."""
-    dev, n, hkv, dim, ps, pages, et, kp, ks, vp, vs, sl, cp, err, st = _cache_call(
-        "pa_q4_read", k_out, v_out, slots, cache, device_error, stream)
-    with _guard(dev):
-        _done("pa_q4_read", _lib().pa_q4_read(n, hkv, dim, ps, pages, et, cp, sl, kp, ks, vp, vs,
-                                              err, st))
+    dev, sizes, kr, vr, sl, cp = _cache_args(k_out, v_out, slots, cache)
+    _call(_lib().pa_q4_read, dev, (*sizes, cp, sl, *kr, *vr, _error_ptr(device_error, dev),
+                                   _stream(stream, dev)))
 
 
 def pa_q4_plan(batch, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
@@ -230,10 +236,12 @@ def pa_q4_plan(batch, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
                dtype=PA_DTYPE_F16) -> pa_q4_plan_t:
     """Plan decode calls over a 4-bit cache (num_sms 0: ask the current device)."""
     plan = pa_q4_plan_t()
-    _done("pa_q4_plan", _lib().pa_q4_plan(
+    st = _lib().pa_q4_plan(
         int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size),
         int(num_pages), int(max_pages_per_seq), int(max_context_len), int(window), int(num_sms),
-        int(dtype), ctypes.byref(plan)))
+        int(dtype), ctypes.byref(plan))
+    if st != PA_OK:
+        raise PAError("pa_q4_plan", st)
     return plan
 
 
@@ -265,8 +273,7 @@ def pa_q4_decode(plan, q, cache, block_tables, context_lens, scale, window, out,
     """One decode step over a 4-bit cache; arguments as pa_decode's."""
     dev, args = _q4_decode_args(plan, q, cache, block_tables, context_lens, scale, window, out,
                                 lse, workspace, stream)
-    with _guard(dev):
-        _done("pa_q4_decode", _lib().pa_q4_decode(*args))
+    _call(_lib().pa_q4_decode, dev, args)
 
 
 class PreparedQ4Decode:
@@ -283,8 +290,7 @@ class PreparedQ4Decode:
         self._fn = _lib().pa_q4_decode
 
     def __call__(self) -> None:
-        with _guard(self._dev):
-            _done("pa_q4_decode", self._fn(*self._args))
+        _call(self._fn, self._dev, self._args)
 
 
 def prepare_q4_decode(plan, q, cache, block_tables, context_lens, scale, window, out, lse,
@@ -343,8 +349,7 @@ def pa_extend_tables(past_lens, new_lens, free_pages, num_pages, block_tables, c
             _check(positions, "positions", i32, (cap,), dev),
             _check(pages_taken, "pages_taken", i32, (1,), dev),
             _error_ptr(device_error, dev), _stream(stream, dev))
-    with _guard(dev):
-        _done("pa_extend_tables", _lib().pa_extend_tables(*args))
+    _call(_lib().pa_extend_tables, dev, args)
 
 
 def pa_rope_axes(q, k, positions, sections, theta, q_out=None, k_out=None, rotary_dim=None,
@@ -370,16 +375,16 @@ def pa_rope_axes(q, k, positions, sections, theta, q_out=None, k_out=None, rotar
         if q.dim() != 3:
             raise ValueError(f"q must have shape (tokens, heads, D), got {tuple(q.shape)}")
         hq = q.shape[1]
-        qp, qs = _rows(q, "q", et, n, hq, D, dev)
-        qop, qos = (qp, qs) if q_out is None else _rows(q_out, "q_out", et, n, hq, D, dev)
+        qp, qs = _rows(q, "q", et, (n, hq, D), dev)
+        qop, qos = (qp, qs) if q_out is None else _rows(q_out, "q_out", et, (n, hq, D), dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k is not None:
         if k.dim() != 3:
             raise ValueError(f"k must have shape (tokens, heads, D), got {tuple(k.shape)}")
         hk = k.shape[1]
-        kp, ks = _rows(k, "k", et, n, hk, D, dev)
-        kop, kos = (kp, ks) if k_out is None else _rows(k_out, "k_out", et, n, hk, D, dev)
+        kp, ks = _rows(k, "k", et, (n, hk, D), dev)
+        kop, kos = (kp, ks) if k_out is None else _rows(k_out, "k_out", et, (n, hk, D), dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
     args = (n, hq, hk, D, D if rotary_dim is None else int(rotary_dim), axes,
@@ -387,5 +392,4 @@ def pa_rope_axes(q, k, positions, sections, theta, q_out=None, k_out=None, rotar
             float(theta), _DTYPE[et], qp or None, qs, kp or None, ks,
             _check(positions, "positions", torch.int32, (axes, n), dev), qop or None, qos,
             kop or None, kos, _stream(stream, dev))
-    with _guard(dev):
-        _done("pa_rope_axes", _lib().pa_rope_axes(*args))
+    _call(_lib().pa_rope_axes, dev, args)
