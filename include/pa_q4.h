@@ -115,8 +115,8 @@ typedef struct pa_q4_plan {
     int ctas;               /* CTAs in all */
     size_t workspace_bytes; /* device workspace of pa_q4_decode */
     int ctrl_bytes;         /* its leading bytes that must be zero before the first call
-                               (error word, arrival counters); every call leaves the
-                               counters zero */
+                               (error word, counters); every call leaves the counters
+                               zero */
     int test_stall_bytes;   /* test hook, 0 in normal use (at most 4096): each warp's
                                first copy expects this many bytes more than it carries,
                                so the bounded wait on it runs out after 1 s

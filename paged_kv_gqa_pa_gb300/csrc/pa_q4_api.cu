@@ -22,35 +22,39 @@ PA_Q4_EXTERN(256)
 #undef PA_Q4_EXTERN
 
 constexpr int kQ4MaxBatch = 4096;
+constexpr int kQ4MinRun = 2;    // pages of a warp, at least
+constexpr int kQ4KernelRows = 8;  // partials per sequence beyond which a kernel merges
 
-// Workspace: [control block | arrival counters, groups x B | (max, sum) of the
-// partials | their outputs], each 256-byte aligned; two partials per CTA.
+// Workspace: [control block | counters of the partials left, groups x B | run
+// size and page sums for the merge kernel | (max, sum) of the partials | their
+// outputs], each 256-byte aligned; two partials per CTA.
 struct Q4WsLayout {
-    size_t ctr_off, ctrl_bytes, ml_off, o_off, total;
+    size_t ctr_off, ctrl_bytes, info_off, ml_off, o_off, total;
 };
 
 static size_t q4_align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-static Q4WsLayout q4_ws_layout(int B, int G, int D, long long groups, int X) {
+static Q4WsLayout q4_ws_layout(int B, int D, long long groups, int X) {
     Q4WsLayout w;
-    const size_t rows = (size_t)groups * X * 2 * G;
+    const size_t rows = (size_t)groups * X * 2;
     w.ctr_off = kCtrlBytes;
     w.ctrl_bytes = kCtrlBytes + q4_align256((size_t)groups * B * 4);
-    w.ml_off = w.ctrl_bytes;
-    w.o_off = w.ml_off + q4_align256(rows * 8);
-    w.total = w.o_off + q4_align256(rows * D * 4);
+    w.info_off = w.ctrl_bytes;
+    w.ml_off = w.info_off + q4_align256(((size_t)B + 3) * 4);
+    w.o_off = w.ml_off + q4_align256(rows * kMaxHeadsPerCta * 8);
+    w.total = w.o_off + q4_align256(rows * kMaxHeadsPerCta * D * 4);
     return w;
 }
 
 static int q4_ctas_per_sm(int D, int B) {
-    int smem = 0;
+    int smem = 0, most = 0;  // shared memory of a CTA, CTAs that the registers allow
     switch (D) {
-        case 64: smem = Q4Cfg<64>::smem(B); break;
-        case 96: smem = Q4Cfg<96>::smem(B); break;
-        case 128: smem = Q4Cfg<128>::smem(B); break;
-        default: smem = Q4Cfg<256>::smem(B); break;
+        case 64: smem = Q4Cfg<64>::smem(B), most = Q4Cfg<64>::kMinBlocks; break;
+        case 96: smem = Q4Cfg<96>::smem(B), most = Q4Cfg<96>::kMinBlocks; break;
+        case 128: smem = Q4Cfg<128>::smem(B), most = Q4Cfg<128>::kMinBlocks; break;
+        default: smem = Q4Cfg<256>::smem(B), most = Q4Cfg<256>::kMinBlocks; break;
     }
-    return std::max(1, std::min(3, 228 * 1024 / (smem + 1024 + 32)));
+    return std::max(1, std::min(most, 228 * 1024 / (smem + 1024 + 128)));
 }
 
 // What a plan's shapes must satisfy; the automatic fields are checked by the caller.
@@ -113,17 +117,18 @@ int pa_q4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
         }
     }
     p.heads_per_cta = g / nchunk;
-    // One wave of resident CTAs over all groups, but no more than the ranges
-    // of kQ4MinPages pages that the longest batch has.
+    // One wave of resident CTAs over all groups, filled to a little under its
+    // slots (a grid that needs every slot had CTAs starting in a second wave),
+    // but no more than give every warp kQ4MinRun pages of the longest batch.
     int span = (max_context_len + kPageSize - 1) / kPageSize;
     if (window > 0) span = std::min(span, (window - 1 + kPageSize - 1) / kPageSize + 1);
     const long long pages = std::max(1ll, (long long)std::max(1, batch) * span);
     const long long slots = (long long)p.num_sms * q4_ctas_per_sm(head_dim, batch);
-    long long x = std::max(1ll, slots / groups);
-    x = std::min(x, (pages + kQ4MinPages - 1) / kQ4MinPages);
+    long long x = std::max(1ll, (slots - slots / 64) / groups);
+    x = std::min(x, (pages + kWarps * kQ4MinRun - 1) / (kWarps * kQ4MinRun));
     p.ctas_per_group = (int)x;
     p.ctas = (int)std::min<long long>(x * groups, INT_MAX);
-    const Q4WsLayout wl = q4_ws_layout(batch, p.heads_per_cta, head_dim, groups, p.ctas_per_group);
+    const Q4WsLayout wl = q4_ws_layout(batch, head_dim, groups, p.ctas_per_group);
     if (wl.ctrl_bytes > (size_t)INT_MAX) return PA_ERR_UNSUPPORTED;
     p.workspace_bytes = wl.total;
     p.ctrl_bytes = (int)wl.ctrl_bytes;
@@ -144,9 +149,9 @@ int pa_q4_decode(const pa_q4_plan_t* plan, const void* q, const void* cache,
         return PA_ERR_INVALID_ARG;
     const long long groups = (long long)plan->num_kv_heads * (g / G);
     if (groups > 65535) return PA_ERR_UNSUPPORTED;
-    const Q4WsLayout wl = q4_ws_layout(plan->batch, G, D, groups, X);
+    const Q4WsLayout wl = q4_ws_layout(plan->batch, D, groups, X);
     if (plan->workspace_bytes < wl.total || plan->ctrl_bytes < 0 ||
-        (size_t)plan->ctrl_bytes < wl.ctrl_bytes)
+        plan->ctrl_bytes < 0 || (size_t)plan->ctrl_bytes < wl.ctrl_bytes)
         return PA_ERR_INVALID_ARG;
     if (!workspace) return PA_ERR_WORKSPACE;
     if ((uintptr_t)workspace & 15u) return PA_ERR_INVALID_ARG;
@@ -164,8 +169,12 @@ int pa_q4_decode(const pa_q4_plan_t* plan, const void* q, const void* cache,
     p.lse = lse;
     p.ws_o = reinterpret_cast<float*>(ws + wl.o_off);
     p.ws_ml = reinterpret_cast<float*>(ws + wl.ml_off);
-    p.counters = reinterpret_cast<unsigned*>(ws + wl.ctr_off);
     p.err = reinterpret_cast<unsigned*>(ws);
+    p.ws_info = reinterpret_cast<int*>(ws + wl.info_off);
+    // A sequence of a batch of B leaves about X / B partials: beyond
+    // kQ4KernelRows a kernel of its own gathers them.
+    p.merge_kernel = X > kQ4KernelRows * plan->batch ? 1 : 0;
+    p.counters = reinterpret_cast<unsigned*>(ws + wl.ctr_off);
     p.B = plan->batch;
     p.Hq = plan->num_q_heads;
     p.Hkv = plan->num_kv_heads;
