@@ -73,19 +73,16 @@ struct Q4Cfg {
     // Pages of a ring slot: two where a page is little work (what a page costs
     // beside its elements -- the wait, the vote, the request -- is then paid
     // once for two, and two chains of mma overlap), one at D 256.
-#ifndef Q4P
-#define Q4P (D == 256 ? 1 : 2)
-#define Q4NS (D == 64 ? 4 : (D == 96 ? 3 : 2))
-#define Q4MB 3
-#define Q4QS (D == 256)
-#endif
-    static constexpr int kPair = Q4P;
+    static constexpr int kPair = D == 256 ? 1 : 2;
     static constexpr int kSlotBytes = kPair * Q4Layout<D>::kPageBytes;
-    static constexpr int kStages = Q4NS;
+    // Two slots are enough: a warp's next one streams in while it works on the
+    // other (three at D 128 or 256 measured no faster, 3-10 % slower on the
+    // largest batches).
+    static constexpr int kStages = D == 64 ? 4 : 2;
     static constexpr int kRingBytes = kWarps * kStages * kSlotBytes;
     // q's fragments: in registers, or in shared memory where the accumulators
     // leave no room for them.
-    static constexpr bool kQShared = Q4QS;
+    static constexpr bool kQShared = D == 256;
     static constexpr int kQBytes = kQShared ? D * 16 : 0;
     // Units of O: a word of dims of one head of a lane, 16 bytes a lane.  At a
     // sequence's end every warp owns a quarter of them and gets the other
@@ -94,10 +91,12 @@ struct Q4Cfg {
     static constexpr int kXBytes = kUnits * (kWarps - 1) * 512;
     static constexpr int kSmemBytes = kRingBytes + kQBytes + kXBytes + kQ4StagedPages * 4 +
                                       kWarps * kMaxHeadsPerCta * 3 * 4 + kWarps * kStages * 8;
-    static constexpr int kMinBlocks = Q4MB;
+    // CTAs per SM by registers: 64 sequences of 4096 tokens at D 64 take 46.9 us
+    // with 4 and 49.9 with 3; at D 128 four did not pay (40.1 and 40.4 us).
+    static constexpr int kMinBlocks = D <= 96 ? 4 : 3;
     static_assert(kMinBlocks * (kSmemBytes + 1024 + 128) <= 228 * 1024, "CTAs per SM");
-    // (the sums over the batch, B + 1 words, follow)
-    static int smem(int B) { return kSmemBytes + (B + 1) * 4; }
+    // (two words per sequence follow: s_base, s_page0)
+    static int smem(int B) { return kSmemBytes + (2 * B + 1) * 4; }
 };
 
 // mma.sync m16n8k16, 16-bit in, fp32 accumulate; and fp32 pairs to 16 bits.
@@ -116,6 +115,16 @@ struct Q4Mma<__half> {
             " {%8, %9}, {%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    }
+    // The same from zero accumulators.
+    __device__ static __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1,
+                                                uint32_t a2, uint32_t a3, uint32_t b0,
+                                                uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+            " {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
     }
     __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
         const __half2 h = __floats2half2_rn(lo, hi);
@@ -140,6 +149,16 @@ struct Q4Mma<__nv_bfloat16> {
             " {%8, %9}, {%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    }
+    // The same from zero accumulators.
+    __device__ static __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1,
+                                                uint32_t a2, uint32_t a3, uint32_t b0,
+                                                uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+            " {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
     }
     __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -361,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     int* s_pid = reinterpret_cast<int*>(s_q + Cfg::kQBytes / 16);
     float* s_ml = reinterpret_cast<float*>(s_pid + kQ4StagedPages);  // [warp][8][m, sum, weights]
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_ml + kWarps * kMaxHeadsPerCta * 3);
-    int* s_base = reinterpret_cast<int*>(bars + kWarps * NS);  // pages in front of sequence b
+    int* s_base = reinterpret_cast<int*>(bars + kWarps * NS);
+    int* s_page0 = s_base + p.B + 1;
     __shared__ int s_red[kWarps];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -379,18 +399,22 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         for (int s = 0; s < NS; ++s) mbar_init(bar_w + s * 8, 1);
         fence_mbar_init();
     }
-    wait_for_prerequisite_grid();
 
     // ---- The batch's pages end to end: s_base[b] of them lie before sequence
-    // b (s_base[B] in all).  A thread sums a run of sequences, a scan over the
-    // CTA joins the runs.
-    const int per_thread = (p.B + kThreads - 1) / kThreads;
-    {
-        const int b0 = min(p.B, (int)threadIdx.x * per_thread), b1 = min(p.B, b0 + per_thread);
+    // b (s_base[B] in all); page f of them is logical page f + s_page0[b] of
+    // its sequence.  A thread sums a run of sequences, a scan over the CTA
+    // joins the runs.
+    const int tid = threadIdx.x;
+    auto scan = [&](bool one, int len) {  // one: B <= kThreads, and len is sequence tid's length
+        const int per = one ? 1 : (p.B + kThreads - 1) / kThreads;
+        const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
         int sum = 0;
         for (int b = b0; b < b1; ++b) {
-            const int n = balanced_seq_pages(p.context_lens[b], p.window, p.max_ctx, p.maxp);
+            const SeqSpan sp =
+                seq_span(one ? len : p.context_lens[b], p.window, p.max_ctx, p.maxp, 1);
+            const int n = sp.valid ? sp.end_page - sp.first_page : 0;
             s_base[b] = n;
+            s_page0[b] = sp.first_page;
             sum += n;
         }
         int inc = sum;
@@ -406,35 +430,12 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         for (int b = b0; b < b1; ++b) {
             const int n = s_base[b];
             s_base[b] = at;
+            s_page0[b] -= at;
             at += n;
         }
-        if (threadIdx.x == kThreads - 1) s_base[p.B] = inc;
+        if (tid == kThreads - 1) s_base[p.B] = inc;
         __syncthreads();
-    }
-    const int total = s_base[p.B];
-    const int range = max(NP * kWarps, (total + p.X - 1) / p.X);  // pages of a CTA
-    if (p.merge_kernel && blockIdx.x == 0 && blockIdx.y == 0) {
-        if (threadIdx.x == 0) p.ws_info[0] = range;
-        for (int i = threadIdx.x; i <= p.B; i += kThreads) p.ws_info[1 + i] = s_base[i];
-    }
-
-    // ---- Sequences that attend nothing: out 0 and lse -inf, or NaN where the
-    // length is out of bounds.
-    T* const out = reinterpret_cast<T*>(p.out);
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        if (s_base[b + 1] != s_base[b]) continue;
-        const bool valid = seq_span(p.context_lens[b], p.window, p.max_ctx, p.maxp, 1).valid;
-        if (!valid && threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_BAD_LENGTH);
-        const uint32_t fill = valid ? 0u : 0x7FFF7FFFu;
-        uint32_t* row = reinterpret_cast<uint32_t*>(out + ((size_t)b * p.Hq + h0) * D);
-        for (int i = threadIdx.x; i < G * D / 2; i += kThreads) row[i] = fill;
-        if (threadIdx.x < G)
-            p.lse[(size_t)b * p.Hq + h0 + threadIdx.x] = valid ? -INFINITY : NAN;
-    }
-    const long long from = (long long)blockIdx.x * range;
-    if (from >= total) return;
-    const int lo = (int)from, hi = (int)min((long long)total, from + range);
-
+    };
     // Sequence of page f: the last b with s_base[b] <= f (behind any empty ones
     // that share that number).
     auto sequence_of = [&](int f) {
@@ -448,7 +449,77 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         }
         return a;
     };
-    int b = sequence_of(lo);
+    // This CTA's range [lo, hi) of the pages and its first sequence b.
+    int range, lo, hi, b;
+    auto locate = [&]() {
+        const int total = s_base[p.B];
+        range = max(NP * kWarps, (total + p.X - 1) / p.X);
+        const long long from = (long long)blockIdx.x * range;
+        lo = (int)min((long long)total, from);
+        hi = (int)min((long long)total, from + range);
+        b = lo < hi ? sequence_of(lo) : 0;
+    };
+    auto table_entry = [&](int f) {
+        const int a = f < s_base[b + 1] ? b : sequence_of(f);
+        return p.block_tables + (size_t)a * p.maxp + (f + s_page0[a]);
+    };
+
+    // Up to kThreads sequences: all this is worked out before the wait for the
+    // previous grid, from lengths that may still change, and the first pages
+    // are requested into L2 (addresses checked as ever; a stale one only
+    // fetches a page that is not used).  After the wait the lengths and the
+    // first ids are read again, in one round trip, and the work stands if no
+    // length has changed.  Steps one behind the other: 32 sequences of 4096
+    // tokens 41.2 -> 39.5 us, one of 128K 38.8 -> 37.5.
+    const bool early = p.B <= kThreads;
+    int len = 0;
+    if (early) {
+        if (tid < p.B) len = __ldcg(p.context_lens + tid);
+        scan(true, len);
+        locate();
+        const int f = lo + (lane / NP) * (NP * kWarps) + NP * warp + lane % NP;
+        if (lane < NS * NP && f < hi) {
+            const int id = __ldcg(table_entry(f));
+            if (id >= 0 && id < p.num_pages)
+                prefetch_l2(p.cache + ((size_t)id * p.Hkv + kvh) * (size_t)PB, PB);
+        }
+    }
+    wait_for_prerequisite_grid();
+    constexpr int kIds = kQ4StagedPages / kThreads;  // ids of a stretch per thread
+    int ids[kIds];
+    bool again = true;
+    if (early) {
+        const int now = tid < p.B ? __ldcg(p.context_lens + tid) : 0;
+#pragma unroll
+        for (int i = 0; i < kIds; ++i) {
+            const int f = lo + tid + i * kThreads;
+            ids[i] = f < hi ? *table_entry(f) : 0;
+        }
+        again = __syncthreads_or(now != len);
+    }
+    if (again) {
+        len = early && tid < p.B ? p.context_lens[tid] : 0;
+        scan(early, len);
+        locate();
+    }
+    if (p.merge_kernel && blockIdx.x == 0 && blockIdx.y == 0) {
+        if (tid == 0) p.ws_info[0] = range;
+        for (int i = tid; i <= p.B; i += kThreads) p.ws_info[1 + i] = s_base[i];
+    }
+
+    // ---- Sequences that attend nothing: out 0 and lse -inf, or NaN where the
+    // length is out of bounds.
+    T* const out = reinterpret_cast<T*>(p.out);
+    for (int e = blockIdx.x; e < p.B; e += gridDim.x) {
+        if (s_base[e + 1] != s_base[e]) continue;
+        const bool valid = seq_span(p.context_lens[e], p.window, p.max_ctx, p.maxp, 1).valid;
+        if (!valid && tid == 0) atomicOr(p.err, PA_DEVERR_BAD_LENGTH);
+        const uint32_t fill = valid ? 0u : 0x7FFF7FFFu;
+        uint32_t* row = reinterpret_cast<uint32_t*>(out + ((size_t)e * p.Hq + h0) * D);
+        for (int i = tid; i < G * D / 2; i += kThreads) row[i] = fill;
+        if (tid < G) p.lse[(size_t)e * p.Hq + h0 + tid] = valid ? -INFINITY : NAN;
+    }
+    if (lo >= hi) return;
 
     // ---- Registers of a sequence: q as the mma's B operand, O^T, the sums.
     // q, word w: pairs (P, P + 4) of its 8 dims, P = 0..3
@@ -456,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     float acc[W][2][4];         // O^T: dims q4_v_dim(g, w) + 2u (rows g), + 2u + 1, heads 2t, 2t + 1
     float lacc[4];              // sums of the rounded weights (all rows alike)
     float m0, m1, l0, l1;       // running maximum (log2 domain), sums of this lane's weights
-    int seq_L = 0, seq_start = 0, seq_page0 = 0;
+    int seq_L = 0, seq_start = 0;
     bool dead = false;          // a copy timed out
     bool bad = false;           // this sequence met a bad page id or a timeout
 
@@ -464,7 +535,6 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         const SeqSpan sp = seq_span(p.context_lens[b], p.window, p.max_ctx, p.maxp, 1);
         seq_L = sp.L;
         seq_start = sp.start;
-        seq_page0 = sp.first_page;
         const T* qrow = reinterpret_cast<const T*>(p.q) + ((size_t)b * p.Hq + h0 + g) * D;
         auto fragment = [&](int w) {
             uint4 x = make_uint4(0, 0, 0, 0);
@@ -503,8 +573,6 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         for (int j = 0; j < N; ++j) {
             const unsigned char* blk = blk0 + j * PB;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
-#pragma unroll
             for (int sl = 0; sl < W / V; ++sl) {  // runs of V words that one read takes
                 uint32_t ka[V], kb[V];
                 uint32_t pa_, pb_;  // (s, z) of the run's group
@@ -530,10 +598,14 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
                 for (int i = 0; i < V; ++i) {
                     const uint4 q = Cfg::kQShared ? s_q[(sl * V + i) * 32 + lane]
                                                   : qf[Cfg::kQShared ? 0 : sl * V + i];
-                    M::mma(s[j], Q::fma2(sa, Q::template code16<0>(ka[i]), za),
-                           Q::fma2(sb, Q::template code16<0>(kb[i]), zb),
-                           Q::fma2(sa, Q::template code16<1>(ka[i]), za),
-                           Q::fma2(sb, Q::template code16<1>(kb[i]), zb), q.x, q.y);
+                    const uint32_t a0 = Q::fma2(sa, Q::template code16<0>(ka[i]), za);
+                    const uint32_t a1 = Q::fma2(sb, Q::template code16<0>(kb[i]), zb);
+                    const uint32_t a2 = Q::fma2(sa, Q::template code16<1>(ka[i]), za);
+                    const uint32_t a3 = Q::fma2(sb, Q::template code16<1>(kb[i]), zb);
+                    if (sl == 0 && i == 0)
+                        M::mma0(s[j], a0, a1, a2, a3, q.x, q.y);
+                    else
+                        M::mma(s[j], a0, a1, a2, a3, q.x, q.y);
                     M::mma(s[j], Q::fma2(sa, Q::template code16<2>(ka[i]), za),
                            Q::fma2(sb, Q::template code16<2>(kb[i]), zb),
                            Q::fma2(sa, Q::template code16<3>(ka[i]), za),
@@ -774,14 +846,11 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         const int c1 = min(hi, c0 + kQ4StagedPages);
         __syncthreads();  // the previous stretch's ids have been used
         bool bad_id = false;
-        for (int f = c0 + threadIdx.x; f < c1; f += kThreads) {
-            const int a = f < s_base[b + 1] ? b : sequence_of(f);
-            int first_page = 0;
-            if (p.window > 0) {
-                const int Lb = p.context_lens[a];
-                first_page = (p.window < Lb ? Lb - p.window : 0) / kPageSize;
-            }
-            int id = p.block_tables[(size_t)a * p.maxp + first_page + (f - s_base[a])];
+#pragma unroll
+        for (int i = 0; i < kIds; ++i) {
+            const int f = c0 + tid + i * kThreads;
+            if (f >= c1) continue;
+            int id = again || c0 != lo ? *table_entry(f) : ids[i];
             if (id < 0 || id >= p.num_pages) {
                 id = -1;
                 bad_id = true;
@@ -793,23 +862,48 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         const bool careful = __syncthreads_or(bad_id);
 
         int ask = NP * warp;  // first page (from c0) of the next slot to request
-        auto request = [&]() {
-            int id = -1;
-            if (lane < NP && ask + lane < c1 - c0) id = s_pid[ask + lane];
-            const uint32_t n_ids = __popc(__ballot_sync(0xffffffffu, id >= 0));
-            const uint32_t bar = bar_w + in_slot * 8;
-            if (lane == 0) mbar_arrive_expect_tx(bar, n_ids * PB + stall);
-            __syncwarp();
-            if (id >= 0)
-                bulk_g2s(ring_u + in_slot * SB + lane * PB,
-                         p.cache + ((size_t)id * p.Hkv + kvh) * (size_t)PB, PB, bar);
-            stall = 0;
+        const int n_ids = c1 - c0;
+        auto request = [&]() PA_INLINE_LAMBDA {
+            if (lane == 0) {
+                const uint32_t bar = bar_w + in_slot * 8, dst = ring_u + in_slot * SB;
+                int id[NP], n = 0;
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    id[j] = j == 0 || ask + j < n_ids ? s_pid[ask + j] : -1;
+                    n += id[j] >= 0 ? PB : 0;
+                }
+                mbar_arrive_expect_tx(bar, n + stall);
+#pragma unroll
+                for (int j = 0; j < NP; ++j)
+                    if (id[j] >= 0)
+                        bulk_g2s(dst + j * PB,
+                                 p.cache + ((size_t)id[j] * p.Hkv + kvh) * (size_t)PB, PB, bar);
+                stall = 0;
+            }
             ask += NP * kWarps;
             in_slot = in_slot + 1 == NS ? 0 : in_slot + 1;
             ++pending;
         };
+        // The next slot's pages are there (or the wait for them ran out).
+        auto wait = [&]() PA_INLINE_LAMBDA {
+            const uint32_t bar = bar_w + out_slot * 8;
+            if (!__all_sync(0xffffffffu, mbar_try_wait(bar, out_phase)) &&
+                !__all_sync(0xffffffffu, mbar_wait_bounded(bar, out_phase))) {
+                if (lane == 0) atomicOr(p.err, PA_DEVERR_TIMEOUT);
+                dead = bad = true;
+            }
+        };
+        auto release = [&]() PA_INLINE_LAMBDA {
+            --pending;
+            __syncwarp();  // every lane has read the slot
+            if (ask < n_ids) request();
+            if (++out_slot == NS) {
+                out_slot = 0;
+                out_phase ^= 1;
+            }
+        };
         if (!dead)
-            for (int i = 0; i < NS && ask < c1 - c0; ++i) request();
+            for (int i = 0; i < NS && ask < n_ids; ++i) request();
         // (the first q is fetched while the first pages are on their way)
         if (c0 == lo) begin_sequence();
 
@@ -817,41 +911,37 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         while (true) {
             const int seg_end = min(c1, s_base[b + 1]);
             // Pages that are attended whole lie in [whole0, whole1).
-            const int base = s_base[b] - seq_page0;  // page of token 0
+            const int base = -s_page0[b];  // page of token 0
             const int whole0 = careful ? INT_MAX : base + (seq_start + kPageSize - 1) / kPageSize;
             const int whole1 = min(seg_end, base + seq_L / kPageSize);
             while (f < seg_end) {
-                const int sub = (f - c0) & (NP - 1);
-                if (sub == 0) {
-                    const bool ok = mbar_wait_bounded(bar_w + out_slot * 8, out_phase);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        if (lane == 0) atomicOr(p.err, PA_DEVERR_TIMEOUT);
-                        dead = bad = true;
+                if (((f - c0) & (NP - 1)) == 0) {
+                    // Slots of whole pages, the bulk of a long sequence.
+                    if (f >= whole0) {
+                        for (; f + NP <= whole1; f += NP * kWarps) {
+                            wait();
+                            if (dead) break;
+                            pages(ring_w + out_slot * SB, 0, Slot{}, std::false_type{});
+                            release();
+                        }
+                        if (!dead && f >= seg_end) break;
+                    }
+                    if (!dead) wait();
+                    if (dead) {
                         f = c1;
                         break;
                     }
-                    --pending;
                 }
-                const unsigned char* blk = ring_w + out_slot * SB + sub * PB;
-                const int tok0 = (f - base) * kPageSize;
-                if (sub == 0 && f >= whole0 && f + NP <= whole1) {
-                    pages(blk, tok0, Slot{}, std::false_type{});
-                    f += NP;
-                } else {
-                    if (careful && s_pid[f - c0] < 0)
-                        bad = true;
-                    else
-                        pages(blk, tok0, One{}, std::true_type{});
-                    ++f;
-                }
+                // One page, with some of its tokens masked or a bad id near.
+                if (careful && s_pid[f - c0] < 0)
+                    bad = true;
+                else
+                    pages(ring_w + out_slot * SB + ((f - c0) & (NP - 1)) * PB,
+                          (f - base) * kPageSize, One{}, std::true_type{});
+                ++f;
                 if (((f - c0) & (NP - 1)) == 0 || f == c1) {  // the slot is used up
                     f += NP * (kWarps - 1);
-                    __syncwarp();  // every lane has read it
-                    if (ask < c1 - c0) request();
-                    if (++out_slot == NS) {
-                        out_slot = 0;
-                        out_phase ^= 1;
-                    }
+                    release();
                 }
             }
             if (s_base[b + 1] > c1 && c1 < hi) break;  // goes on in the next stretch

@@ -48,7 +48,9 @@ __device__ __noinline__ float exact_code(float x, float z, float s) {
 // rounds the quotient to an integer r in one step, wrong only where d / s lies
 // within 2^-16 of the middle between two integers; there the residual
 // d - r s, which is exact, decides.  Such middles are common, not rare: values
-// and scales of T are coarse, so about one bf16 element in 300 is an exact tie.
+// and scales of T are coarse, so about one bf16 element in 300 is an exact
+// tie.  They are looked for two elements at a time: all eight together, three
+// warps in five took the slow side.
 template <typename T>
 __device__ __forceinline__ void quantise8(const uint4& raw, uint32_t (&code)[2], uint32_t& s16,
                                           uint32_t& z16) {
@@ -67,41 +69,44 @@ __device__ __forceinline__ void quantise8(const uint4& raw, uint32_t (&code)[2],
     const bool nan = mx != mx || mn != mn;
     mx = fminf(fmaxf(mx, -Q::kLimit), Q::kLimit);
     mn = fminf(fmaxf(mn, -Q::kLimit), Q::kLimit);
-    const float qs = __fdiv_rn(mx - mn, 15.f);
+    const float qs = (mx - mn) * (1.f / 15.f);  // (within 2 of its units)
     s16 = Q::from_float(qs);
     if (Q::near_tie(qs)) s16 = exact_scale<T>(mx, mn);
     // z = RN_T(mn - 16 s): mn is a value of T, so this is one fma of T.
     z16 = Q::fma2(Q::from_float(-16.f), s16, Q::from_float(mn)) & 0xffffu;
     const float s = Q::to_float(s16), z = Q::to_float(z16);
-    const float inv = __frcp_rn(s);  // (s = 0: inf; the codes are dropped below)
+    float inv;  // within 1 unit (s = 0: inf, and the codes are dropped below)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const float half = 0.5f * s, close = half * 0.99996f;
     float v[8];
-    float worst = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float d = Q::to_float(i & 1 ? x[i / 2] >> 16 : x[i / 2] & 0xffffu) - z;
-        v[i] = fmaf(d, inv, kMagic);
-        worst = fmaxf(worst, fabsf(fmaf(kMagic - v[i], s, d)));
-    }
-    const float half = 0.5f * s;
-    if ((worst > half * 0.99996f || s < 1e-37f) && s16 != 0) {
-        if (s < 1e-37f) {  // (only bf16 scales get here)
+    for (int i = 0; i < 8; i += 2) {
+        float xv[2], d[2], res[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = kMagic +
-                       exact_code(Q::to_float(i & 1 ? x[i / 2] >> 16 : x[i / 2] & 0xffffu), z, s);
-        } else {
+        for (int k = 0; k < 2; ++k) {
+            xv[k] = Q::to_float(k ? x[i / 2] >> 16 : x[i / 2] & 0xffffu);
+            d[k] = xv[k] - z;
+            // Off by less than 2^-17 before it is rounded, for quotients up to 32:
+            // d, 1 / s and its use, 32 (2^-24 + 2^-23).
+            v[i + k] = fmaf(d[k], inv, kMagic);
+            res[k] = fmaf(kMagic - v[i + k], s, d[k]);
+        }
+        if (fmaxf(fabsf(res[0]), fabsf(res[1])) > close) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float xv = Q::to_float(i & 1 ? x[i / 2] >> 16 : x[i / 2] & 0xffffu);
-                const float d = xv - z;
-                const float back = d - xv;  // what d lost: x - z = d + e
-                const float e = (xv - (d - back)) - (z + back);
-                const float res = fmaf(kMagic - v[i], s, d);
-                const float over = (fabsf(res) - half) + copysignf(1.f, res) * e;
-                if (over > 0.f || (over == 0.f && (__float_as_uint(v[i]) & 1u)))
-                    v[i] += copysignf(1.f, res);
+            for (int k = 0; k < 2; ++k) {
+                const float back = d[k] - xv[k];  // what d lost: x - z = d + e
+                const float e = (xv[k] - (d[k] - back)) - (z + back);
+                const float over = (fabsf(res[k]) - half) + copysignf(1.f, res[k]) * e;
+                if (over > 0.f || (over == 0.f && (__float_as_uint(v[i + k]) & 1u)))
+                    v[i + k] += copysignf(1.f, res[k]);
             }
         }
+    }
+    if (s < 1e-37f && s16 != 0) {  // 1 / s overflows (bf16 only)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = kMagic +
+                   exact_code(Q::to_float(i & 1 ? x[i / 2] >> 16 : x[i / 2] & 0xffffu), z, s);
     }
     // The bits of kMagic + 16 + c, each moved to its place and added up; what
     // all eight constants add up to is taken off again.

@@ -413,3 +413,58 @@ def test_empty_calls():
     assert int(c.count_nonzero()) == 0
     out, lse, err = decode_case(21, [0, 0, 0], 2, 1, 64, "f16", max_len=0)
     assert (out == 0).all() and np.isneginf(lse).all()
+
+
+@pytest.fixture(scope="module")
+def late_writer():
+    """tests/cuda/pdl_writer.cu: a kernel that lets the next one start early, waits 20 us and only
+    then writes the block table and the lengths."""
+    import ctypes
+    import os
+    import subprocess
+    here = os.path.dirname(os.path.abspath(__file__))
+    os.makedirs(os.path.join(here, "_build"), exist_ok=True)
+    so = os.path.join(here, "_build", "libpdl_writer_q4.so")
+    src = os.path.join(here, "cuda", "pdl_writer.cu")
+    if not os.path.exists(so) or os.path.getmtime(so) < os.path.getmtime(src):
+        subprocess.run(["nvcc", "-gencode", "arch=compute_103a,code=sm_103a", "-O2", "-shared",
+                        "-Xcompiler", "-fPIC", src, "-o", so], check=True)
+    lib = ctypes.CDLL(so)
+    P = ctypes.c_void_p
+    lib.launch_delayed_copy.argtypes = [P, P, ctypes.c_int, P, P, ctypes.c_int, ctypes.c_ulonglong,
+                                        P]
+    return lib
+
+
+@pytest.mark.parametrize("old", ["same lengths", "a token more", "pages fewer", "garbage"])
+@pytest.mark.parametrize("lens,window,D", [([3000, 1200, 0, 2049, 77], 0, 128),
+                                           ([3000, 1200, 2049, 77], 1000, 64),
+                                           ([20000], 0, 256), ([30] * 127 + [0], 0, 64),
+                                           ([40, 3] * 100, 0, 96)])
+def test_decode_uses_lengths_and_ids_written_late(late_writer, lens, window, D, old):
+    # What the kernel reads before its dependency wait are hints; everything counts only as it
+    # stands after the wait.  The old table points at a page of NaN scales.
+    q, cache, bt, lens = make_decode(30, lens, 4, 2, D, "f16")
+    want = ref.decode(q, cache.cpu().numpy(), bt, lens, D ** -0.5, window, "f16")
+    unused = sorted(set(range(cache.shape[0])) - set(bt.ravel().tolist()))
+    old_bt = np.full_like(bt, unused[0])
+    old_lens = {"same lengths": lens, "a token more": np.minimum(lens + 1, lens.max()),
+                "pages fewer": lens // 2,
+                "garbage": np.where(np.arange(lens.size) % 2, -5, 1 << 30)}[old].astype(np.int32)
+    if old == "garbage":
+        old_bt[:, ::2] = -7
+        old_bt[:, 1::2] = 1 << 30
+    B, Hq = q.shape[:2]
+    plan = pa.pa_q4_plan(B, Hq, 2, D, 16, cache.shape[0], bt.shape[1], int(lens.max()), window)
+    ws = pa.new_workspace(plan, "cuda")
+    tq = to_t(q, "f16")
+    new = torch.from_numpy(bt).cuda(), torch.from_numpy(lens).cuda()
+    now = torch.from_numpy(old_bt).cuda(), torch.from_numpy(old_lens).cuda()
+    out = torch.full_like(tq, float("nan"))
+    lse = torch.full((B, Hq), float("nan"), device="cuda")
+    stream = torch.cuda.current_stream()
+    assert late_writer.launch_delayed_copy(new[0].data_ptr(), now[0].data_ptr(), bt.size,
+                                           new[1].data_ptr(), now[1].data_ptr(), lens.size, 20000,
+                                           stream.cuda_stream) == 0
+    pa.pa_q4_decode(plan, tq, cache, now[0], now[1], D ** -0.5, window, out, lse, ws)
+    check((out.double().cpu().numpy(), lse.double().cpu().numpy(), pa.pa_get_error(ws)), want)
