@@ -49,8 +49,8 @@ __device__ __noinline__ float exact_code(float x, float z, float s) {
 // within 2^-16 of the middle between two integers; there the residual
 // d - r s, which is exact, decides.  Such middles are common, not rare: values
 // and scales of T are coarse, so about one bf16 element in 300 is an exact
-// tie.  They are looked for two elements at a time: all eight together, three
-// warps in five took the slow side.
+// tie.  They are looked for four elements at a time: of all eight together, three
+// warps in five had one.
 template <typename T>
 __device__ __forceinline__ void quantise8(const uint4& raw, uint32_t (&code)[2], uint32_t& s16,
                                           uint32_t& z16) {
@@ -67,6 +67,7 @@ __device__ __forceinline__ void quantise8(const uint4& raw, uint32_t (&code)[2],
     float mx = Q::to_float(ext & 0xffffu);
     float mn = -Q::to_float(ext >> 16);
     const bool nan = mx != mx || mn != mn;
+    const float most = mx, least = mn;
     mx = fminf(fmaxf(mx, -Q::kLimit), Q::kLimit);
     mn = fminf(fmaxf(mn, -Q::kLimit), Q::kLimit);
     const float qs = (mx - mn) * (1.f / 15.f);  // (within 2 of its units)
@@ -79,26 +80,37 @@ __device__ __forceinline__ void quantise8(const uint4& raw, uint32_t (&code)[2],
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
     const float half = 0.5f * s, close = half * 0.99996f;
     float v[8];
+    const float2 inv2 = make_float2(inv, inv), s2 = make_float2(s, s), nz2 = make_float2(-z, -z);
+    const float2 magic2 = make_float2(kMagic, kMagic), minus2 = make_float2(-1.f, -1.f);
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        float xv[2], d[2], res[2];
+    for (int i = 0; i < 8; i += 4) {
+        float2 xv[2], d[2], res[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            xv[k] = Q::to_float(k ? x[i / 2] >> 16 : x[i / 2] & 0xffffu);
-            d[k] = xv[k] - z;
+            const uint32_t w = x[i / 2 + k];
+            xv[k] = make_float2(Q::to_float(w & 0xffffu), Q::to_float(w >> 16));
+            d[k] = __fadd2_rn(xv[k], nz2);
             // Off by less than 2^-17 before it is rounded, for quotients up to 32:
             // d, 1 / s and its use, 32 (2^-24 + 2^-23).
-            v[i + k] = fmaf(d[k], inv, kMagic);
-            res[k] = fmaf(kMagic - v[i + k], s, d[k]);
+            const float2 r = __ffma2_rn(d[k], inv2, magic2);
+            res[k] = __ffma2_rn(__ffma2_rn(r, minus2, magic2), s2, d[k]);
+            v[i + 2 * k] = r.x;
+            v[i + 2 * k + 1] = r.y;
         }
-        if (fmaxf(fabsf(res[0]), fabsf(res[1])) > close) {
+        const float worst = fmaxf(fmaxf(fabsf(res[0].x), fabsf(res[0].y)),
+                                  fmaxf(fabsf(res[1].x), fabsf(res[1].y)));
+        if (__any_sync(0xffffffffu, worst > close)) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float back = d[k] - xv[k];  // what d lost: x - z = d + e
-                const float e = (xv[k] - (d[k] - back)) - (z + back);
-                const float over = (fabsf(res[k]) - half) + copysignf(1.f, res[k]) * e;
-                if (over > 0.f || (over == 0.f && (__float_as_uint(v[i + k]) & 1u)))
-                    v[i + k] += copysignf(1.f, res[k]);
+            for (int k = 0; k < 4; ++k) {
+                const float xk = k & 1 ? xv[k / 2].y : xv[k / 2].x;
+                const float dk = k & 1 ? d[k / 2].y : d[k / 2].x;
+                const float rk = k & 1 ? res[k / 2].y : res[k / 2].x;
+                const float back = dk - xk;  // what d lost: x - z = d + e
+                const float e = (xk - (dk - back)) - (z + back);
+                const float over = (fabsf(rk) - half) + copysignf(1.f, rk) * e;
+                // above the middle, or on it with r odd
+                const float bar = __uint_as_float((__float_as_uint(v[i + k]) & 1u) * 0x80000001u);
+                if (over > bar) v[i + k] += copysignf(1.f, rk);
             }
         }
     }
@@ -108,6 +120,14 @@ __device__ __forceinline__ void quantise8(const uint4& raw, uint32_t (&code)[2],
             v[i] = kMagic +
                    exact_code(Q::to_float(i & 1 ? x[i / 2] >> 16 : x[i / 2] & 0xffffu), z, s);
     }
+    // Codes below 0 or above 15 come from values beyond the limits, or spaced
+    // wider than the step: seen from the group's least and greatest.
+    constexpr float kLow = kMagic + 16.f, kHigh = kMagic + 31.f;
+    if (__any_sync(0xffffffffu,
+                   !((least - z) * inv >= 15.625f && (most - z) * inv <= 31.375f))) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], kLow), kHigh);
+    }
     // The bits of kMagic + 16 + c, each moved to its place and added up; what
     // all eight constants add up to is taken off again.
     constexpr uint32_t kOne = 0x4B400010u;
@@ -116,10 +136,7 @@ __device__ __forceinline__ void quantise8(const uint4& raw, uint32_t (&code)[2],
     for (int k = 0; k < 2; ++k) {
         uint32_t sum = 0u - kSum;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float c = fminf(fmaxf(v[4 * k + i], kMagic + 16.f), kMagic + 31.f);
-            sum += __float_as_uint(c) << (4 * i);
-        }
+        for (int i = 0; i < 4; ++i) sum += __float_as_uint(v[4 * k + i]) << (4 * i);
         code[k] = nan || s16 == 0 ? 0u : sum;
     }
     if (nan) {

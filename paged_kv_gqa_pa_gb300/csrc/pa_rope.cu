@@ -18,12 +18,14 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "pa_q4.cuh"
 
 namespace pa {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeItems = 4;  // items a thread requests before it waits for the angles
+constexpr int kRopeThreads = 256;  // at most
+constexpr int kRopeItems = 2;  // items a thread requests before it waits for the angles
 
 struct RopeAxesParams {
     const unsigned char* q;
@@ -97,12 +99,12 @@ struct RopeElem<float> {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const RopeAxesParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 5) rope_axes_kernel(const RopeAxesParams p) {
     constexpr int N = RopeElem<T>::kN;
     constexpr int ES = 16 / N;
     __shared__ float s_cos[kMaxRopePairs];
     __shared__ float s_sin[kMaxRopePairs];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, nt = blockDim.x;
     const long long t = blockIdx.x;
     const int half = p.R / 2;
     const int turn = half / N;                // rotated items of a head
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const RopeAxesP
     unsigned char* dst[kRopeItems];
 #pragma unroll
     for (int u = 0; u < kRopeItems; ++u) {
-        const int i = tid + u * kRopeThreads;
+        const int i = tid + u * nt;
         c[u] = -1;
         if (i < items) {
             const unsigned char* src;
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const RopeAxesP
             if (c[u] < turn) b[u] = *reinterpret_cast<const uint4*>(src + (size_t)half * ES);
         }
     }
-    for (int i = tid; i < half; i += kRopeThreads) {
+    for (int i = tid; i < half; i += nt) {
         const int pos = p.positions[(size_t)p.axis[i] * p.n + t];
         const unsigned long long turns = (unsigned long long)(long long)pos * p.freq[i];
         const float fr = (float)(int)(turns >> 32) * 4.656612873077393e-10f;  // 2^-31: half turns
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const RopeAxesP
 #pragma unroll
     for (int u = 0; u < kRopeItems; ++u)
         if (c[u] >= 0) finish(c[u], a[u], b[u], dst[u]);
-    for (int i = tid + kRopeItems * kRopeThreads; i < items; i += kRopeThreads) {
+    for (int i = tid + kRopeItems * nt; i < items; i += nt) {
         int ci;
         const unsigned char* src;
         unsigned char* d;
@@ -270,7 +272,10 @@ extern "C" int pa_rope_axes(int num_tokens, int num_q_heads, int num_kv_heads, i
     p.inverse = inverse;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)num_tokens);
-    cfg.blockDim = dim3(kRopeThreads);
+    // Threads for kRopeItems items each.
+    const int items = (num_q_heads + num_kv_heads) * (half / vec + (head_dim - rotary_dim) / vec);
+    const int threads = (items + kRopeItems * 32 - 1) / (kRopeItems * 32) * 32;
+    cfg.blockDim = dim3(std::min(kRopeThreads, threads));
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
