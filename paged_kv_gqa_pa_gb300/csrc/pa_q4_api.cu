@@ -23,7 +23,7 @@ PA_Q4_EXTERN(256)
 
 constexpr int kQ4MaxBatch = 4096;
 constexpr int kQ4MinRun = 2;    // pages of a warp, at least
-constexpr int kQ4KernelRows = 8;  // partials per sequence beyond which a kernel merges
+constexpr int kQ4KernelRows = 4;  // partials per sequence beyond which a kernel merges
 
 // Workspace: [control block | counters of the partials left, groups x B | run
 // size and page sums for the merge kernel | (max, sum) of the partials | their
@@ -119,13 +119,18 @@ int pa_q4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
     p.heads_per_cta = g / nchunk;
     // One wave of resident CTAs over all groups, filled to a little under its
     // slots (a grid that needs every slot had CTAs starting in a second wave),
-    // but no more than give every warp kQ4MinRun pages of the longest batch.
+    // but no more than give every sequence one and every warp kQ4MinRun pages
+    // of the longest batch.
     int span = (max_context_len + kPageSize - 1) / kPageSize;
     if (window > 0) span = std::min(span, (window - 1 + kPageSize - 1) / kPageSize + 1);
     const long long pages = std::max(1ll, (long long)std::max(1, batch) * span);
     const long long slots = (long long)p.num_sms * q4_ctas_per_sm(head_dim, batch);
     long long x = std::max(1ll, (slots - slots / 64) / groups);
-    x = std::min(x, (pages + kWarps * kQ4MinRun - 1) / (kWarps * kQ4MinRun));
+    if (span <= kQ4Short && batch <= x)
+        x = std::max(1, batch);  // one for each sequence
+    else
+        x = std::min(x, std::max<long long>(batch, (pages + kWarps * kQ4MinRun - 1) /
+                                                       (kWarps * kQ4MinRun)));
     p.ctas_per_group = (int)x;
     p.ctas = (int)std::min<long long>(x * groups, INT_MAX);
     const Q4WsLayout wl = q4_ws_layout(batch, head_dim, groups, p.ctas_per_group);
@@ -172,7 +177,9 @@ int pa_q4_decode(const pa_q4_plan_t* plan, const void* q, const void* cache,
     p.err = reinterpret_cast<unsigned*>(ws);
     p.ws_info = reinterpret_cast<int*>(ws + wl.info_off);
     // A sequence of a batch of B leaves about X / B partials: beyond
-    // kQ4KernelRows a kernel of its own gathers them.
+    // kQ4KernelRows a kernel of its own gathers them (limits of 4, 8 and 20: 4
+    // sequences of 1000 tokens 11.3, 12.7 and 12.7 us, 8 ragged ones up to 4000
+    // 15.0, 15.9 and 16.0, one of 2000 7.9, 7.9 and 9.8).
     p.merge_kernel = X > kQ4KernelRows * plan->batch ? 1 : 0;
     p.counters = reinterpret_cast<unsigned*>(ws + wl.ctr_off);
     p.B = plan->batch;
