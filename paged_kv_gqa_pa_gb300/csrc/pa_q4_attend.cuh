@@ -99,8 +99,8 @@ struct Q4Cfg {
     // with 4 and 49.9 with 3; at D 128 four did not pay (40.1 and 40.4 us).
     static constexpr int kMinBlocks = D <= 96 ? 4 : 3;
     static_assert(kMinBlocks * (kSmemBytes + 1024 + 128) <= 228 * 1024, "CTAs per SM");
-    // (two words per sequence follow: s_base, s_page0)
-    static int smem(int B) { return kSmemBytes + (2 * B + 1) * 4; }
+    // (three words per sequence follow: s_base, s_page0, s_len)
+    static int smem(int B) { return kSmemBytes + (3 * B + 1) * 4; }
 };
 
 // mma.sync m16n8k16, 16-bit in, fp32 accumulate; and fp32 pairs to 16 bits.
@@ -386,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_ml + kWarps * kMaxHeadsPerCta * 3);
     int* s_base = reinterpret_cast<int*>(bars + kWarps * NS);
     int* s_page0 = s_base + p.B + 1;
+    int* s_len = s_page0 + p.B;
     __shared__ int s_red[kWarps];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -420,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
             const int n = sp.valid ? sp.end_page - sp.first_page : 0;
             s_base[b] = n;
             s_page0[b] = sp.first_page;
+            s_len[b] = sp.L;
             sum += n;
             longest = max(longest, n);
         }
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     T* const out = reinterpret_cast<T*>(p.out);
     for (int e = blockIdx.x; e < p.B; e += gridDim.x) {
         if (s_base[e + 1] != s_base[e]) continue;
-        const bool valid = seq_span(p.context_lens[e], p.window, p.max_ctx, p.maxp, 1).valid;
+        const bool valid = seq_span(s_len[e], p.window, p.max_ctx, p.maxp, 1).valid;
         if (!valid && tid == 0) atomicOr(p.err, PA_DEVERR_BAD_LENGTH);
         const uint32_t fill = valid ? 0u : 0x7FFF7FFFu;
         uint32_t* row = reinterpret_cast<uint32_t*>(out + ((size_t)e * p.Hq + h0) * D);
@@ -534,7 +536,8 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
 
     // ---- Registers of a sequence: q as the mma's B operand, O^T, the sums.
     // q, word w: pairs (P, P + 4) of its 8 dims, P = 0..3
-    [[maybe_unused]] uint4 qf[Cfg::kQShared ? 1 : W];
+    // (kQShared: this warp's share of it on its way to shared memory)
+    uint4 qf[Cfg::kQShared ? W / kWarps : W];
     float acc[W][2][4];         // O^T: dims q4_v_dim(g, w) + 2u (rows g), + 2u + 1, heads 2t, 2t + 1
     float lacc[4];              // sums of the rounded weights (all rows alike)
     float m0, m1, l0, l1;       // running maximum (log2 domain), sums of this lane's weights
@@ -542,24 +545,29 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     bool dead = false;          // a copy timed out
     bool bad = false;           // this sequence met a bad page id or a timeout
 
-    auto begin_sequence = [&]() PA_INLINE_LAMBDA {
-        const SeqSpan sp = seq_span(p.context_lens[b], p.window, p.max_ctx, p.maxp, 1);
-        seq_L = sp.L;
-        seq_start = sp.start;
-        const T* qrow = reinterpret_cast<const T*>(p.q) + ((size_t)b * p.Hq + h0 + g) * D;
-        auto fragment = [&](int w) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (g < G) x = *reinterpret_cast<const uint4*>(qrow + q4_k_dim<D>(t, w));
-            return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                              __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-        };
-        if constexpr (Cfg::kQShared) {  // (no warp still reads the previous sequence's)
-            for (int w = warp; w < W; w += kWarps) s_q[w * 32 + lane] = fragment(w);
-            __syncthreads();
-        } else {
+    // The q of a sequence is requested first, and again for the next sequence
+    // before the states of the present one are joined, which hides the loads.
+    constexpr int QL = Cfg::kQShared ? W / kWarps : W;  // words of q this warp loads
+    auto load_q = [&](int seq) PA_INLINE_LAMBDA {
+        const T* qrow = reinterpret_cast<const T*>(p.q) + ((size_t)seq * p.Hq + h0 + g) * D;
 #pragma unroll
-            for (int w = 0; w < W; ++w) qf[w] = fragment(w);
+        for (int i = 0; i < QL; ++i) {
+            const int w = Cfg::kQShared ? warp + i * kWarps : i;
+            qf[i] = make_uint4(0, 0, 0, 0);
+            if (g < G) qf[i] = *reinterpret_cast<const uint4*>(qrow + q4_k_dim<D>(t, w));
         }
+    };
+    auto begin_sequence = [&]() PA_INLINE_LAMBDA {
+        seq_L = s_len[b];
+        seq_start = (p.window > 0 && p.window < seq_L) ? seq_L - p.window : 0;
+#pragma unroll
+        for (int i = 0; i < QL; ++i) {
+            const uint4 x = qf[i];
+            qf[i] = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                               __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+            if (Cfg::kQShared) s_q[(warp + i * kWarps) * 32 + lane] = qf[i];
+        }
+        if (Cfg::kQShared) __syncthreads();  // (no warp still reads the previous sequence's)
 #pragma unroll
         for (int w = 0; w < W; ++w)
 #pragma unroll
@@ -916,7 +924,10 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         if (!dead)
             for (int i = 0; i < NS && ask < n_ids; ++i) request();
         // (the first q is fetched while the first pages are on their way)
-        if (c0 == lo) begin_sequence();
+        if (c0 == lo) {
+            load_q(b);
+            begin_sequence();
+        }
 
         int f = dead ? c1 : c0 + NP * warp;  // next page of this warp
         while (true) {
@@ -956,10 +967,15 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
                 }
             }
             if (s_base[b + 1] > c1 && c1 < hi) break;  // goes on in the next stretch
+            if (s_base[b + 1] >= hi) {  // the range's last
+                end_sequence();
+                break;
+            }
+            int next = b + 1;
+            while (s_base[next + 1] == s_base[next]) ++next;
+            load_q(next);
             end_sequence();
-            if (s_base[b + 1] >= hi) break;  // the range's last
-            ++b;
-            while (s_base[b + 1] == s_base[b]) ++b;
+            b = next;
             begin_sequence();
             if (s_base[b] >= c1) break;
         }
