@@ -209,7 +209,8 @@ def check(got, want):
     assert (over <= 0).all(), f"out off by {np.abs(out - w_out).max():.3e}, beyond by {over.max():.3e}"
     fin = np.isfinite(w_lse)
     assert np.array_equal(lse[~fin], w_lse[~fin])
-    assert (np.abs(lse - w_lse)[fin] <= ltol[fin]).all(), np.abs(lse - w_lse)[fin].max()
+    d = np.abs(lse[fin] - w_lse[fin])
+    assert (d <= ltol[fin]).all(), d.max()
 
 
 def decode_case(seed, lens, Hq, Hkv, D, dtype, window=0, scale=None, **kw):
@@ -468,3 +469,108 @@ def test_decode_uses_lengths_and_ids_written_late(late_writer, lens, window, D, 
                                            stream.cuda_stream) == 0
     pa.pa_q4_decode(plan, tq, cache, now[0], now[1], D ** -0.5, window, out, lse, ws)
     check((out.double().cpu().numpy(), lse.double().cpu().numpy(), pa.pa_get_error(ws)), want)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(12, 1), (24, 1), (21, 3), (64, 2)])
+def test_decode_head_chunks(Hq, Hkv):
+    # More than 8 query heads per KV head go in equal chunks; 7 of 8 columns used.
+    decode_case(Hq, [300, 17, 64], Hq, Hkv, 64, "f16")
+    decode_case(Hq, [300, 17, 600], Hq, Hkv, 128, "bf16", window=130)
+
+
+def test_decode_nan_in_one_query_head_stays_there():
+    q, cache, bt, lens = make_decode(40, [500, 20], 8, 1, 128, "f16")
+    want = ref.decode(q, cache.cpu().numpy(), bt, lens, 0.1, 0, "f16")
+    q = q.copy()
+    q[0, 3, 17] = np.nan
+    out, lse, err = run_decode(q, cache, bt, lens, 0.1, 0, "f16")
+    assert err == 0 and np.isnan(out[0, 3]).all() and np.isnan(lse[0, 3])
+    rest = [0, 1, 2, 4, 5, 6, 7]
+    for b in (0, 1):
+        hs = rest if b == 0 else list(range(8))
+        check((out[b, hs], lse[b, hs], 0), [x[b, hs] for x in want])
+
+
+def test_sequences_may_share_pages():
+    q, cache, bt, lens = make_decode(41, [160, 160, 90], 4, 2, 128, "f16")
+    bt[1, :5] = bt[0, :5]
+    want = ref.decode(q, cache.cpu().numpy(), bt, lens, 0.1, 0, "f16")
+    check(run_decode(q, cache, bt, lens, 0.1, 0, "f16"), want)
+
+
+def test_offsets_beyond_32_bits():
+    # 900,000 pages of 5120 bytes: 4.6 GB, used near their end.
+    pages, D = 900_000, 256
+    cache = torch.empty(pages, 1, 20 * D, dtype=torch.uint8, device="cuda")
+    ids = np.array([pages - 1, 3, pages - 2, 840_001, pages - 7], np.int32)
+    g = np.random.default_rng(42)
+    n = 75
+    k, v = kv_values(g, (n, 1, D), "f16"), kv_values(g, (n, 1, D), "f16")
+    pos = np.arange(n)
+    slots = ids[pos // 16].astype(np.int64) * 16 + pos % 16
+    small = np.full((5, 1, 20 * D), 255, np.uint8)
+    want, kv = reference_cache(small, k, v, (pos // 16) * 16 + pos % 16, D, "f16")
+    cache[torch.from_numpy(ids).long().cuda()] = 255
+    sl = torch.from_numpy(slots).cuda()
+    pa.pa_q4_write(to_t(k, "f16"), to_t(v, "f16"), sl, cache)
+    assert np.array_equal(cache[torch.from_numpy(ids).long().cuda()].cpu().numpy(), want)
+    out = torch.empty(n, 1, D, dtype=torch.float16, device="cuda"), torch.empty(
+        n, 1, D, dtype=torch.float16, device="cuda")
+    pa.pa_q4_read(cache, sl, *out)
+    for o, w in zip(out, kv):
+        np.testing.assert_array_equal(o.double().cpu().numpy(), w)
+    q = ref.rn(g.standard_normal((1, 4, D)), "f16")
+    lens = np.array([n], np.int32)
+    res = run_decode(q, cache, ids[None], lens, 0.1, 0, "f16")
+    check(res, ref.decode(q, want, np.arange(5, dtype=np.int32)[None], lens, 0.1, 0, "f16"))
+
+
+def test_read_takes_slots_twice():
+    g = np.random.default_rng(43)
+    k = kv_values(g, (4, 2, 96), "bf16")
+    cache = pa.new_q4_cache(1, 2, 96)
+    pa.pa_q4_write(to_t(k, "bf16"), to_t(k, "bf16"), torch.arange(4, device="cuda"), cache)
+    out = torch.empty(6, 2, 96, dtype=torch.bfloat16, device="cuda")
+    out2 = torch.empty_like(out)
+    pa.pa_q4_read(cache, torch.tensor([2, 2, 0, 3, 2, 15], device="cuda"), out, out2)
+    assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[4]) and torch.equal(out, out2)
+    assert (out[5] == 0).all()  # an empty cell of a fresh cache
+
+
+def test_two_graphs_share_a_workspace_one_after_the_other():
+    q, cache, bt, lens = make_decode(44, [3000, 100, 2000, 900, 3], 8, 2, 128, "f16")
+    want = ref.decode(q, cache.cpu().numpy(), bt, lens, 0.1, 0, "f16")
+    plan = pa.pa_q4_plan(5, 8, 2, 128, 16, cache.shape[0], bt.shape[1], 3000)
+    ws = pa.new_workspace(plan, "cuda")
+    tq, tb, tl = to_t(q, "f16"), torch.from_numpy(bt).cuda(), torch.from_numpy(lens).cuda()
+    runs = []
+    for _ in range(2):
+        out, lse = torch.empty_like(tq), torch.empty(5, 8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(3):
+                pa.pa_q4_decode(plan, tq, cache, tb, tl, 0.1, 0, out, lse, ws)
+        runs.append((graph, out, lse))
+    for i in (0, 1, 1, 0):
+        runs[i][0].replay()
+    torch.cuda.synchronize()
+    for _, out, lse in runs:
+        check((out.double().cpu().numpy(), lse.double().cpu().numpy(), pa.pa_get_error(ws)), want)
+
+
+def test_the_largest_batch():
+    g = np.random.default_rng(45)
+    decode_case(45, g.integers(0, 20, 4096).tolist(), 1, 1, 64, "f16")
+
+
+def test_plans_for_other_sm_counts():
+    q, cache, bt, lens = make_decode(46, [500, 20, 1000], 4, 2, 128, "f16")
+    want = ref.decode(q, cache.cpu().numpy(), bt, lens, 0.1, 0, "f16")
+    for sms in (1, 8, 500):
+        plan = pa.pa_q4_plan(3, 4, 2, 128, 16, cache.shape[0], bt.shape[1], 1000, 0, sms)
+        ws = pa.new_workspace(plan, "cuda")
+        tq = to_t(q, "f16")
+        out, lse = torch.empty_like(tq), torch.empty(3, 4, device="cuda")
+        pa.pa_q4_decode(plan, tq, cache, torch.from_numpy(bt).cuda(),
+                        torch.from_numpy(lens).cuda(), 0.1, 0, out, lse, ws)
+        check((out.double().cpu().numpy(), lse.double().cpu().numpy(), pa.pa_get_error(ws)), want)
