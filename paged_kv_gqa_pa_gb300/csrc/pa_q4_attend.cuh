@@ -8,30 +8,37 @@
 // cache's codes stand for, made in registers right in front of the
 // mma.sync m16n8k16 that takes them.
 //
-//  * What bounds it.  A page of one KV head is 20 D bytes against 64 D for
-//    fp16, so memory could deliver about 38 elements per clock and SM at D 128.
-//    Each pair of elements costs a shift, a logic op and a packed fma (the
-//    code becomes the float 16 + c, the fma applies s and z with one
-//    rounding); with the softmax and the ring that is about 2 issue slots per
-//    element-pair and thread, 60-70 % of the issue rate at full memory speed.
-//    So the layout spends nothing else: codes and parameters lie as the
-//    mma fragments want them (no ldmatrix, no transposition, no bank
-//    conflict), both halves of a register come from one fma.
+//  * What bounds it.  A page of one KV head is 20 D bytes (64 D in fp16), so
+//    memory could deliver about 38 elements per clock and SM at D 128.  A pair
+//    of elements costs a shift, a logic op and a packed fma (the code becomes
+//    the float 16 + c, the fma applies s and z with one rounding); with the
+//    softmax and the ring a page of D 128 is about 290 warp instructions, 65 %
+//    of what an SM issues in the 112 cycles that memory needs for it.  So the
+//    layout spends nothing else: codes and parameters lie as the mma fragments
+//    want them (no ldmatrix, no transposition, no bank conflict), both halves of
+//    a register come from one fma.  tcgen05 would take its operands from shared
+//    memory, where the values would first have to be stored; at up to 8 query
+//    heads mma.sync is a fifth busy.
+//    Measured on GB300: 4 sequences of 100K tokens, 24/4 heads at D 256, 90 us,
+//    5.68 TB/s (0.84 of the measured copy rate).  From 128K to 512K tokens at D
+//    128 each further byte goes at 0.9-1.0 of that rate (bf16, whose weights take
+//    two mma, at 0.8); what is lost is a fixed part of 8 us and more: the start,
+//    warps of an SM that end unevenly, joining and merging.
 //  * Copies.  K, V and parameters of a page are one block, fetched by one
 //    cp.async.bulk into the ring of the warp that works on it; the pages of a
 //    CTA's range go to its four warps in turn.
 //  * Maximum.  m is raised, and O rescaled, only when a score exceeds it by
-//    more than 2^8 (weights then stay below 2^8, far from fp16's limit); so
-//    most pages need no shuffle, just one vote.
+//    more than 8 in the log2 domain (weights then stay below 2^8, far from
+//    fp16's limit); so most pages need no shuffle, just one vote.
 //  * Split.  Where every sequence is short (kQ4Short pages) and there are CTAs
-//    enough, each has one to itself.  Otherwise the pages the batch attends, all sequences end to end, are cut
-//    into equal ranges, one per CTA of the group, whatever the lengths; a range
-//    may hold many short sequences or part of a long one.  At a sequence's end
-//    the warps' states meet in shared memory.  A sequence inside the range is
-//    written; one cut by a border leaves a partial (o, maximum, sum) per CTA
-//    in the workspace.  Who merges a sequence's partials, always in order: the
-//    last CTA to leave one, or, in plans where a sequence may leave many, a
-//    second kernel that has them all in flight.
+//    enough, each has one to itself.  Otherwise the pages the batch attends, all
+//    sequences end to end, are cut into equal ranges, one per CTA of the group,
+//    whatever the lengths; a range may hold many short sequences or part of a
+//    long one.  At a sequence's end the warps' states meet in shared memory.  A
+//    sequence inside the range is written; one cut by a border leaves a partial
+//    (o, maximum, sum) per CTA in the workspace.  Who merges a sequence's
+//    partials, always in order: the last CTA to leave one, or, in plans where a
+//    sequence may leave many, a second kernel that has them all in flight.
 #pragma once
 
 #include <math.h>
@@ -80,8 +87,8 @@ struct Q4Cfg {
     static constexpr int kPair = D == 256 ? 1 : 2;
     static constexpr int kSlotBytes = kPair * Q4Layout<D>::kPageBytes;
     // Two slots are enough: a warp's next one streams in while it works on the
-    // other (three at D 128 or 256 measured no faster, 3-10 % slower on the
-    // largest batches).
+    // other (one sequence of 128K tokens at D 128: 39.9 us with two, 41.0 with
+    // three).
     static constexpr int kStages = D == 64 ? 4 : 2;
     static constexpr int kRingBytes = kWarps * kStages * kSlotBytes;
     // q's fragments: in registers, or in shared memory where the accumulators

@@ -7,6 +7,12 @@
 // slot and the addresses are worked out once; the four lanes of an aligned
 // quad hold a group of 32 dims, and D / 8 consecutive lanes a row.  The next
 // head's rows are requested before the present ones are worked on.
+//
+// Measured on GB300, 16384 bf16 rows of 4 heads at D 256 (88 MB either way, 13
+// us at the measured copy rate): the writer 31.6 us, bound by what it issues
+// (73 % of the slots; the borders of exact codes are most of it), the reader
+// 16.7 us, bound by memory latency (0.78 of the copy rate).  64 rows of 8 heads
+// at D 128: 1.9 us each, a launch.
 #include <algorithm>
 
 #include "pa_q4.cuh"
@@ -332,8 +338,10 @@ static int q4_cache_call(bool write, int num_tokens, int num_kv_heads, int head_
     p.n = num_tokens;
     p.Hkv = num_kv_heads;
     p.num_slots = (long long)num_pages * kPageSize;
-    // All heads of a token in one thread where the tokens alone make a few
-    // waves of CTAs, else as many threads as there are heads.
+    // As many heads in one thread as leave 512 CTAs: what is worked out once per
+    // token is then shared, and short inputs still spread out.  16384 rows of 4
+    // heads at D 256, written and read: 4 heads a thread 45.4 us, 2 heads 49.1,
+    // 1 head 61.7.
     const long long ctas = ((long long)num_tokens * (head_dim / 8) + kQ4Threads - 1) / kQ4Threads;
     p.heads = (int)std::max(1ll, std::min<long long>(num_kv_heads, ctas / 512));
     const cudaError_t e =

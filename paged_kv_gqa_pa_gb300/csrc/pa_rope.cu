@@ -8,6 +8,12 @@
 // 16 bytes of their partners R / 2 dims on, or 16 bytes behind dim R, which
 // are copied.
 //
+// Measured on GB300: 16384 bf16 tokens of 28 heads at D 256 70.8 us, 6.64 TB/s
+// (0.98 of the measured copy rate).  Two items a thread and 48 registers, five
+// CTAs of 256 threads per SM, keep the loads in flight; with four items (71
+// registers) it took 88.1 us, with two and four CTAs 77.0.  64 tokens of 40
+// heads at D 128: 2.3 us, a launch.
+//
 // Angles: the frequency as a fraction of a turn is a 64-bit fixed-point
 // number f = round(2^64 theta^(-2 i / R) / (2 pi)), so position * f modulo
 // 2^64 is the angle modulo one turn, exactly but for f's rounding (2^-33 of a
