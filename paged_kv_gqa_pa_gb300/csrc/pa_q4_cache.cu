@@ -338,12 +338,12 @@ static int q4_cache_call(bool write, int num_tokens, int num_kv_heads, int head_
     p.n = num_tokens;
     p.Hkv = num_kv_heads;
     p.num_slots = (long long)num_pages * kPageSize;
-    // As many heads in one thread as leave 512 CTAs: what is worked out once per
-    // token is then shared, and short inputs still spread out.  16384 rows of 4
-    // heads at D 256, written and read: 4 heads a thread 45.4 us, 2 heads 49.1,
-    // 1 head 61.7.
+    // As many heads in one thread as leave 608 CTAs (four per SM): what is worked
+    // out once per token is then shared, and short inputs still spread out.
+    // 16384 rows of 4 heads at D 256, written and read: 4 heads a thread 45.4
+    // us, 2 heads 49.1, 1 head 61.7.
     const long long ctas = ((long long)num_tokens * (head_dim / 8) + kQ4Threads - 1) / kQ4Threads;
-    p.heads = (int)std::max(1ll, std::min<long long>(num_kv_heads, ctas / 512));
+    p.heads = (int)std::max(1ll, std::min<long long>(num_kv_heads, ctas * num_kv_heads / 608));
     const cudaError_t e =
         dtype == PA_DTYPE_BF16
             ? launch_q4_cache<__nv_bfloat16>(write, head_dim, p, static_cast<cudaStream_t>(stream))
