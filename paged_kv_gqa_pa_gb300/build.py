@@ -1,7 +1,9 @@
 """Build libpa_gb300.so in-tree with nvcc for sm_103a (GB300).
 
 Each translation unit under csrc/ compiles in parallel; the objects link into
-one shared library with the static CUDA runtime.  Usage:
+one shared library with the static CUDA runtime.  csrc/pa_pyfast.c, the argument
+marshalling of q4.py in C, becomes a Python extension beside it where the
+interpreter's headers are installed (q4.py works without it).  Usage:
     python -m paged_kv_gqa_pa_gb300.build [--force] [--verbose]
 """
 from __future__ import annotations
@@ -12,12 +14,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpa_gb300.so")
+PYFAST_SRC = os.path.join(CSRC, "pa_pyfast.c")
+PYFAST = os.path.join(BUILD, "_pa_fast.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -39,6 +44,32 @@ def _deps():
             glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
 
 
+def _python_include():
+    inc = sysconfig.get_paths()["include"]
+    return inc if os.path.exists(os.path.join(inc, "Python.h")) else None
+
+
+def build_pyfast(force: bool = False, verbose: bool = False):
+    """The marshalling extension; None without the interpreter's headers or a C compiler."""
+    inc = _python_include()
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    if inc is None or cc is None:
+        return None
+    deps = [PYFAST_SRC, os.path.join(ROOT, "include", "pa.h"),
+            os.path.join(ROOT, "include", "pa_q4.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(PYFAST) and all(
+            os.path.getmtime(p) <= os.path.getmtime(PYFAST) for p in deps):
+        return PYFAST
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = PYFAST + f".tmp{os.getpid()}"
+    cmd = [cc, "-O2", "-shared", "-fPIC", "-I", inc, "-o", tmp, PYFAST_SRC]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, PYFAST)
+    return PYFAST
+
+
 def up_to_date() -> bool:
     if not os.path.exists(LIB):
         return False
@@ -47,6 +78,7 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
+    build_pyfast(force, verbose)
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -13,9 +13,12 @@ with.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 
 import torch
 
+from . import build as _build
 from .binding import (PA_DTYPE_BF16, PA_DTYPE_F16, PA_DTYPE_F32, PA_OK, PAError, load,
                       new_workspace, pa_get_error)
 
@@ -24,6 +27,9 @@ PA_DEVERR_NO_PAGES = 16
 PAGE_SIZE = 16
 _DTYPE = {torch.float16: PA_DTYPE_F16, torch.bfloat16: PA_DTYPE_BF16, torch.float32: PA_DTYPE_F32}
 _TORCH = {v: k for k, v in _DTYPE.items()}
+
+# The current stream's handle without a Stream object around it (1 us less).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class pa_q4_plan_t(ctypes.Structure):
@@ -52,11 +58,31 @@ class pa_q4_plan_t(ctypes.Structure):
 
 
 _bound = None
+# The marshalling extension (csrc/pa_pyfast.c), once the library is loaded: it makes the usual
+# call in about half the host time, and returns None where it leaves a call to the code here.
+_fast = None
+
+
+def _load_fast(lib):
+    if _raw_stream is None or not os.path.exists(_build.PYFAST):
+        return None
+    try:
+        spec = importlib.util.spec_from_file_location("_pa_fast", _build.PYFAST)
+        fast = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(fast)
+    except ImportError:  # built for another interpreter
+        return None
+    names = ("pa_q4_write", "pa_q4_read", "pa_q4_decode", "pa_extend_tables", "pa_rope_axes")
+    fast.setup((torch.float16, torch.bfloat16, torch.float32, torch.int32, torch.int64,
+                torch.uint8),
+               tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
+               getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), _raw_stream)
+    return fast
 
 
 def _lib():
     """The library with this module's signatures set."""
-    global _bound
+    global _bound, _fast
     if _bound is not None:
         return _bound
     lib = load()
@@ -77,6 +103,7 @@ def _lib():
     lib.pa_rope_axes.argtypes = ([i] * 6 + [ctypes.POINTER(i), i, i, ctypes.c_float, i] +
                                  [P, ll, P, ll, P, P, ll, P, ll, P])
     lib.pa_rope_axes.restype = i
+    _fast = _load_fast(lib)
     _bound = lib
     return lib
 
@@ -134,10 +161,6 @@ def _device_of(t, name):
     return t.get_device()
 
 
-# The current stream's handle without a Stream object around it (1 us less).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _stream(stream, dev):
     """cudaStream_t as an int: the device's current stream by default."""
     if stream is None:
@@ -160,6 +183,15 @@ def _call(fn, dev, args):
             status = fn(*args)
     if status != PA_OK:
         raise PAError(fn.__name__, status)
+
+
+def _answer(fn, status):
+    """Whether the extension made the call; raises for a status."""
+    if status is None:
+        return False
+    if status != PA_OK:
+        raise PAError(fn, status)
+    return True
 
 
 def _error_ptr(t, dev):
@@ -218,6 +250,9 @@ def _cache_args(k, v, slots, cache):
 def pa_q4_write(k, v, slots, cache, device_error=None, stream=None) -> None:
     """Quantise rows k, v [tokens, Hkv, D] (fp16 or bf16, columns of wider rows allowed)
     into the cache at `slots` (int64 [tokens], distinct; -1: left out)."""
+    if _fast is not None and device_error is None and stream is None and _answer(
+            "pa_q4_write", _fast.q4_write(k, v, slots, cache)):
+        return
     dev, sizes, kr, vr, sl, cp = _cache_args(k, v, slots, cache)
     _call(_lib().pa_q4_write, dev, (*sizes, *kr, *vr, sl, cp, _error_ptr(device_error, dev),
                                     _stream(stream, dev)))
@@ -226,6 +261,9 @@ def pa_q4_write(k, v, slots, cache, device_error=None, stream=None) -> None:
 def pa_q4_read(cache, slots, k_out, v_out, device_error=None, stream=None) -> None:
     """Rows the cache stands for at `slots`, into k_out, v_out [tokens, Hkv, D]
     (slot -1: zeros)."""
+    if _fast is not None and device_error is None and stream is None and _answer(
+            "pa_q4_read", _fast.q4_read(cache, slots, k_out, v_out)):
+        return
     dev, sizes, kr, vr, sl, cp = _cache_args(k_out, v_out, slots, cache)
     _call(_lib().pa_q4_read, dev, (*sizes, cp, sl, *kr, *vr, _error_ptr(device_error, dev),
                                    _stream(stream, dev)))
@@ -271,6 +309,10 @@ def _q4_decode_args(plan, q, cache, block_tables, context_lens, scale, window, o
 def pa_q4_decode(plan, q, cache, block_tables, context_lens, scale, window, out, lse, workspace,
                  stream=None) -> None:
     """One decode step over a 4-bit cache; arguments as pa_decode's."""
+    if _fast is not None and stream is None and _answer(
+            "pa_q4_decode", _fast.q4_decode(plan, q, cache, block_tables, context_lens, scale,
+                                            window, out, lse, workspace)):
+        return
     dev, args = _q4_decode_args(plan, q, cache, block_tables, context_lens, scale, window, out,
                                 lse, workspace, stream)
     _call(_lib().pa_q4_decode, dev, args)
@@ -333,6 +375,11 @@ def pa_extend_tables(past_lens, new_lens, free_pages, num_pages, block_tables, c
                      stream=None) -> None:
     """Block tables, lengths, slots and positions of a step, from the requests' lengths
     (past_lens, new_lens int32 [B]) and a list of free pages (int32); see include/pa_q4.h."""
+    if _fast is not None and device_error is None and stream is None and _answer(
+            "pa_extend_tables", _fast.extend_tables(past_lens, new_lens, free_pages, num_pages,
+                                                    block_tables, context_lens, starts, slots,
+                                                    positions, pages_taken)):
+        return
     dev = _device_of(past_lens, "past_lens")
     if block_tables.dim() != 2 or slots.dim() != 1 or free_pages.dim() != 1:
         raise ValueError("block_tables must be 2-D, slots and free_pages 1-D")
@@ -358,6 +405,10 @@ def pa_rope_axes(q, k, positions, sections, theta, q_out=None, k_out=None, rotar
     columns of wider rows allowed) with positions int32 [axes, tokens]; sections: pairs
     per axis.  q_out, k_out default to q and k (in place); q or k may be None.
     inverse=True turns back: applied to a gradient it is the rotation's backward pass."""
+    if _fast is not None and stream is None and _answer(
+            "pa_rope_axes", _fast.rope_axes(q, k, positions, sections, theta, q_out, k_out,
+                                            rotary_dim, interleaved, inverse)):
+        return
     some = q if q is not None else k
     if some is None:
         raise ValueError("q or k is needed")

@@ -263,3 +263,145 @@ def test_reference_tables_by_hand():
     assert got[1].tolist() == [33, 16, 2] and got[2].tolist() == [0, 13, 13, 15]
     assert got[3].tolist() == [5 * 16 + 4 + i for i in range(12)] + [48, 16, 17, -1, -1]
     assert got[4].tolist() == list(range(20, 33)) + [0, 1, 0, 0] and got[5:] == (2, 0)
+
+
+class FakeTensor:
+    """What the marshalling extension looks at of a tensor."""
+
+    def __init__(self, dtype, shape, ptr, stride=None, dev=0, contiguous=True):
+        self.dtype, self.shape, self._ptr, self._dev, self._c = dtype, tuple(shape), ptr, dev, contiguous
+        st = []
+        n = 1
+        for d in reversed(shape):
+            st.append(n)
+            n *= d
+        self._stride = tuple(reversed(st)) if stride is None else stride
+
+    def get_device(self):
+        return self._dev
+
+    def data_ptr(self):
+        return self._ptr
+
+    def is_contiguous(self):
+        return self._c
+
+    def stride(self):
+        return self._stride
+
+
+@pytest.fixture
+def marshalled(lib):
+    """The extension with recording stand-ins for the five C functions; yields (module, calls)."""
+    if q4._fast is None:
+        pytest.skip("the marshalling extension is not built here")
+    calls = []
+    P, i, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
+    protos = dict(
+        write=ctypes.CFUNCTYPE(i, *[i] * 6, P, ll, P, ll, P, P, P, P),
+        read=ctypes.CFUNCTYPE(i, *[i] * 6, P, P, P, ll, P, ll, P, P),
+        decode=ctypes.CFUNCTYPE(i, P, P, P, P, P, ctypes.c_float, i, P, P, P, P),
+        tables=ctypes.CFUNCTYPE(i, *[i] * 6, *[P] * 11),
+        rope=ctypes.CFUNCTYPE(i, *[i] * 6, ctypes.POINTER(i), i, i, ctypes.c_float, i, P, ll, P, ll,
+                              P, P, ll, P, ll, P))
+    keep = []
+    for name, proto in protos.items():
+        def fn(*a, name=name):
+            if name == "rope":
+                a = a[:6] + ([a[6][j] for j in range(a[5])],) + a[7:]
+            if name == "decode":
+                a = (ctypes.string_at(a[0], ctypes.sizeof(q4.pa_q4_plan_t)),) + a[1:]
+            calls.append((name, a))
+            return 3 if name == "read" else 0
+        keep.append(proto(fn))
+    T = (torch.float16, torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8)
+    q4._fast.setup(T, tuple(ctypes.cast(f, P).value for f in keep), lambda: 0, lambda d: 4096 + d)
+    yield q4._fast, calls
+    q4._load_fast(lib)  # the real functions again
+
+
+def test_marshalling_of_the_usual_calls(marshalled):
+    fast, calls = marshalled
+    f16, i32, i64 = torch.float16, torch.int32, torch.int64
+    k = FakeTensor(f16, (5, 2, 128), 1 << 20, stride=(1024, 128, 1))
+    v = FakeTensor(f16, (5, 2, 128), 2 << 20)
+    sl, c = FakeTensor(i64, (5,), 3 << 20), FakeTensor(torch.uint8, (9, 2, 2560), 1 << 40)
+    assert fast.q4_write(k, v, sl, c) == 0
+    assert calls.pop() == ("write", (5, 2, 128, 16, 9, 0, 1 << 20, 1024, 2 << 20, 256, 3 << 20,
+                                     1 << 40, None, 4096))
+    assert fast.q4_read(c, sl, k, v) == 3  # the status comes back
+    assert calls.pop() == ("read", (5, 2, 128, 16, 9, 0, 1 << 40, 3 << 20, 1 << 20, 1024, 2 << 20,
+                                    256, None, 4096))
+    plan = _plan(dtype=1)
+    bf = torch.bfloat16
+    q, out = FakeTensor(bf, (2, 8, 128), 16), FakeTensor(bf, (2, 8, 128), 32)
+    bt, cl = FakeTensor(i32, (2, 16), 48), FakeTensor(i32, (2,), 64)
+    cache = FakeTensor(torch.uint8, (64, 2, 2560), 80)
+    lse, ws = FakeTensor(torch.float32, (2, 8), 96), FakeTensor(torch.uint8, (plan.workspace_bytes,), 112)
+    assert fast.q4_decode(plan, q, cache, bt, cl, 0.5, 7, out, lse, ws) == 0
+    assert calls.pop() == ("decode", (bytes(plan), 16, 80, 48, 64, 0.5, 7, 32, 96, 112, 4096))
+    t = [FakeTensor(i32, (3,), 16 * j) for j in (1, 2)] + [FakeTensor(i32, (11,), 48), 77,
+         FakeTensor(i32, (3, 6), 64), FakeTensor(i32, (3,), 80), FakeTensor(i32, (4,), 96),
+         FakeTensor(i64, (20,), 112), FakeTensor(i32, (20,), 128), FakeTensor(i32, (1,), 144)]
+    assert fast.extend_tables(*t) == 0
+    assert calls.pop() == ("tables", (3, 6, 16, 77, 11, 20, *[16 * j for j in range(1, 10)], None, 4096))
+    f32 = torch.float32
+    q, k = FakeTensor(f32, (5, 4, 64), 16), FakeTensor(f32, (5, 2, 64), 32, stride=(512, 64, 1))
+    o = FakeTensor(f32, (5, 2, 64), 48)
+    pos = FakeTensor(i32, (3, 5), 64)
+    assert fast.rope_axes(q, k, pos, (4, 6, 6), 1e4, None, o, 32, True, False) == 0
+    assert calls.pop() == ("rope", (5, 4, 2, 64, 32, 3, [4, 6, 6], 1, 0, 1e4, 2, 16, 256, 32, 512, 64,
+                                    16, 256, 48, 128, 4096))
+    assert fast.rope_axes(q, k, pos, (4, 6, 6), 1e4, None, None, None, False, True) == 0
+    assert calls.pop()[1][4:9] == (64, 3, [4, 6, 6], 0, 1)
+    assert not calls
+
+
+def test_marshalling_leaves_everything_else_alone(marshalled):
+    fast, calls = marshalled
+    f16, i32, i64 = torch.float16, torch.int32, torch.int64
+    ok = dict(k=FakeTensor(f16, (5, 2, 128), 16), v=FakeTensor(f16, (5, 2, 128), 32),
+              sl=FakeTensor(i64, (5,), 48), c=FakeTensor(torch.uint8, (9, 2, 2560), 64))
+    for name, bad in [("k", FakeTensor(f16, (5, 2, 128), 16, dev=1)), ("k", None), ("k", 3),
+                      ("k", FakeTensor(f16, (5, 256), 16)), ("k", FakeTensor(i32, (5, 2, 128), 16)),
+                      ("k", FakeTensor(f16, (5, 2, 128), 16, stride=(256, 1, 2))),
+                      ("v", FakeTensor(f16, (5, 2, 128), 16, stride=(64, 640, 1))),
+                      ("v", FakeTensor(torch.bfloat16, (5, 2, 128), 16)),
+                      ("v", FakeTensor(f16, (4, 2, 128), 16)),
+                      ("sl", FakeTensor(i32, (5,), 48)), ("sl", FakeTensor(i64, (6,), 48)),
+                      ("sl", FakeTensor(i64, (5,), 48, contiguous=False)),
+                      ("sl", FakeTensor(i64, (5,), 48, dev=-1)),
+                      ("c", FakeTensor(torch.uint8, (9, 3, 2560), 64)),
+                      ("c", FakeTensor(torch.uint8, (9, 2, 1280), 64)),
+                      ("c", FakeTensor(torch.uint8, (1 << 32, 2, 2560), 64)),
+                      ("c", FakeTensor(torch.int8, (9, 2, 2560), 64))]:
+        a = dict(ok, **{name: bad})
+        assert fast.q4_write(a["k"], a["v"], a["sl"], a["c"]) is None, (name, bad)
+        assert fast.q4_read(a["c"], a["sl"], a["k"], a["v"]) is None, (name, bad)
+    plan = _plan()
+    base = [plan, FakeTensor(f16, (2, 8, 128), 16), FakeTensor(torch.uint8, (64, 2, 2560), 32),
+            FakeTensor(i32, (2, 16), 48), FakeTensor(i32, (2,), 64), 0.5, 0,
+            FakeTensor(f16, (2, 8, 128), 80), FakeTensor(torch.float32, (2, 8), 96),
+            FakeTensor(torch.uint8, (plan.workspace_bytes,), 112)]
+    assert fast.q4_decode(*base) == 0
+    calls.clear()
+    for i, bad in [(0, object()), (0, b"x" * 8), (1, FakeTensor(f16, (3, 8, 128), 16)), (5, 1), (5, "a"),
+                   (6, 0.0), (6, 1 << 40), (6, True), (8, FakeTensor(f16, (2, 8), 96)),
+                   (9, FakeTensor(torch.uint8, (plan.workspace_bytes - 1,), 112)),
+                   (9, FakeTensor(torch.uint8, (1, plan.workspace_bytes), 112)),
+                   (2, FakeTensor(torch.uint8, (63, 2, 2560), 32))]:
+        a = list(base)
+        a[i] = bad
+        assert fast.q4_decode(*a) is None, (i, bad)
+    assert fast.q4_decode(*base[:9]) is None and fast.extend_tables(1, 2) is None
+    f32 = torch.float32
+    r = [FakeTensor(f32, (5, 4, 64), 16), FakeTensor(f32, (5, 2, 64), 32), FakeTensor(i32, (3, 5), 64),
+         (4, 6, 6), 1e4, None, None, None, False, False]
+    for i, bad in [(0, None), (1, None), (1, FakeTensor(f32, (4, 2, 64), 32)),
+                   (1, FakeTensor(f16, (5, 2, 64), 32)), (2, FakeTensor(i32, (2, 5), 64)),
+                   (3, [4, 6, 6]), (3, (1, 2, 3, 4, 5)), (3, (4.0, 6, 6)), (3, ()), (4, 10000),
+                   (5, FakeTensor(f32, (5, 2, 64), 16)), (7, 32.0), (8, 1), (9, None)]:
+        a = list(r)
+        a[i] = bad
+        assert fast.rope_axes(*a) is None, (i, bad)
+    assert not calls

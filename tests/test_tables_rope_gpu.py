@@ -347,3 +347,36 @@ def test_prefill_and_decode_steps_together(dtype, D, graph):
         check((out.double().cpu().numpy(), lse.double().cpu().numpy(), 0),
               ref.decode(rows[last, :Hq], cache_h, hbt, hl, D ** -0.5, 0, dtype))
         bt, lens, used = hbt, hl.astype(np.int64), used + taken
+
+
+def test_calls_without_the_marshalling_extension(monkeypatch):
+    """The same calls through the Python checks alone give the same bits."""
+    if q4._fast is None:
+        pytest.skip("the marshalling extension is not built here")
+    fast = q4._fast
+    g = np.random.default_rng(50)
+    D, H, n = 128, 2, 40
+    rows = to_t(kv_values(g, (n, 3 * H, D), "f16"), "f16")
+    results = []
+    for ext in (fast, None):
+        monkeypatch.setattr(q4, "_fast", ext)
+        past, new = i32([0, 0]), i32([33, 7])
+        bt, lens, starts, taken = i32(np.full((2, 4), -1)), i32([0, 0]), i32([0, 0, 0]), i32([0])
+        slots, pos = torch.zeros(n, dtype=torch.int64, device="cuda"), i32(np.zeros(n))
+        pa.pa_extend_tables(past, new, i32([5, 1, 4, 2]), 6, bt, lens, starts, slots, pos, taken)
+        x = rows.clone()
+        pa.pa_rope_axes(x[:, :H], x[:, H:2 * H], pos.expand(2, -1).contiguous(), (32, 32), 1e4)
+        cache = pa.new_q4_cache(6, H, D)
+        pa.pa_q4_write(x[:, H:2 * H], x[:, 2 * H:], slots, cache)
+        k, v = torch.empty(n, H, D, dtype=torch.float16, device="cuda"), torch.empty(
+            n, H, D, dtype=torch.float16, device="cuda")
+        pa.pa_q4_read(cache, slots, k, v)
+        plan = pa.pa_q4_plan(2, H, H, D, 16, 6, 4, 64)
+        q = x[[32, 39], :H].contiguous()
+        out, lse = torch.empty_like(q), torch.empty(2, H, device="cuda")
+        pa.pa_q4_decode(plan, q, cache, bt, lens, 0.1, 0, out, lse, pa.new_workspace(plan, "cuda"))
+        results.append([t.clone() for t in (bt, lens, starts, slots, pos, taken, x, cache, k, v, out,
+                                            lse)])
+    assert int(results[0][5]) == 4
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
