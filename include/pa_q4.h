@@ -111,7 +111,8 @@ typedef struct pa_q4_plan {
     int num_sms;            /* SM count the plan was made for */
     int heads_per_cta;      /* query heads one CTA serves (a divisor of Hq / Hkv, at most 8) */
     int ctas_per_group;     /* CTAs that share the batch's pages of one KV head and head
-                               chunk; a caller may lower it (to 1 or more) */
+                               chunk; without clusters a caller may lower it (to 1 or
+                               more) */
     int ctas;               /* CTAs in all */
     size_t workspace_bytes; /* device workspace of pa_q4_decode */
     int ctrl_bytes;         /* its leading bytes that must be zero before the first call
@@ -121,6 +122,10 @@ typedef struct pa_q4_plan {
                                first copy expects this many bytes more than it carries,
                                so the bounded wait on it runs out after 1 s
                                (PA_DEVERR_TIMEOUT, NaN rows) */
+    int cluster;            /* 2 to 8: so many CTAs share each sequence as a thread-block
+                               cluster and merge in it (ctas_per_group is batch times
+                               that); 0: the batch's pages are cut into equal ranges.  A
+                               caller may set 0 */
 } pa_q4_plan_t;
 
 /*

@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "pa_q4_attend.cuh"
 
@@ -14,7 +15,9 @@ namespace pa {
     extern template cudaError_t launch_q4_attend_d<D, __half>(const Q4AttendParams&, dim3,       \
                                                               cudaStream_t);                     \
     extern template cudaError_t launch_q4_attend_d<D, __nv_bfloat16>(const Q4AttendParams&, dim3, \
-                                                                     cudaStream_t);
+                                                                     cudaStream_t);              \
+    extern template cudaError_t q4_attend_clusters<D, __half>(int, int, int*);                   \
+    extern template cudaError_t q4_attend_clusters<D, __nv_bfloat16>(int, int, int*);
 PA_Q4_EXTERN(64)
 PA_Q4_EXTERN(96)
 PA_Q4_EXTERN(128)
@@ -23,6 +26,8 @@ PA_Q4_EXTERN(256)
 
 constexpr int kQ4MaxBatch = 4096;
 constexpr int kQ4MinRun = 2;    // pages of a warp, at least
+constexpr int kQ4MaxCluster = 8;  // (the largest that every launch may have)
+constexpr int kQ4ClusterExtra = 12;  // pages of head_dim 128, see pa_q4_plan
 constexpr int kQ4KernelRows = 4;  // partials per sequence beyond which a kernel merges
 
 // Workspace: [control block | counters of the partials left, groups x B | run
@@ -55,6 +60,46 @@ static int q4_ctas_per_sm(int D, int B) {
         default: smem = Q4Cfg<256>::smem(B), most = Q4Cfg<256>::kMinBlocks; break;
     }
     return std::max(1, std::min(most, 228 * 1024 / (smem + 1024 + 128)));
+}
+
+// Clusters of c CTAs held at once: the current device's answer (asked for once
+// per device and CTAs per SM), or for a plan made for an SM count a low estimate
+// (a cluster must lie within one GPC, so up to a third of the slots stay unused).
+static long long q4_clusters_held(bool this_device, int D, int dtype, int batch, int c,
+                                  long long slots) {
+    constexpr int kMaxDevices = 64, kMaxPerSm = 8;
+    static std::atomic<int> cache[kMaxDevices][4][2][kMaxPerSm][kQ4MaxCluster];  // value + 1
+    const long long estimate = slots * 2 / (3 * c);
+    const int per_sm = q4_ctas_per_sm(D, batch);
+    int dev = 0;
+    if (!this_device || per_sm > kMaxPerSm) return estimate;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return estimate;
+    }
+    const int di = D == 64 ? 0 : D == 96 ? 1 : D == 128 ? 2 : 3;
+    const int ti = dtype == PA_DTYPE_BF16 ? 1 : 0;
+    std::atomic<int>& slot = cache[dev][di][ti][per_sm - 1][c - 1];
+    const int known = slot.load();
+    if (known > 0) return known - 1;
+    int held = 0;
+    cudaError_t e;
+#define PA_HELD(DD)                                                  \
+    e = ti ? q4_attend_clusters<DD, __nv_bfloat16>(c, batch, &held) \
+           : q4_attend_clusters<DD, __half>(c, batch, &held)
+    switch (D) {
+        case 64: PA_HELD(64); break;
+        case 96: PA_HELD(96); break;
+        case 128: PA_HELD(128); break;
+        default: PA_HELD(256); break;
+    }
+#undef PA_HELD
+    if (e != cudaSuccess || held < 0) {
+        cudaGetLastError();
+        return estimate;
+    }
+    slot.store(held + 1);
+    return held;
 }
 
 // What a plan's shapes must satisfy; the automatic fields are checked by the caller.
@@ -107,7 +152,8 @@ int pa_q4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
     if (g % nchunk != 0) return PA_ERR_UNSUPPORTED;
     const long long groups = (long long)num_kv_heads * nchunk;
     if (groups > 65535) return PA_ERR_UNSUPPORTED;
-    if (p.num_sms == 0) {
+    const bool this_device = p.num_sms == 0;
+    if (this_device) {
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&p.num_sms, cudaDevAttrMultiProcessorCount, dev) !=
@@ -126,11 +172,35 @@ int pa_q4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
     const long long pages = std::max(1ll, (long long)std::max(1, batch) * span);
     const long long slots = (long long)p.num_sms * q4_ctas_per_sm(head_dim, batch);
     long long x = std::max(1ll, (slots - slots / 64) / groups);
-    if (span <= kQ4Short && batch <= x)
+    if (span <= q4_short(head_dim) && batch <= x)
         x = std::max(1, batch);  // one for each sequence
     else
         x = std::min(x, std::max<long long>(batch, (pages + kWarps * kQ4MinRun - 1) /
                                                        (kWarps * kQ4MinRun)));
+    // A cluster for each sequence, which saves the partials' way through the L2
+    // (2 to 4 us) but gives the CTAs of the longest sequence more pages than equal
+    // ranges do: the largest cluster of which one wave holds all, with a page for
+    // every warp, where that is at most kQ4ClusterExtra pages more, twice that
+    // with several sequences (whose borders equal ranges cut twice).  Clusters
+    // against equal ranges, head_dim 128, 8 KV heads, at so many pages more: one
+    // sequence -1 6.0 and 6.9 us, 8 7.5 and 8.1, 12 8.0 and 7.9, 23 9.3 and 8.4;
+    // 4 sequences -10 8.0 and 11.4, 13 12.2 and 13.2, 18 13.4 and 14.6, 27 14.9 and
+    // 15.5, 36 18.1 and 17.2; one of 16 longer than the rest 11.7 and 12.9.  At the
+    // limits head_dim 64 (32, 39 pages) 8.5 and 9.7, 10.1 and 10.3.  Clusters that
+    // one wave does not hold cost 5 to 10 us (16 sequences of 1000 tokens by 4 CTAs
+    // 19.3, by 3 12.2, equal ranges 15.4).
+    if (batch > 0 && span > q4_short(head_dim)) {
+        int c = std::min(kQ4MaxCluster, (span + kWarps - 1) / kWarps);
+        while (c > 1 && (groups * batch * c > slots ||
+                         q4_clusters_held(this_device, head_dim, dtype, batch, c, slots) <
+                             groups * batch))
+            --c;
+        const long long extra = (span + c - 1) / c - (pages + x - 1) / x;
+        if (c > 1 && extra * head_dim <= kQ4ClusterExtra * 128 * (batch > 1 ? 2 : 1)) {
+            p.cluster = c;
+            x = (long long)c * batch;
+        }
+    }
     p.ctas_per_group = (int)x;
     p.ctas = (int)std::min<long long>(x * groups, INT_MAX);
     const Q4WsLayout wl = q4_ws_layout(batch, head_dim, groups, p.ctas_per_group);
@@ -150,6 +220,8 @@ int pa_q4_decode(const pa_q4_plan_t* plan, const void* q, const void* cache,
     const int g = plan->num_q_heads / plan->num_kv_heads;
     const int G = plan->heads_per_cta, X = plan->ctas_per_group, D = plan->head_dim;
     if (G < 1 || G > kMaxHeadsPerCta || g % G != 0 || X < 1 || X > (1 << 20) ||
+        (plan->cluster != 0 && (plan->cluster < 2 || plan->cluster > kQ4MaxCluster ||
+                                (long long)plan->cluster * plan->batch != X)) ||
         window != plan->window || plan->test_stall_bytes < 0 || plan->test_stall_bytes > 4096)
         return PA_ERR_INVALID_ARG;
     const long long groups = (long long)plan->num_kv_heads * (g / G);
@@ -176,11 +248,13 @@ int pa_q4_decode(const pa_q4_plan_t* plan, const void* q, const void* cache,
     p.ws_ml = reinterpret_cast<float*>(ws + wl.ml_off);
     p.err = reinterpret_cast<unsigned*>(ws);
     p.ws_info = reinterpret_cast<int*>(ws + wl.info_off);
-    // A sequence of a batch of B leaves about X / B partials: beyond
-    // kQ4KernelRows a kernel of its own gathers them (limits of 4, 8 and 20: 4
-    // sequences of 1000 tokens 11.3, 12.7 and 12.7 us, 8 ragged ones up to 4000
-    // 15.0, 15.9 and 16.0, one of 2000 7.9, 7.9 and 9.8).
-    p.merge_kernel = X > kQ4KernelRows * plan->batch ? 1 : 0;
+    p.cluster = plan->cluster;
+    // A sequence of a batch of B cut into equal ranges leaves about X / B
+    // partials: beyond kQ4KernelRows a kernel of its own gathers them.  By the last
+    // CTA to leave one, and by the kernel: 16 sequences of 20000 tokens (3.5 each)
+    // 78.9 and 81.8 us, 8 ragged ones up to 30000 (7) 36.6 and 34.8, 4 of 9000 (14)
+    // 21.2 and 18.7.
+    p.merge_kernel = !p.cluster && X > kQ4KernelRows * plan->batch ? 1 : 0;
     p.counters = reinterpret_cast<unsigned*>(ws + wl.ctr_off);
     p.B = plan->batch;
     p.Hq = plan->num_q_heads;

@@ -30,11 +30,15 @@
 //  * Maximum.  m is raised, and O rescaled, only when a score exceeds it by
 //    more than 8 in the log2 domain (weights then stay below 2^8, far from
 //    fp16's limit); so most pages need no shuffle, just one vote.
-//  * Split.  Where every sequence is short (kQ4Short pages) and there are CTAs
-//    enough, each has one to itself.  Otherwise the pages the batch attends, all
-//    sequences end to end, are cut into equal ranges, one per CTA of the group,
-//    whatever the lengths; a range may hold many short sequences or part of a
-//    long one.  At a sequence's end the warps' states meet in shared memory.  A
+//  * Split.  Where every sequence is short (q4_short pages) and there are CTAs
+//    enough, each has one to itself.  Where clusters of CTAs, one per sequence,
+//    fit the GPU at once and leave no CTA many pages more than equal ranges do
+//    (pa_q4_plan has the figures), a cluster shares a sequence evenly and merges
+//    its CTAs' states through distributed shared memory: 4 sequences of 1000
+//    tokens 11.4 -> 7.8 us.  Otherwise the pages the batch attends, all sequences
+//    end to end, are cut into equal ranges, one per CTA of the group, whatever the
+//    lengths; a range may hold many short sequences or part of a long one.  At a
+//    sequence's end the warps' states meet in shared memory.  A
 //    sequence inside the range is written; one cut by a border leaves a partial
 //    (o, maximum, sum) per CTA in the workspace.  Who merges a sequence's
 //    partials, always in order: the last CTA to leave one, or, in plans where a
@@ -56,8 +60,10 @@ namespace pa {
 #define PA_INLINE_LAMBDA __attribute__((always_inline))
 
 // Pages up to which a sequence goes to one CTA where there is one for each: 40
-// sequences of up to 40 tokens 13.2 -> 4.3 us, one of 256 tokens 5.5 -> 4.6.
-constexpr int kQ4Short = 24;
+// sequences of up to 40 tokens 13.2 -> 4.3 us.  Against clusters at 16 and 24
+// pages: D 64 ragged 5.0 and 6.0, 5.7 and 6.1 us, D 128 5.4 and 6.0, 6.2 and 5.8
+// (ragged 7.0 and 7.4), D 256 7.5 and 7.3, 9.0 and 7.5.
+constexpr int q4_short(int D) { return D == 256 ? 16 : 24; }
 constexpr int kQ4StagedPages = 512;  // page ids a CTA stages at a time
 
 struct Q4AttendParams {
@@ -75,6 +81,7 @@ struct Q4AttendParams {
     int B, Hq, Hkv, g, num_pages, maxp, max_ctx, window;
     int nchunk, G, X;
     int merge_kernel;  // 1: q4_merge_kernel merges, 0: the last to leave a partial
+    int cluster;       // > 0: CTAs of a sequence's cluster (X = B clusters of them)
     int stall_tx;   // test hook
     float scale_log2;
 };
@@ -99,6 +106,7 @@ struct Q4Cfg {
     // sequence's end every warp owns a quarter of them and gets the other
     // warps' shares through shared memory.
     static constexpr int kUnits = 2 * Q4Layout<D>::kWords;
+    static_assert(kUnits * 512 <= kRingBytes, "a cluster's CTA leaves its state in the ring");
     static constexpr int kXBytes = kUnits * (kWarps - 1) * 512;
     static constexpr int kSmemBytes = kRingBytes + kQBytes + kXBytes + kQ4StagedPages * 4 +
                                       kWarps * kMaxHeadsPerCta * 3 * 4 + kWarps * kStages * 8;
@@ -242,6 +250,36 @@ __device__ __forceinline__ void q4_store_unit(const Q4AttendParams& p, int b, in
                               q4_v_dim<D>(lane >> 2, u >> 1)) = r;
 }
 
+// A cluster's barrier, and reads of a peer's shared memory.
+__device__ __forceinline__ void q4_cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t q4_peer(const void* p, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float4 q4_ld_peer4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float2 q4_ld_peer2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 // Log-sum-exp merge of rows i, i + step, ... for this lane's heads and dims of
 // NU units, u, u + du, ...: NR rows of them in flight.
 struct Q4Merge {
@@ -371,7 +409,10 @@ __global__ void __launch_bounds__(kQ4MergeWarps * 32) q4_merge_kernel(const Q4At
     q4_finish_unit<D, T>(p, b, h0, u, lane, top, sum, o);
 }
 
-template <int D, typename T>
+// kCluster: X is B clusters of p.cluster CTAs, one for each sequence (instances
+// of their own: with the merge of a cluster in the same code, bf16's spilled 32
+// bytes and 64 ragged sequences took 50.3 us for 49.3).
+template <int D, typename T, bool kCluster>
 __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     q4_attend_kernel(const Q4AttendParams p) {
     using L = Q4Layout<D>;
@@ -395,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     int* s_page0 = s_base + p.B + 1;
     int* s_len = s_page0 + p.B;
     __shared__ int s_red[kWarps];
+    __shared__ float2 s_sum[kMaxHeadsPerCta];  // cluster: this CTA's maximum and sum of each head
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -417,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     // its sequence.  A thread sums a run of sequences, a scan over the CTA
     // joins the runs.
     const int tid = threadIdx.x;
-    // Returns whether a sequence is longer than kQ4Short pages.
+    // Returns whether a sequence is longer than q4_short pages.
     auto scan = [&](bool one, int len) {  // one: B <= kThreads, and len is sequence tid's length
         const int per = one ? 1 : (p.B + kThreads - 1) / kThreads;
         const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
@@ -449,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
             at += n;
         }
         if (tid == kThreads - 1) s_base[p.B] = inc;
-        return __syncthreads_or(longest > kQ4Short) != 0;
+        return __syncthreads_or(longest > q4_short(D)) != 0;
     };
     // Sequence of page f: the last b with s_base[b] <= f (behind any empty ones
     // that share that number).
@@ -468,6 +510,15 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     int range, lo, hi, b;
     auto locate = [&](bool any_long) {
         const int total = s_base[p.B];
+        if constexpr (kCluster) {  // an even share of a sequence
+            b = blockIdx.x / p.cluster;
+            const int first = s_base[b], n = s_base[b + 1] - first;
+            range = max(NP, ((n + p.cluster - 1) / p.cluster + NP - 1) / NP * NP);
+            const int at = (int)(blockIdx.x - b * p.cluster) * range;
+            lo = first + min(n, at);
+            hi = first + min(n, at + range);
+            return;
+        }
         if (!any_long && p.B <= p.X) {  // a CTA for each sequence
             range = max(1, total);      // (no border cuts anything)
             b = min((int)blockIdx.x, p.B - 1);
@@ -539,7 +590,8 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         for (int i = tid; i < G * D / 2; i += kThreads) row[i] = fill;
         if (tid < G) p.lse[(size_t)e * p.Hq + h0 + tid] = valid ? -INFINITY : NAN;
     }
-    if (lo >= hi) return;
+    // (A cluster whose sequence attends anything needs all its CTAs below.)
+    if (lo >= hi && (!kCluster || s_base[b + 1] == s_base[b])) return;
 
     // ---- Registers of a sequence: q as the mma's B operand, O^T, the sums.
     // q, word w: pairs (P, P + 4) of its 8 dims, P = 0..3
@@ -779,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     int cut_head = -1, cut_tail = -1, head_count = 0;
     unsigned* counters = p.counters + (size_t)group * p.B;
     auto end_sequence = [&]() PA_INLINE_LAMBDA {
-        const bool cut = s_base[b] < lo || s_base[b + 1] > hi;
+        const bool cut = !kCluster && (s_base[b] < lo || s_base[b + 1] > hi);
         const size_t row = row0 + (s_base[b] > lo ? 1 : 0);
         if (cut) (s_base[b] > lo ? cut_tail : cut_head) = b;
 #pragma unroll
@@ -833,11 +885,14 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
                 const float4 v = xbuf[(u * (kWarps - 1) + x) * 32 + lane];
                 o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
             }
-            if (!cut) {
+            if (!cut && !kCluster) {
                 q4_store_unit<D, T>(p, b, h0, u, lane, o, inv[k]);
             } else {
                 o.x *= inv[k], o.y *= inv[k], o.z *= inv[k], o.w *= inv[k];
-                reinterpret_cast<float4*>(p.ws_o)[(row * Cfg::kUnits + u) * 32 + lane] = o;
+                if (kCluster)  // (the ring is idle: this is the range's end)
+                    reinterpret_cast<float4*>(ring)[u * 32 + lane] = o;
+                else
+                    reinterpret_cast<float4*>(p.ws_o)[(row * Cfg::kUnits + u) * 32 + lane] = o;
             }
         }
         if (warp == 0 && g == 0) {
@@ -845,7 +900,9 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
             for (int k = 0; k < 2; ++k) {
                 const int h = 2 * t + k;
                 if (h >= G) continue;
-                if (!cut)
+                if (kCluster)
+                    s_sum[h] = make_float2(top[k], sum[k]);
+                else if (!cut)
                     p.lse[(size_t)b * p.Hq + h0 + h] =
                         (top[k] + log2f(sum[k])) * 0.69314718055994531f;
                 else
@@ -987,6 +1044,51 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
             if (s_base[b] >= c1) break;
         }
     }
+    if constexpr (kCluster) {
+        // Every CTA's state is in its ring and s_sum (nothing attended: a sum of
+        // 0); each warp of the cluster merges units of all of them, whose reads go
+        // out together.  The second barrier keeps the shared memory until all
+        // have read it.
+        if (lo >= hi && tid < kMaxHeadsPerCta) s_sum[tid] = make_float2(-INFINITY, 0.f);
+        __syncthreads();
+        q4_cluster_barrier();
+        const int rank = blockIdx.x - b * p.cluster;
+        const int rows = (s_base[b + 1] - s_base[b] + range - 1) / range;
+        for (int u = rank * kWarps + warp; u < Cfg::kUnits; u += p.cluster * kWarps) {
+            const int h = 2 * t + (u & 1);
+            float m = -INFINITY, sum = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            constexpr int N = 8;  // peers in flight
+            for (int r0 = 0; r0 < rows; r0 += N) {
+                float2 ml[N];
+                float4 v[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int r = min(r0 + i, rows - 1);
+                    ml[i] = q4_ld_peer2(q4_peer(s_sum + h, r));
+                    v[i] = q4_ld_peer4(q4_peer(ring + (u * 32 + lane) * 16, r));
+                    if (r0 + i >= rows) ml[i] = make_float2(-INFINITY, 0.f);
+                }
+                float top = m;
+#pragma unroll
+                for (int i = 0; i < N; ++i) top = fmaxf(top, ml[i].x);
+                const float f = m == -INFINITY ? 0.f : ex2(m - top);
+                sum *= f;
+                o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float w = ml[i].y == 0.f ? 0.f
+                                                   : (ml[i].y != ml[i].y ? NAN : ex2(ml[i].x - top) * ml[i].y);
+                    if (w == 0.f) continue;
+                    sum += w;
+                    o.x += w * v[i].x, o.y += w * v[i].y, o.z += w * v[i].z, o.w += w * v[i].w;
+                }
+                m = top;
+            }
+            q4_finish_unit<D, T>(p, b, h0, u, lane, m, sum, o);
+        }
+        q4_cluster_barrier();
+    }
     // After a timeout: copies still on their way must not outlive the CTA's
     // shared memory.
     for (; dead && pending > 0; --pending) {
@@ -996,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
             out_phase ^= 1;
         }
     }
-    if (p.merge_kernel) return;
+    if (kCluster || p.merge_kernel) return;
     // (here, behind the loop: in it the merge's loads in flight made the
     // accumulators spill, 64 ragged sequences 51 -> 88 us)
     if (cut_head < 0 && cut_tail < 0) return;
@@ -1020,6 +1122,32 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     }
 }
 
+// The kernel's shared memory limit raised to what the largest batch asks for.
+template <int D, typename T, bool kCluster>
+cudaError_t q4_attend_attributes() {
+    return cudaFuncSetAttribute(q4_attend_kernel<D, T, kCluster>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, Q4Cfg<D>::smem(4096));
+}
+
+// Clusters of c CTAs that the current device holds at once.
+template <int D, typename T>
+cudaError_t q4_attend_clusters(int c, int batch, int* held) {
+    cudaError_t e = q4_attend_attributes<D, T, true>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Q4Cfg<D>::smem(batch);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(held, q4_attend_kernel<D, T, true>, &cfg);
+}
+
 template <int D, typename T>
 cudaError_t launch_q4_attend_d(const Q4AttendParams& p, dim3 grid, cudaStream_t stream) {
     const int smem = Q4Cfg<D>::smem(p.B);
@@ -1031,8 +1159,8 @@ cudaError_t launch_q4_attend_d(const Q4AttendParams& p, dim3 grid, cudaStream_t 
     if (e != cudaSuccess) return e;
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
     if (!bit || !(done.load() & bit)) {
-        e = cudaFuncSetAttribute(q4_attend_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Q4Cfg<D>::smem(4096));
+        e = q4_attend_attributes<D, T, false>();
+        if (e == cudaSuccess) e = q4_attend_attributes<D, T, true>();
         if (e != cudaSuccess) return e;
         done.fetch_or(bit);
     }
@@ -1041,12 +1169,17 @@ cudaError_t launch_q4_attend_d(const Q4AttendParams& p, dim3 grid, cudaStream_t 
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, q4_attend_kernel<D, T>, p);
+    cfg.numAttrs = p.cluster ? 2 : 1;
+    e = p.cluster ? cudaLaunchKernelEx(&cfg, q4_attend_kernel<D, T, true>, p)
+                  : cudaLaunchKernelEx(&cfg, q4_attend_kernel<D, T, false>, p);
     if (e != cudaSuccess || !p.merge_kernel) return e;
     cfg.gridDim = dim3(p.B, grid.y, Q4Cfg<D>::kUnits);
     cfg.blockDim = dim3(kQ4MergeWarps * 32);

@@ -5,4 +5,6 @@ namespace pa {
 template cudaError_t launch_q4_attend_d<128, __half>(const Q4AttendParams&, dim3, cudaStream_t);
 template cudaError_t launch_q4_attend_d<128, __nv_bfloat16>(const Q4AttendParams&, dim3,
                                                            cudaStream_t);
+template cudaError_t q4_attend_clusters<128, __half>(int, int, int*);
+template cudaError_t q4_attend_clusters<128, __nv_bfloat16>(int, int, int*);
 }  // namespace pa

@@ -51,6 +51,7 @@ class pa_q4_plan_t(ctypes.Structure):
         ("workspace_bytes", ctypes.c_size_t),
         ("ctrl_bytes", ctypes.c_int),
         ("test_stall_bytes", ctypes.c_int),
+        ("cluster", ctypes.c_int),
     ]
 
     def as_dict(self):

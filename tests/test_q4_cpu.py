@@ -30,7 +30,7 @@ def test_plan_struct_layout_matches_header():
     fields = re.findall(r"\b(?:int|size_t|float)\s+([a-z_0-9]+)\s*;", body)
     assert fields == [f for f, _ in q4.pa_q4_plan_t._fields_]
     assert q4.pa_q4_plan_t.workspace_bytes.offset == 56
-    assert ctypes.sizeof(q4.pa_q4_plan_t) == 72
+    assert ctypes.sizeof(q4.pa_q4_plan_t) == 80
 
 
 def test_page_bytes():
@@ -154,7 +154,9 @@ def test_decode_checks_return_before_launch(lib):
                              ("ctrl_bytes", 256, IA), ("test_stall_bytes", 5000, IA),
                              ("num_q_heads", 9, IA), ("head_dim", 100, binding.PA_ERR_UNSUPPORTED),
                              ("max_context_len", 1 << 20, IA),
-                             ("ctas_per_group", plan.ctas_per_group + 1, IA)]:
+                             ("ctas_per_group", plan.ctas_per_group + 1, IA),
+                             ("cluster", 1, IA), ("cluster", 9, IA), ("cluster", -2, IA),
+                             ("cluster", plan.ctas_per_group, IA)]:
         bad = q4.pa_q4_plan_t.from_buffer_copy(plan)
         setattr(bad, field, value)
         assert call(_0=ctypes.byref(bad)) == st, field
@@ -405,3 +407,17 @@ def test_marshalling_leaves_everything_else_alone(marshalled):
         a[i] = bad
         assert fast.rope_axes(*a) is None, (i, bad)
     assert not calls
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_plan_clusters(D, dtype):
+    """Clusters share sequences of medium length; short, very long and many ones go without."""
+    for batch, tokens, want in [(1, 128, False), (1, 1000, True), (4, 1000, True),
+                                (2, 100000, False), (400, 1000, False), (0, 1000, False)]:
+        plan = q4.pa_q4_plan(batch, 16, 4, D, 16, 1 << 16, 6250, tokens, 0, 152, dtype)
+        assert (plan.cluster != 0) == want, (batch, tokens)
+        if want:
+            assert 2 <= plan.cluster <= 8
+            assert plan.ctas_per_group == plan.cluster * batch
+            assert plan.ctas == plan.ctas_per_group * 4

@@ -176,12 +176,14 @@ def make_decode(seed, lens, Hq, Hkv, D, dtype, q_std=1.0, maxp=None):
 
 
 def run_decode(q, cache, bt, lens, scale, window, dtype, max_len=None, ctas=None, ws=None,
-               stall=0):
+               stall=0, cluster=None):
     B, Hq, D = q.shape
     plan = pa.pa_q4_plan(B, Hq, cache.shape[1], D, 16, cache.shape[0], bt.shape[1],
                          int(lens.max()) if max_len is None else max_len, window, 0, DT[dtype])
     if ctas is not None:
-        plan.ctas_per_group = ctas
+        plan.ctas_per_group, plan.cluster = ctas, 0
+    if cluster == 0:
+        plan.cluster = 0
     plan.test_stall_bytes = stall
     guard = 64
     nan = float("nan")
@@ -226,14 +228,37 @@ def decode_case(seed, lens, Hq, Hkv, D, dtype, window=0, scale=None, **kw):
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("D", [64, 96, 128, 256])
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 2), (6, 1), (8, 1), (16, 1), (10, 5)])
-def test_decode_lengths(Hq, Hkv, D, dtype):
-    decode_case(D + Hq, [1, 15, 16, 17, 0, 255, 700], Hq, Hkv, D, dtype)
+@pytest.mark.parametrize("cluster", [None, 0])
+def test_decode_lengths(Hq, Hkv, D, dtype, cluster):
+    decode_case(D + Hq, [1, 15, 16, 17, 0, 255, 700], Hq, Hkv, D, dtype, cluster=cluster)
 
 
 @pytest.mark.parametrize("D,dtype", [(64, "bf16"), (96, "f16"), (128, "f16"), (256, "bf16")])
 @pytest.mark.parametrize("window", [1, 5, 16, 17, 100, 333, 5000])
-def test_decode_windows(window, D, dtype):
-    decode_case(window, [1, 4, 16, 33, 333, 1000, 0], 4, 2, D, dtype, window=window)
+@pytest.mark.parametrize("cluster", [None, 0])
+def test_decode_windows(window, D, dtype, cluster):
+    decode_case(window, [1, 4, 16, 33, 333, 1000, 0], 4, 2, D, dtype, window=window,
+                cluster=cluster)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (96, "f16"), (128, "bf16"), (256, "f16")])
+@pytest.mark.parametrize("C", [2, 3, 7, 8])
+def test_decode_cluster_sizes(C, D, dtype):
+    # Shares that end inside a slot, ranks without a page, one page for all of them.
+    lens = [1, 16, 17, 0, 400, 16 * C, 16 * C + 1, 33 * C]
+    q, cache, bt, lens = make_decode(60 + C, lens, 6, 2, D, dtype)
+    want = ref.decode(q, cache.cpu().numpy(), bt, lens, 0.1, 0, dtype)
+    plan = pa.pa_q4_plan(len(lens), 6, 2, D, 16, cache.shape[0], bt.shape[1],
+                         int(lens.max()), 0, 0, DT[dtype])
+    plan.cluster, plan.ctas_per_group = C, C * len(lens)
+    plan.workspace_bytes = 1 << 28
+    plan.ctrl_bytes = max(plan.ctrl_bytes, 4096)
+    ws = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    tq = to_t(q, dtype)
+    out, lse = torch.full_like(tq, float("nan")), torch.empty(len(lens), 6, device="cuda")
+    pa.pa_q4_decode(plan, tq, cache, torch.from_numpy(bt).cuda(), torch.from_numpy(lens).cuda(), 0.1, 0,
+                    out, lse, ws)
+    check((out.double().cpu().numpy(), lse.double().cpu().numpy(), pa.pa_get_error(ws)), want)
 
 
 @pytest.mark.parametrize("D,dtype", [(64, "f16"), (96, "bf16"), (128, "bf16"), (256, "f16")])
@@ -307,7 +332,7 @@ def test_decode_carries_nan_values_to_their_rows_only():
     assert nan[1, 2:, 32:64].all() and nan.sum() == 2 * 32
 
 
-@pytest.mark.parametrize("ctas", [1, None])
+@pytest.mark.parametrize("ctas", [1, 6, None])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_bad_page_ids_and_lengths_give_nan_rows(D, ctas):
     q, cache, bt, lens = make_decode(16, [700, 300, 90, 16], 4, 1, D, "f16")
@@ -333,20 +358,22 @@ def test_bad_page_ids_and_lengths_give_nan_rows(D, ctas):
         rows(got, [0, 2, 3], [1])
 
 
-def test_copy_timeout_is_reported_and_the_next_call_is_clean():
+@pytest.mark.parametrize("cluster", [None, 0])
+def test_copy_timeout_is_reported_and_the_next_call_is_clean(cluster):
     q, cache, bt, lens = make_decode(17, [500, 20], 4, 1, 128, "f16")
-    out, lse, err = run_decode(q, cache, bt, lens, 0.1, 0, "f16", stall=16)
+    out, lse, err = run_decode(q, cache, bt, lens, 0.1, 0, "f16", stall=16, cluster=cluster)
     assert err & binding.PA_DEVERR_TIMEOUT
     assert np.isnan(out).all() and np.isnan(lse).all()
     check(run_decode(q, cache, bt, lens, 0.1, 0, "f16"),
           ref.decode(q, cache.cpu().numpy(), bt, lens, 0.1, 0, "f16"))
 
 
-def test_calls_repeat_bit_for_bit():
+@pytest.mark.parametrize("cluster", [None, 0])
+def test_calls_repeat_bit_for_bit(cluster):
     q, cache, bt, lens = make_decode(18, [3000, 100, 2000], 8, 2, 128, "f16")
-    first = run_decode(q, cache, bt, lens, 0.1, 0, "f16")
+    first = run_decode(q, cache, bt, lens, 0.1, 0, "f16", cluster=cluster)
     for _ in range(5):
-        again = run_decode(q, cache, bt, lens, 0.1, 0, "f16")
+        again = run_decode(q, cache, bt, lens, 0.1, 0, "f16", cluster=cluster)
         assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
 
 
@@ -437,12 +464,13 @@ def late_writer():
     return lib
 
 
+@pytest.mark.parametrize("cluster", [None, 0])
 @pytest.mark.parametrize("old", ["same lengths", "a token more", "pages fewer", "garbage"])
 @pytest.mark.parametrize("lens,window,D", [([3000, 1200, 0, 2049, 77], 0, 128),
                                            ([3000, 1200, 2049, 77], 1000, 64),
                                            ([20000], 0, 256), ([30] * 127 + [0], 0, 64),
                                            ([40, 3] * 100, 0, 96)])
-def test_decode_uses_lengths_and_ids_written_late(late_writer, lens, window, D, old):
+def test_decode_uses_lengths_and_ids_written_late(late_writer, lens, window, D, old, cluster):
     # What the kernel reads before its dependency wait are hints; everything counts only as it
     # stands after the wait.  The old table points at a page of NaN scales.
     q, cache, bt, lens = make_decode(30, lens, 4, 2, D, "f16")
@@ -457,6 +485,8 @@ def test_decode_uses_lengths_and_ids_written_late(late_writer, lens, window, D, 
         old_bt[:, 1::2] = 1 << 30
     B, Hq = q.shape[:2]
     plan = pa.pa_q4_plan(B, Hq, 2, D, 16, cache.shape[0], bt.shape[1], int(lens.max()), window)
+    if cluster == 0:
+        plan.cluster = 0
     ws = pa.new_workspace(plan, "cuda")
     tq = to_t(q, "f16")
     new = torch.from_numpy(bt).cuda(), torch.from_numpy(lens).cuda()
