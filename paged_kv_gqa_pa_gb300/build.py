@@ -1,15 +1,16 @@
 """Build libpa_gb300.so in-tree with nvcc for sm_103a (GB300).
 
 Each translation unit under csrc/ compiles in parallel; the objects link into
-one shared library with the static CUDA runtime.  csrc/pa_pyfast.c, the argument
-marshalling of q4.py in C, becomes a Python extension beside it where the
-interpreter's headers are installed (q4.py works without it).  Usage:
+one shared library with the static CUDA runtime.  csrc/pa_pyfast.cpp, the
+argument marshalling of q4.py, becomes a Python extension beside it where the
+interpreter's and torch's headers are installed (q4.py works without it).  Usage:
     python -m paged_kv_gqa_pa_gb300.build [--force] [--verbose]
 """
 from __future__ import annotations
 
 import argparse
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -21,7 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpa_gb300.so")
-PYFAST_SRC = os.path.join(CSRC, "pa_pyfast.c")
+PYFAST_SRC = os.path.join(CSRC, "pa_pyfast.cpp")
 PYFAST = os.path.join(BUILD, "_pa_fast.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -44,30 +45,53 @@ def _deps():
             glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
 
 
-def _python_include():
-    inc = sysconfig.get_paths()["include"]
-    return inc if os.path.exists(os.path.join(inc, "Python.h")) else None
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
-def build_pyfast(force: bool = False, verbose: bool = False):
-    """The marshalling extension; None without the interpreter's headers or a C compiler."""
-    inc = _python_include()
-    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
-    if inc is None or cc is None:
+def _cuda_include():
+    return os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+
+
+def _start_pyfast(force: bool, verbose: bool):
+    """A running compilation of the marshalling extension and its output file; None if it is
+    up to date, or without a C++ compiler or the interpreter's or torch's headers."""
+    inc, torch_dir = sysconfig.get_paths()["include"], _torch_dir()
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if cxx is None or torch_dir is None or not os.path.exists(os.path.join(inc, "Python.h")):
         return None
-    deps = [PYFAST_SRC, os.path.join(ROOT, "include", "pa.h"),
+    header = os.path.join(torch_dir, "include", "torch", "csrc", "autograd", "python_variable.h")
+    if not os.path.exists(header):
+        return None
+    deps = [PYFAST_SRC, os.path.join(ROOT, "include", "pa.h"), header,
             os.path.join(ROOT, "include", "pa_q4.h"), os.path.abspath(__file__)]
     if not force and os.path.exists(PYFAST) and all(
             os.path.getmtime(p) <= os.path.getmtime(PYFAST) for p in deps):
-        return PYFAST
+        return None
     os.makedirs(BUILD, exist_ok=True)
     tmp = PYFAST + f".tmp{os.getpid()}"
-    cmd = [cc, "-O2", "-shared", "-fPIC", "-I", inc, "-o", tmp, PYFAST_SRC]
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-I", inc,
+           "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-isystem", _cuda_include(), "-o", tmp, PYFAST_SRC,
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, PYFAST)
-    return PYFAST
+    return subprocess.Popen(cmd), tmp
+
+
+def _finish_pyfast(job) -> None:
+    if job is None:
+        return
+    proc, tmp = job
+    if proc.wait() == 0:
+        os.replace(tmp, PYFAST)
+    else:  # (an older one must not stay behind)
+        print("the marshalling extension was not built; q4.py goes without it", file=sys.stderr)
+        for path in (tmp, PYFAST):
+            if os.path.exists(path):
+                os.remove(path)
 
 
 def up_to_date() -> bool:
@@ -78,7 +102,14 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    build_pyfast(force, verbose)
+    pyfast = _start_pyfast(force, verbose)
+    try:
+        return _build_lib(force, verbose, ptxas_verbose)
+    finally:
+        _finish_pyfast(pyfast)
+
+
+def _build_lib(force: bool, verbose: bool, ptxas_verbose: bool) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

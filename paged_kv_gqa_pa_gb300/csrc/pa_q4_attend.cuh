@@ -1045,11 +1045,9 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         }
     }
     if constexpr (kCluster) {
-        // Every CTA's state is in its ring and s_sum (nothing attended: a sum of
-        // 0); each warp of the cluster merges units of all of them, whose reads go
-        // out together.  The second barrier keeps the shared memory until all
-        // have read it.
-        if (lo >= hi && tid < kMaxHeadsPerCta) s_sum[tid] = make_float2(-INFINITY, 0.f);
+        // The state of every CTA with pages is in its ring and s_sum; each warp of
+        // the cluster merges units of all of them, whose reads go out together.
+        // The second barrier keeps the shared memory until all have read it.
         __syncthreads();
         q4_cluster_barrier();
         const int rank = blockIdx.x - b * p.cluster;

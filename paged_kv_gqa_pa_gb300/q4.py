@@ -59,8 +59,8 @@ class pa_q4_plan_t(ctypes.Structure):
 
 
 _bound = None
-# The marshalling extension (csrc/pa_pyfast.c), once the library is loaded: it makes the usual
-# call in about half the host time, and returns None where it leaves a call to the code here.
+# The marshalling extension (csrc/pa_pyfast.cpp), once the library is loaded: it makes the usual
+# call in a third of the host time, and returns None where it leaves a call to the code here.
 _fast = None
 
 
@@ -74,9 +74,7 @@ def _load_fast(lib):
     except ImportError:  # built for another interpreter
         return None
     names = ("pa_q4_write", "pa_q4_read", "pa_q4_decode", "pa_extend_tables", "pa_rope_axes")
-    fast.setup((torch.float16, torch.bfloat16, torch.float32, torch.int32, torch.int64,
-                torch.uint8),
-               tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
+    fast.setup(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
                getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), _raw_stream)
     return fast
 

@@ -267,29 +267,10 @@ def test_reference_tables_by_hand():
     assert got[4].tolist() == list(range(20, 33)) + [0, 1, 0, 0] and got[5:] == (2, 0)
 
 
-class FakeTensor:
-    """What the marshalling extension looks at of a tensor."""
-
-    def __init__(self, dtype, shape, ptr, stride=None, dev=0, contiguous=True):
-        self.dtype, self.shape, self._ptr, self._dev, self._c = dtype, tuple(shape), ptr, dev, contiguous
-        st = []
-        n = 1
-        for d in reversed(shape):
-            st.append(n)
-            n *= d
-        self._stride = tuple(reversed(st)) if stride is None else stride
-
-    def get_device(self):
-        return self._dev
-
-    def data_ptr(self):
-        return self._ptr
-
-    def is_contiguous(self):
-        return self._c
-
-    def stride(self):
-        return self._stride
+def tens(dtype, shape, stride=None):
+    """A CPU tensor of this form (its device, -1, is the stand-in's current one)."""
+    return torch.empty(shape, dtype=dtype) if stride is None else \
+        torch.empty_strided(shape, stride, dtype=dtype)
 
 
 @pytest.fixture
@@ -316,8 +297,7 @@ def marshalled(lib):
             calls.append((name, a))
             return 3 if name == "read" else 0
         keep.append(proto(fn))
-    T = (torch.float16, torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8)
-    q4._fast.setup(T, tuple(ctypes.cast(f, P).value for f in keep), lambda: 0, lambda d: 4096 + d)
+    q4._fast.setup(tuple(ctypes.cast(f, P).value for f in keep), lambda: -1, lambda d: 4096 + d)
     yield q4._fast, calls
     q4._load_fast(lib)  # the real functions again
 
@@ -325,84 +305,90 @@ def marshalled(lib):
 def test_marshalling_of_the_usual_calls(marshalled):
     fast, calls = marshalled
     f16, i32, i64 = torch.float16, torch.int32, torch.int64
-    k = FakeTensor(f16, (5, 2, 128), 1 << 20, stride=(1024, 128, 1))
-    v = FakeTensor(f16, (5, 2, 128), 2 << 20)
-    sl, c = FakeTensor(i64, (5,), 3 << 20), FakeTensor(torch.uint8, (9, 2, 2560), 1 << 40)
+
+    def at(*t):
+        return tuple(x.data_ptr() for x in t)
+
+    k = tens(f16, (5, 2, 128), (1024, 128, 1))
+    v = tens(f16, (5, 2, 128))
+    sl, c = tens(i64, (5,)), tens(torch.uint8, (9, 2, 2560))
+    kp, vp, slp, cp = at(k, v, sl, c)
     assert fast.q4_write(k, v, sl, c) == 0
-    assert calls.pop() == ("write", (5, 2, 128, 16, 9, 0, 1 << 20, 1024, 2 << 20, 256, 3 << 20,
-                                     1 << 40, None, 4096))
+    assert calls.pop() == ("write", (5, 2, 128, 16, 9, 0, kp, 1024, vp, 256, slp, cp, None, 4095))
     assert fast.q4_read(c, sl, k, v) == 3  # the status comes back
-    assert calls.pop() == ("read", (5, 2, 128, 16, 9, 0, 1 << 40, 3 << 20, 1 << 20, 1024, 2 << 20,
-                                    256, None, 4096))
+    assert calls.pop() == ("read", (5, 2, 128, 16, 9, 0, cp, slp, kp, 1024, vp, 256, None, 4095))
     plan = _plan(dtype=1)
     bf = torch.bfloat16
-    q, out = FakeTensor(bf, (2, 8, 128), 16), FakeTensor(bf, (2, 8, 128), 32)
-    bt, cl = FakeTensor(i32, (2, 16), 48), FakeTensor(i32, (2,), 64)
-    cache = FakeTensor(torch.uint8, (64, 2, 2560), 80)
-    lse, ws = FakeTensor(torch.float32, (2, 8), 96), FakeTensor(torch.uint8, (plan.workspace_bytes,), 112)
+    q, out = tens(bf, (2, 8, 128)), tens(bf, (2, 8, 128))
+    bt, cl = tens(i32, (2, 16)), tens(i32, (2,))
+    cache = tens(torch.uint8, (64, 2, 2560))
+    lse, ws = tens(torch.float32, (2, 8)), tens(torch.uint8, (plan.workspace_bytes,))
     assert fast.q4_decode(plan, q, cache, bt, cl, 0.5, 7, out, lse, ws) == 0
-    assert calls.pop() == ("decode", (bytes(plan), 16, 80, 48, 64, 0.5, 7, 32, 96, 112, 4096))
-    t = [FakeTensor(i32, (3,), 16 * j) for j in (1, 2)] + [FakeTensor(i32, (11,), 48), 77,
-         FakeTensor(i32, (3, 6), 64), FakeTensor(i32, (3,), 80), FakeTensor(i32, (4,), 96),
-         FakeTensor(i64, (20,), 112), FakeTensor(i32, (20,), 128), FakeTensor(i32, (1,), 144)]
+    assert calls.pop() == ("decode", (bytes(plan), *at(q, cache, bt, cl), 0.5, 7,
+                                      *at(out, lse, ws), 4095))
+    t = [tens(i32, (3,)), tens(i32, (3,)), tens(i32, (11,)), 77, tens(i32, (3, 6)), tens(i32, (3,)),
+         tens(i32, (4,)), tens(i64, (20,)), tens(i32, (20,)), tens(i32, (1,))]
     assert fast.extend_tables(*t) == 0
-    assert calls.pop() == ("tables", (3, 6, 16, 77, 11, 20, *[16 * j for j in range(1, 10)], None, 4096))
+    assert calls.pop() == ("tables", (3, 6, 16, 77, 11, 20, *at(*t[:3], *t[4:]), None, 4095))
     f32 = torch.float32
-    q, k = FakeTensor(f32, (5, 4, 64), 16), FakeTensor(f32, (5, 2, 64), 32, stride=(512, 64, 1))
-    o = FakeTensor(f32, (5, 2, 64), 48)
-    pos = FakeTensor(i32, (3, 5), 64)
+    q, k = tens(f32, (5, 4, 64)), tens(f32, (5, 2, 64), (512, 64, 1))
+    o = tens(f32, (5, 2, 64))
+    pos = tens(i32, (3, 5))
+    qp, kp, op, pp = at(q, k, o, pos)
     assert fast.rope_axes(q, k, pos, (4, 6, 6), 1e4, None, o, 32, True, False) == 0
-    assert calls.pop() == ("rope", (5, 4, 2, 64, 32, 3, [4, 6, 6], 1, 0, 1e4, 2, 16, 256, 32, 512, 64,
-                                    16, 256, 48, 128, 4096))
+    assert calls.pop() == ("rope", (5, 4, 2, 64, 32, 3, [4, 6, 6], 1, 0, 1e4, 2, qp, 256, kp, 512, pp,
+                                    qp, 256, op, 128, 4095))
     assert fast.rope_axes(q, k, pos, (4, 6, 6), 1e4, None, None, None, False, True) == 0
     assert calls.pop()[1][4:9] == (64, 3, [4, 6, 6], 0, 1)
     assert not calls
+    fast.setup((1, 2, 3, 4, 5), lambda: 0, lambda d: 4096)  # another device is the current one
+    assert fast.rope_axes(q, k, pos, (4, 6, 6), 1e4, None, o, 32, True, False) is None
 
 
 def test_marshalling_leaves_everything_else_alone(marshalled):
     fast, calls = marshalled
     f16, i32, i64 = torch.float16, torch.int32, torch.int64
-    ok = dict(k=FakeTensor(f16, (5, 2, 128), 16), v=FakeTensor(f16, (5, 2, 128), 32),
-              sl=FakeTensor(i64, (5,), 48), c=FakeTensor(torch.uint8, (9, 2, 2560), 64))
-    for name, bad in [("k", FakeTensor(f16, (5, 2, 128), 16, dev=1)), ("k", None), ("k", 3),
-                      ("k", FakeTensor(f16, (5, 256), 16)), ("k", FakeTensor(i32, (5, 2, 128), 16)),
-                      ("k", FakeTensor(f16, (5, 2, 128), 16, stride=(256, 1, 2))),
-                      ("v", FakeTensor(f16, (5, 2, 128), 16, stride=(64, 640, 1))),
-                      ("v", FakeTensor(torch.bfloat16, (5, 2, 128), 16)),
-                      ("v", FakeTensor(f16, (4, 2, 128), 16)),
-                      ("sl", FakeTensor(i32, (5,), 48)), ("sl", FakeTensor(i64, (6,), 48)),
-                      ("sl", FakeTensor(i64, (5,), 48, contiguous=False)),
-                      ("sl", FakeTensor(i64, (5,), 48, dev=-1)),
-                      ("c", FakeTensor(torch.uint8, (9, 3, 2560), 64)),
-                      ("c", FakeTensor(torch.uint8, (9, 2, 1280), 64)),
-                      ("c", FakeTensor(torch.uint8, (1 << 32, 2, 2560), 64)),
-                      ("c", FakeTensor(torch.int8, (9, 2, 2560), 64))]:
+    ok = dict(k=tens(f16, (5, 2, 128)), v=tens(f16, (5, 2, 128)),
+              sl=tens(i64, (5,)), c=tens(torch.uint8, (9, 2, 2560)))
+    for name, bad in [("k", None), ("k", 3),
+                      ("k", tens(f16, (5, 256))), ("k", tens(i32, (5, 2, 128))),
+                      ("k", tens(f16, (5, 2, 128), (256, 1, 2))),
+                      ("v", tens(f16, (5, 2, 128), (64, 640, 1))),
+                      ("v", tens(torch.bfloat16, (5, 2, 128))),
+                      ("v", tens(f16, (4, 2, 128))),
+                      ("sl", tens(i32, (5,))), ("sl", tens(i64, (6,))),
+                      ("sl", tens(i64, (5,), (2,))), ("v", tens(f16, (5, 2, 128)).to_sparse()),
+                      ("v", torch.empty((5, 2, 128), dtype=f16, device="meta")),
+                      ("v", np.zeros((5, 2, 128), np.float16)),
+                      ("c", tens(torch.uint8, (9, 3, 2560))),
+                      ("c", tens(torch.uint8, (9, 2, 1280))),
+                      ("c", tens(torch.int8, (9, 2, 2560)))]:
         a = dict(ok, **{name: bad})
         assert fast.q4_write(a["k"], a["v"], a["sl"], a["c"]) is None, (name, bad)
         assert fast.q4_read(a["c"], a["sl"], a["k"], a["v"]) is None, (name, bad)
     plan = _plan()
-    base = [plan, FakeTensor(f16, (2, 8, 128), 16), FakeTensor(torch.uint8, (64, 2, 2560), 32),
-            FakeTensor(i32, (2, 16), 48), FakeTensor(i32, (2,), 64), 0.5, 0,
-            FakeTensor(f16, (2, 8, 128), 80), FakeTensor(torch.float32, (2, 8), 96),
-            FakeTensor(torch.uint8, (plan.workspace_bytes,), 112)]
+    base = [plan, tens(f16, (2, 8, 128)), tens(torch.uint8, (64, 2, 2560)),
+            tens(i32, (2, 16)), tens(i32, (2,)), 0.5, 0,
+            tens(f16, (2, 8, 128)), tens(torch.float32, (2, 8)),
+            tens(torch.uint8, (plan.workspace_bytes,))]
     assert fast.q4_decode(*base) == 0
     calls.clear()
-    for i, bad in [(0, object()), (0, b"x" * 8), (1, FakeTensor(f16, (3, 8, 128), 16)), (5, 1), (5, "a"),
-                   (6, 0.0), (6, 1 << 40), (6, True), (8, FakeTensor(f16, (2, 8), 96)),
-                   (9, FakeTensor(torch.uint8, (plan.workspace_bytes - 1,), 112)),
-                   (9, FakeTensor(torch.uint8, (1, plan.workspace_bytes), 112)),
-                   (2, FakeTensor(torch.uint8, (63, 2, 2560), 32))]:
+    for i, bad in [(0, object()), (0, b"x" * 8), (1, tens(f16, (3, 8, 128))), (5, 1), (5, "a"),
+                   (6, 0.0), (6, 1 << 40), (6, True), (8, tens(f16, (2, 8))),
+                   (9, tens(torch.uint8, (plan.workspace_bytes - 1,))),
+                   (9, tens(torch.uint8, (1, plan.workspace_bytes))),
+                   (2, tens(torch.uint8, (63, 2, 2560)))]:
         a = list(base)
         a[i] = bad
         assert fast.q4_decode(*a) is None, (i, bad)
     assert fast.q4_decode(*base[:9]) is None and fast.extend_tables(1, 2) is None
     f32 = torch.float32
-    r = [FakeTensor(f32, (5, 4, 64), 16), FakeTensor(f32, (5, 2, 64), 32), FakeTensor(i32, (3, 5), 64),
+    r = [tens(f32, (5, 4, 64)), tens(f32, (5, 2, 64)), tens(i32, (3, 5)),
          (4, 6, 6), 1e4, None, None, None, False, False]
-    for i, bad in [(0, None), (1, None), (1, FakeTensor(f32, (4, 2, 64), 32)),
-                   (1, FakeTensor(f16, (5, 2, 64), 32)), (2, FakeTensor(i32, (2, 5), 64)),
+    for i, bad in [(0, None), (1, None), (1, tens(f32, (4, 2, 64))),
+                   (1, tens(f16, (5, 2, 64))), (2, tens(i32, (2, 5))),
                    (3, [4, 6, 6]), (3, (1, 2, 3, 4, 5)), (3, (4.0, 6, 6)), (3, ()), (4, 10000),
-                   (5, FakeTensor(f32, (5, 2, 64), 16)), (7, 32.0), (8, 1), (9, None)]:
+                   (5, tens(f32, (5, 2, 64))), (7, 32.0), (8, 1), (9, None)]:
         a = list(r)
         a[i] = bad
         assert fast.rope_axes(*a) is None, (i, bad)
