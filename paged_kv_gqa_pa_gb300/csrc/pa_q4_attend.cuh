@@ -1075,8 +1075,8 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
                 o.x *= f, o.y *= f, o.z *= f, o.w *= f;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const float w = ml[i].y == 0.f ? 0.f
-                                                   : (ml[i].y != ml[i].y ? NAN : ex2(ml[i].x - top) * ml[i].y);
+                    const float l = ml[i].y;
+                    const float w = l == 0.f ? 0.f : (l != l ? NAN : ex2(ml[i].x - top) * l);
                     if (w == 0.f) continue;
                     sum += w;
                     o.x += w * v[i].x, o.y += w * v[i].y, o.z += w * v[i].z, o.w += w * v[i].w;

@@ -108,12 +108,16 @@ __device__ __forceinline__ void quantise8(const uint4& raw, uint32_t (&code)[2],
         if (__any_sync(0xffffffffu, worst > close)) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float xk = k & 1 ? xv[k / 2].y : xv[k / 2].x;
-                const float dk = k & 1 ? d[k / 2].y : d[k / 2].x;
+                // what d lost: x - z = d + e (packed: 16384 bf16 rows of 4 heads at
+                // D 256, written and read, 44.1 -> 43.1 us)
+                const float2 back = __ffma2_rn(xv[k / 2], minus2, d[k / 2]);
+                const float2 kept = __ffma2_rn(__ffma2_rn(back, minus2, d[k / 2]), minus2, xv[k / 2]);
+                const float2 e2 = __ffma2_rn(__fadd2_rn(back, make_float2(z, z)), minus2, kept);
                 const float rk = k & 1 ? res[k / 2].y : res[k / 2].x;
-                const float back = dk - xk;  // what d lost: x - z = d + e
-                const float e = (xk - (dk - back)) - (z + back);
-                const float over = (fabsf(rk) - half) + copysignf(1.f, rk) * e;
+                const float e = k & 1 ? e2.y : e2.x;
+                const float over = (fabsf(rk) - half) +
+                                   __uint_as_float(__float_as_uint(e) ^
+                                                   (__float_as_uint(rk) & 0x80000000u));
                 // above the middle, or on it with r odd
                 const float bar = __uint_as_float((__float_as_uint(v[i + k]) & 1u) * 0x80000001u);
                 if (over > bar) v[i + k] += copysignf(1.f, rk);
