@@ -124,8 +124,8 @@ typedef struct pa_q4_plan {
                                (PA_DEVERR_TIMEOUT, NaN rows) */
     int cluster;            /* 2 to 8: so many CTAs share each sequence as a thread-block
                                cluster and merge in it (ctas_per_group is batch times
-                               that); 0: the batch's pages are cut into equal ranges.  A
-                               caller may set 0 */
+                               that); 0: the batch's pages are cut into ranges of about
+                               equal work.  A caller may set 0 */
 } pa_q4_plan_t;
 
 /*

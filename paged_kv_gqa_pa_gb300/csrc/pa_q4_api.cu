@@ -45,7 +45,7 @@ static Q4WsLayout q4_ws_layout(int B, int D, long long groups, int X) {
     w.ctr_off = kCtrlBytes;
     w.ctrl_bytes = kCtrlBytes + q4_align256((size_t)groups * B * 4);
     w.info_off = w.ctrl_bytes;
-    w.ml_off = w.info_off + q4_align256(((size_t)B + 3) * 4);
+    w.ml_off = w.info_off + q4_align256((2 * (size_t)B + 4) * 4);
     w.o_off = w.ml_off + q4_align256(rows * kMaxHeadsPerCta * 8);
     w.total = w.o_off + q4_align256(rows * kMaxHeadsPerCta * D * 4);
     return w;
@@ -169,34 +169,32 @@ int pa_q4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
     // of the longest batch.
     int span = (max_context_len + kPageSize - 1) / kPageSize;
     if (window > 0) span = std::min(span, (window - 1 + kPageSize - 1) / kPageSize + 1);
-    const long long pages = std::max(1ll, (long long)std::max(1, batch) * span);
+    const long long cost = std::max(1ll, (long long)std::max(1, batch) * (span + kQ4Start));
     const long long slots = (long long)p.num_sms * q4_ctas_per_sm(head_dim, batch);
     long long x = std::max(1ll, (slots - slots / 64) / groups);
     if (span <= q4_short(head_dim) && batch <= x)
         x = std::max(1, batch);  // one for each sequence
     else
-        x = std::min(x, std::max<long long>(batch, (pages + kWarps * kQ4MinRun - 1) /
-                                                       (kWarps * kQ4MinRun)));
+        x = std::min(x, std::max<long long>(batch, (cost + kWarps * kQ4MinRun - 1) /
+                                                      (kWarps * kQ4MinRun)));
     // A cluster for each sequence, which saves the partials' way through the L2
     // (2 to 4 us) but gives the CTAs of the longest sequence more pages than equal
     // ranges do: the largest cluster of which one wave holds all, with a page for
-    // every warp, where that is at most kQ4ClusterExtra pages more, twice that
-    // with several sequences (whose borders equal ranges cut twice).  Clusters
-    // against equal ranges, head_dim 128, 8 KV heads, at so many pages more: one
-    // sequence -1 6.0 and 6.9 us, 8 7.5 and 8.1, 12 8.0 and 7.9, 23 9.3 and 8.4;
-    // 4 sequences -10 8.0 and 11.4, 13 12.2 and 13.2, 18 13.4 and 14.6, 27 14.9 and
-    // 15.5, 36 18.1 and 17.2; one of 16 longer than the rest 11.7 and 12.9.  At the
-    // limits head_dim 64 (32, 39 pages) 8.5 and 9.7, 10.1 and 10.3.  Clusters that
-    // one wave does not hold cost 5 to 10 us (16 sequences of 1000 tokens by 4 CTAs
-    // 19.3, by 3 12.2, equal ranges 15.4).
+    // every warp, where that is at most kQ4ClusterExtra pages of head_dim 128 more.
+    // Clusters against equal ranges, head_dim 128, 8 KV heads: one sequence of 1000
+    // tokens 6.2 and 7.2 us, of 2500 7.9 and 7.9, of 4000 9.3 and 8.4; 4 of 1000 7.6
+    // and 9.5, of 4000 11.9 and 12.0, of 6000 14.9 and 14.0; 16 of 2500 (bf16) 19.2
+    // and 20.7.  One longer than the rest, 8 in all, of 2000 8.9 and 9.0, of 4000
+    // 11.5 and 9.3.  Clusters that one wave does not hold cost 5 to 10 us (16
+    // sequences of 1000 tokens, bf16, by 4 CTAs 18.8, by 3 12.5).
     if (batch > 0 && span > q4_short(head_dim)) {
         int c = std::min(kQ4MaxCluster, (span + kWarps - 1) / kWarps);
         while (c > 1 && (groups * batch * c > slots ||
                          q4_clusters_held(this_device, head_dim, dtype, batch, c, slots) <
                              groups * batch))
             --c;
-        const long long extra = (span + c - 1) / c - (pages + x - 1) / x;
-        if (c > 1 && extra * head_dim <= kQ4ClusterExtra * 128 * (batch > 1 ? 2 : 1)) {
+        const long long extra = (span + c - 1) / c - (cost + x - 1) / x;
+        if (c > 1 && extra * head_dim <= kQ4ClusterExtra * 128) {
             p.cluster = c;
             x = (long long)c * batch;
         }
@@ -252,8 +250,9 @@ int pa_q4_decode(const pa_q4_plan_t* plan, const void* q, const void* cache,
     // A sequence of a batch of B cut into equal ranges leaves about X / B
     // partials: beyond kQ4KernelRows a kernel of its own gathers them.  By the last
     // CTA to leave one, and by the kernel: 16 sequences of 20000 tokens (3.5 each)
-    // 78.9 and 81.8 us, 8 ragged ones up to 30000 (7) 36.6 and 34.8, 4 of 9000 (14)
-    // 21.2 and 18.7.
+    // 76.5 and 79.8 us, 8 ragged ones up to 30000 (7) 34.9 and 32.8, 4 of 9000 (14)
+    // 20.4 and 17.6; at 4 to 5 of them D 96 would do with the CTA (26.4 and 28.1),
+    // D 256 does not (45.1 and 42.7).
     p.merge_kernel = !p.cluster && X > kQ4KernelRows * plan->batch ? 1 : 0;
     p.counters = reinterpret_cast<unsigned*>(ws + wl.ctr_off);
     p.B = plan->batch;

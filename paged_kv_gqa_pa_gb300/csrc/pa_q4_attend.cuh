@@ -35,10 +35,10 @@
 //    fit the GPU at once and leave no CTA many pages more than equal ranges do
 //    (pa_q4_plan has the figures), a cluster shares a sequence evenly and merges
 //    its CTAs' states through distributed shared memory: 4 sequences of 1000
-//    tokens 11.4 -> 7.8 us.  Otherwise the pages the batch attends, all sequences
-//    end to end, are cut into equal ranges, one per CTA of the group, whatever the
-//    lengths; a range may hold many short sequences or part of a long one.  At a
-//    sequence's end the warps' states meet in shared memory.  A
+//    tokens 9.5 -> 7.6 us.  Otherwise the pages the batch attends, all sequences
+//    end to end, are cut into ranges of equal cost (kQ4Start), one per CTA of the
+//    group, whatever the lengths; a range may hold many short sequences or part of
+//    a long one.  At a sequence's end the warps' states meet in shared memory.  A
 //    sequence inside the range is written; one cut by a border leaves a partial
 //    (o, maximum, sum) per CTA in the workspace.  Who merges a sequence's
 //    partials, always in order: the last CTA to leave one, or, in plans where a
@@ -64,6 +64,12 @@ namespace pa {
 // pages: D 64 ragged 5.0 and 6.0, 5.7 and 6.1 us, D 128 5.4 and 6.0, 6.2 and 5.8
 // (ragged 7.0 and 7.4), D 256 7.5 and 7.3, 9.0 and 7.5.
 constexpr int q4_short(int D) { return D == 256 ? 16 : 24; }
+// What a sequence's start and end cost a CTA, in pages: equal ranges are equal
+// in this cost, not in pages.  0, 4, 8, 12, 16, 24: 64 ragged sequences up to
+// 4096 tokens (bf16, D 128) 50.0, 49.5, 48.7, 47.7, 48.0, 48.1 us, 4 of 4096 at D
+// 256 15.5, 14.6, 12.7, 12.8, 12.7, 13.2, 32 of 4096 (fp16) 39.7, 39.8, 38.7, 37.9,
+// 37.8, 37.8, 256 of up to 512 45.5, 41.0, 39.7, 39.3, 38.4, 38.4.
+constexpr int kQ4Start = 12;
 constexpr int kQ4StagedPages = 512;  // page ids a CTA stages at a time
 
 struct Q4AttendParams {
@@ -75,7 +81,7 @@ struct Q4AttendParams {
     float* lse;
     float* ws_o;    // [groups][X][2] partial outputs, normalised, [unit][lane][4]
     float* ws_ml;   // [groups][X][2][8][2] their maximum (log2 domain) and exp-sum
-    int* ws_info;   // for the merge kernel: pages of a range, then s_base [B + 1]
+    int* ws_info;   // for the merge kernel: cost of a range, then s_base and s_rank [B + 1]
     unsigned* counters;  // [groups][B] partials left so far
     unsigned* err;
     int B, Hq, Hkv, g, num_pages, maxp, max_ctx, window;
@@ -114,8 +120,8 @@ struct Q4Cfg {
     // with 4 and 49.9 with 3; at D 128 four did not pay (40.1 and 40.4 us).
     static constexpr int kMinBlocks = D <= 96 ? 4 : 3;
     static_assert(kMinBlocks * (kSmemBytes + 1024 + 128) <= 228 * 1024, "CTAs per SM");
-    // (three words per sequence follow: s_base, s_page0, s_len)
-    static int smem(int B) { return kSmemBytes + (3 * B + 1) * 4; }
+    // (four words per sequence follow: s_base, s_rank, s_page0, s_len)
+    static int smem(int B) { return kSmemBytes + (4 * B + 2) * 4; }
 };
 
 // mma.sync m16n8k16, 16-bit in, fp32 accumulate; and fp32 pairs to 16 bits.
@@ -224,13 +230,15 @@ __device__ __forceinline__ int q4_v_dim(int g, int w) {
     return D == 96 ? 32 * w + 4 * g : (D / 8) * g + 4 * w;
 }
 
-// The partial rows of one sequence, pages [first, end), with ranges of `range`
-// pages: one per CTA it touches.  A CTA's second row holds a sequence that
+// The partial rows of one sequence, pages [first, end) and `rank` sequences
+// with pages before it, with ranges of the cost `range`: one per CTA whose range
+// has pages of it.  A CTA's second row holds a sequence that
 // begins inside its range, its first row any other.
 struct Q4Rows {
     int x0, n;  // first CTA, rows
     int slot0;  // which row of x0
-    __device__ __forceinline__ Q4Rows(int range, int first, int end) {
+    __device__ __forceinline__ Q4Rows(int range, int first, int end, int rank) {
+        first += kQ4Start * (rank + 1), end += kQ4Start * (rank + 1);
         x0 = first / range;
         n = (end - 1) / range - x0 + 1;
         slot0 = first > x0 * range ? 1 : 0;
@@ -384,7 +392,7 @@ __global__ void __launch_bounds__(kQ4MergeWarps * 32) q4_merge_kernel(const Q4At
     wait_for_prerequisite_grid();
     const int range = p.ws_info[0], first = p.ws_info[1 + b], end = p.ws_info[2 + b];
     if (end <= first) return;
-    const Q4Rows rows(range, first, end);
+    const Q4Rows rows(range, first, end, p.ws_info[p.B + 2 + b]);
     if (rows.n == 1) return;  // not cut
     const int h0 = (group / p.nchunk) * p.g + (group % p.nchunk) * p.G;
     Q4Merge r[1];
@@ -433,9 +441,11 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     float* s_ml = reinterpret_cast<float*>(s_pid + kQ4StagedPages);  // [warp][8][m, sum, weights]
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_ml + kWarps * kMaxHeadsPerCta * 3);
     int* s_base = reinterpret_cast<int*>(bars + kWarps * NS);
-    int* s_page0 = s_base + p.B + 1;
+    int* s_rank = s_base + p.B + 1;
+    int* s_page0 = s_rank + p.B + 1;
     int* s_len = s_page0 + p.B;
-    __shared__ int s_red[kWarps];
+    __shared__ int s_red[2];
+    __shared__ long long s_scan[kWarps];
     __shared__ float2 s_sum[kMaxHeadsPerCta];  // cluster: this CTA's maximum and sum of each head
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -463,7 +473,8 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     auto scan = [&](bool one, int len) {  // one: B <= kThreads, and len is sequence tid's length
         const int per = one ? 1 : (p.B + kThreads - 1) / kThreads;
         const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-        int sum = 0, longest = 0;
+        int longest = 0;
+        long long sum = 0;  // sequences with pages << 32 | pages
         for (int b = b0; b < b1; ++b) {
             const SeqSpan sp =
                 seq_span(one ? len : p.context_lens[b], p.window, p.max_ctx, p.maxp, 1);
@@ -471,26 +482,31 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
             s_base[b] = n;
             s_page0[b] = sp.first_page;
             s_len[b] = sp.L;
-            sum += n;
+            sum += n > 0 ? (1ll << 32) + n : 0;
             longest = max(longest, n);
         }
-        int inc = sum;
+        long long inc = sum;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, inc, m);
+            const long long o = __shfl_up_sync(0xffffffffu, inc, m);
             if (lane >= m) inc += o;
         }
-        if (lane == 31) s_red[warp] = inc;
+        if (lane == 31) s_scan[warp] = inc;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) inc += s_red[w];
-        int at = inc - sum;
+        for (int w = 0; w < warp; ++w) inc += s_scan[w];
+        int at = (int)(inc - sum), rank = (int)((inc - sum) >> 32);
         for (int b = b0; b < b1; ++b) {
             const int n = s_base[b];
             s_base[b] = at;
+            s_rank[b] = rank;
             s_page0[b] -= at;
             at += n;
+            rank += n > 0;
         }
-        if (tid == kThreads - 1) s_base[p.B] = inc;
+        if (tid == kThreads - 1) {
+            s_base[p.B] = (int)inc;
+            s_rank[p.B] = (int)(inc >> 32);
+        }
         return __syncthreads_or(longest > q4_short(D)) != 0;
     };
     // Sequence of page f: the last b with s_base[b] <= f (behind any empty ones
@@ -506,8 +522,24 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
         }
         return a;
     };
-    // This CTA's range [lo, hi) of the pages and its first sequence b.
-    int range, lo, hi, b;
+    // Page at which cost x falls: the pages of b have the costs behind
+    // s_base[b] + kQ4Start (s_rank[b] + 1), its start the kQ4Start before them.
+    auto page_at = [&](long long x) {
+        int a = 0, z = p.B;
+        while (a < z) {
+            const int m = (a + z + 1) >> 1;
+            if (s_base[m] + kQ4Start * s_rank[m] <= x)
+                a = m;
+            else
+                z = m - 1;
+        }
+        if (a == p.B) return s_base[a];
+        const int in = (int)(x - s_base[a] - kQ4Start * (s_rank[a] + 1));
+        return s_base[a] + min(s_base[a + 1] - s_base[a], max(0, in));
+    };
+    // This CTA's range [lo, hi) of the pages, the cost it begins at, and its
+    // first sequence b.
+    int range, from = 0, lo, hi, b;
     auto locate = [&](bool any_long) {
         const int total = s_base[p.B];
         if constexpr (kCluster) {  // an even share of a sequence
@@ -520,16 +552,17 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
             return;
         }
         if (!any_long && p.B <= p.X) {  // a CTA for each sequence
-            range = max(1, total);      // (no border cuts anything)
+            range = max(1, total + kQ4Start * s_rank[p.B]);  // (no border cuts anything)
             b = min((int)blockIdx.x, p.B - 1);
             lo = (int)blockIdx.x < p.B ? s_base[b] : total;
             hi = (int)blockIdx.x < p.B ? s_base[b + 1] : total;
             return;
         }
-        range = max(NP * kWarps, (total + p.X - 1) / p.X);
-        const long long from = (long long)blockIdx.x * range;
-        lo = (int)min((long long)total, from);
-        hi = (int)min((long long)total, from + range);
+        const int cost = total + kQ4Start * s_rank[p.B];
+        range = max(NP * kWarps, (cost + p.X - 1) / p.X);
+        from = (int)min((long long)cost, (long long)blockIdx.x * range);
+        lo = page_at(from);
+        hi = page_at((long long)from + range);
         b = lo < hi ? sequence_of(lo) : 0;
     };
     auto table_entry = [&](int f) {
@@ -575,7 +608,10 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     }
     if (p.merge_kernel && blockIdx.x == 0 && blockIdx.y == 0) {
         if (tid == 0) p.ws_info[0] = range;
-        for (int i = tid; i <= p.B; i += kThreads) p.ws_info[1 + i] = s_base[i];
+        for (int i = tid; i <= p.B; i += kThreads) {
+            p.ws_info[1 + i] = s_base[i];
+            p.ws_info[p.B + 2 + i] = s_rank[i];
+        }
     }
 
     // ---- Sequences that attend nothing: out 0 and lse -inf, or NaN where the
@@ -832,8 +868,9 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     unsigned* counters = p.counters + (size_t)group * p.B;
     auto end_sequence = [&]() PA_INLINE_LAMBDA {
         const bool cut = !kCluster && (s_base[b] < lo || s_base[b + 1] > hi);
-        const size_t row = row0 + (s_base[b] > lo ? 1 : 0);
-        if (cut) (s_base[b] > lo ? cut_tail : cut_head) = b;
+        const bool tail = s_base[b] + kQ4Start * (s_rank[b] + 1) > from;
+        const size_t row = row0 + (tail ? 1 : 0);
+        if (cut) (tail ? cut_tail : cut_head) = b;
 #pragma unroll
         for (int k = 4; k < 32; k <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, k);
@@ -910,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
                         make_float2(top[k], sum[k]);
             }
         }
-        if (cut && s_base[b] <= lo && !p.merge_kernel) {
+        if (cut && !tail && !p.merge_kernel) {
             __syncthreads();
             if (threadIdx.x == 0) head_count = q4_arrive(counters + b);
         }
@@ -1103,7 +1140,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     __syncthreads();
     if (threadIdx.x == 0) {
         auto last = [&](int c, int before) {
-            const bool is = before == Q4Rows(range, s_base[c], s_base[c + 1]).n - 1;
+            const bool is = before == Q4Rows(range, s_base[c], s_base[c + 1], s_rank[c]).n - 1;
             if (is) counters[c] = 0;  // ready for the next call
             return is;
         };
@@ -1115,7 +1152,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
     for (int i = 0; i < 2; ++i) {
         const int c = i == 0 ? cut_head : cut_tail;
         if (s_red[i])
-            q4_merge_units<D, T, 2, 4>(p, Q4Rows(range, s_base[c], s_base[c + 1]), c, group, h0,
+            q4_merge_units<D, T, 2, 4>(p, Q4Rows(range, s_base[c], s_base[c + 1], s_rank[c]), c, group, h0,
                                        warp, kWarps);
     }
 }

@@ -332,6 +332,27 @@ def test_decode_carries_nan_values_to_their_rows_only():
     assert nan[1, 2:, 32:64].all() and nan.sum() == 2 * 32
 
 
+@pytest.mark.parametrize("D,dtype", [(64, "f16"), (96, "bf16"), (128, "f16"), (256, "bf16")])
+@pytest.mark.parametrize("ctas", [3, 8, 13, 19, 31, 40])
+def test_decode_ranges_within_a_sequences_start(ctas, D, dtype):
+    """Ranges shorter than what a start counts for: some CTAs get no page, and borders fall on,
+    before and behind the first pages, with empty sequences between; both kinds of merge."""
+    lens = [0, 400, 1, 0, 0, 16, 17, 300]
+    q, cache, bt, lens = make_decode(80 + ctas, lens, 6, 2, D, dtype)
+    want = ref.decode(q, cache.cpu().numpy(), bt, lens, 0.1, 0, dtype)
+    plan = pa.pa_q4_plan(len(lens), 6, 2, D, 16, cache.shape[0], bt.shape[1],
+                         int(lens.max()), 0, 0, DT[dtype])
+    plan.cluster, plan.ctas_per_group = 0, ctas
+    plan.workspace_bytes = 1 << 26
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    tq = to_t(q, dtype)
+    args = [tq, cache, torch.from_numpy(bt).cuda(), torch.from_numpy(lens).cuda(), 0.1, 0]
+    for _ in range(2):
+        out, lse = torch.full_like(tq, float("nan")), torch.empty(len(lens), 6, device="cuda")
+        pa.pa_q4_decode(plan, *args, out, lse, ws)
+        check((out.double().cpu().numpy(), lse.double().cpu().numpy(), pa.pa_get_error(ws)), want)
+
+
 @pytest.mark.parametrize("ctas", [1, 6, None])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_bad_page_ids_and_lengths_give_nan_rows(D, ctas):
