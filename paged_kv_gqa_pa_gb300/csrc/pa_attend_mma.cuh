@@ -715,12 +715,18 @@ __global__ void __launch_bounds__(kThreads, MmaCfg<D, ROPE, DEEP>::kMinBlocks)
     // itself, and used only if the length's real range lies inside them
     // (otherwise they are loaded again).  A decode step moves the range by at
     // most a page, so this saves one dependent memory round trip per CTA.
+    // One thread reads the hint for the CTA: the previous grid may be writing
+    // the length at this moment, and threads with different hints would place
+    // the entries by different shifts, which leaves page ids that nobody wrote.
+    // (s_ml holds nothing yet; it is written again behind the barrier that
+    // closes the staging below.)
     constexpr bool kSpecIds = !ROPE;
     constexpr int kSpecLoads = 3;  // per thread: ranges of up to 3 * kThreads entries
     const bool spec_ids = kSpecIds && !(kBalancedInstance && p.balanced);
-    int len_hint = 0;
-    if (spec_ids) len_hint = __ldcg(p.context_lens + b);
-    __syncthreads();  // barriers and rotary tables initialised
+    int* const s_len_hint = reinterpret_cast<int*>(s_ml);
+    if (spec_ids && threadIdx.x == 0) *s_len_hint = __ldcg(p.context_lens + b);
+    __syncthreads();  // barriers, rotary tables and the hint in place
+    const int len_hint = spec_ids ? *s_len_hint : 0;
     wait_for_prerequisite_grid();
     if (kBalancedInstance && p.balanced) {
         BalancedItem it;
