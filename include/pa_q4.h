@@ -105,7 +105,7 @@ typedef struct pa_q4_plan {
     int page_size;          /* 16 */
     int num_pages;          /* pages in the cache */
     int max_pages_per_seq;  /* row length of block_tables */
-    int max_context_len;    /* upper bound on every context_lens[b] */
+    int max_context_len;    /* upper bound on every context_lens[b]; at most 2^31 - 16 */
     int window;             /* sliding window in tokens, 0 = whole context */
     int dtype;              /* PA_DTYPE_F16 or PA_DTYPE_BF16: q, out, the cache's values */
     int num_sms;            /* SM count the plan was made for */

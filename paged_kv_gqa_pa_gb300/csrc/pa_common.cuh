@@ -179,6 +179,17 @@ __host__ __device__ constexpr bool kFusedMergeLegal(int G, int D, int R) {
 static_assert(2 * kFusedMaxStaged * 4 <= kWarps * kMaxHeadsPerCta * 64 * 4,
               "the staged (m, weight) pairs fit the combine buffer");
 
+// Pages that a sequence of at most max_context_len tokens can attend:
+// ceil(max_context_len / ps), or with a window at most ceil((window - 1) / ps)
+// + 1 (the window need not start on a page edge).  Any value of either from 0
+// on: nothing is added to a length before it is divided.
+inline int attended_pages(int max_context_len, int window) {
+    auto pages = [](int tokens) { return tokens / kPageSize + (tokens % kPageSize != 0); };
+    const int span = pages(max_context_len);
+    const int wspan = window > 0 ? pages(window - 1) + 1 : span;
+    return wspan < span ? wspan : span;
+}
+
 // Span of pages a sequence attends, shared by the partition and merge kernels
 // so both agree on the partition count of every sequence.
 struct SeqSpan {

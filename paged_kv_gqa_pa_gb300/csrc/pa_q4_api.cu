@@ -116,7 +116,9 @@ static int q4_check_shapes(const pa_q4_plan_t* p) {
     if (p->dtype == PA_DTYPE_F32 || !q4_head_dim_ok(p->head_dim) || p->page_size != kPageSize ||
         p->batch > kQ4MaxBatch)
         return PA_ERR_UNSUPPORTED;
-    // The batch's pages end to end are counted in 32 bits.
+    // Positions, and lengths rounded up to whole pages, are counted in 32 bits.
+    if (p->max_context_len > INT_MAX - (kPageSize - 1)) return PA_ERR_UNSUPPORTED;
+    // So are the batch's pages end to end.
     const long long span = ((long long)p->max_context_len + kPageSize - 1) / kPageSize;
     if (span * std::max(1, p->batch) > (1ll << 30)) return PA_ERR_UNSUPPORTED;
     return PA_OK;
@@ -167,8 +169,7 @@ int pa_q4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
     // slots (a grid that needs every slot had CTAs starting in a second wave),
     // but no more than give every sequence one and every warp kQ4MinRun pages
     // of the longest batch.
-    int span = (max_context_len + kPageSize - 1) / kPageSize;
-    if (window > 0) span = std::min(span, (window - 1 + kPageSize - 1) / kPageSize + 1);
+    const int span = attended_pages(max_context_len, window);
     const long long cost = std::max(1ll, (long long)std::max(1, batch) * (span + kQ4Start));
     const long long slots = (long long)p.num_sms * q4_ctas_per_sm(head_dim, batch);
     long long x = std::max(1ll, (slots - slots / 64) / groups);

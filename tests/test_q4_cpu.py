@@ -407,3 +407,38 @@ def test_plan_clusters(D, dtype):
             assert 2 <= plan.cluster <= 8
             assert plan.ctas_per_group == plan.cluster * batch
             assert plan.ctas == plan.ctas_per_group * 4
+
+
+INT_MAX = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("batch,tokens", [(1, 20), (1, 1000), (4, 4000), (4, 100000), (300, 500)])
+def test_plan_with_a_window_that_holds_everything(batch, tokens, D):
+    """A window of the longest length or more, up to the largest int, plans like no window."""
+    want = _plan(batch=batch, num_q_heads=24, num_kv_heads=4, head_dim=D, max_pages_per_seq=6250,
+                 max_context_len=tokens)
+    for window in (tokens + 16, 1 << 20, INT_MAX - 15, INT_MAX - 14, INT_MAX):
+        got = _plan(batch=batch, num_q_heads=24, num_kv_heads=4, head_dim=D, max_pages_per_seq=6250,
+                    max_context_len=tokens, window=window)
+        assert (got.ctas_per_group, got.ctas, got.cluster) == (want.ctas_per_group, want.ctas,
+                                                               want.cluster), window
+        assert got.workspace_bytes == want.workspace_bytes
+
+
+def test_plan_of_the_longest_lengths(lib):
+    # Lengths rounded up to whole pages have to fit an int.
+    long = dict(batch=1, max_pages_per_seq=1 << 27)
+    whole = _plan(**long, max_context_len=1 << 30)
+    assert whole.ctas_per_group > 100
+    assert _plan(**long, max_context_len=2 ** 31 - 16).ctas_per_group == whole.ctas_per_group
+    few = _plan(**long, max_context_len=2 ** 31 - 16, window=100)
+    assert few.ctas_per_group == _plan(max_context_len=256, window=100, batch=1).ctas_per_group
+    for tokens in (2 ** 31 - 15, INT_MAX):
+        for window in (0, 100):
+            with pytest.raises(pa.PAError) as e:
+                _plan(**long, max_context_len=tokens, window=window)
+            assert e.value.status == binding.PA_ERR_UNSUPPORTED
+    few.max_context_len = INT_MAX  # an edited plan
+    assert lib.pa_q4_decode(ctypes.byref(few), FAKE, FAKE, FAKE, FAKE, 1.0, 100, FAKE, FAKE, FAKE,
+                            None) == binding.PA_ERR_UNSUPPORTED
