@@ -81,7 +81,7 @@ typedef struct pa_plan {
     int page_size;          /* tokens per page (16) */
     int num_pages;          /* pages in the K (and V) pool */
     int max_pages_per_seq;  /* row length of block_tables */
-    int max_context_len;    /* upper bound on every context_lens[b] */
+    int max_context_len;    /* upper bound on every context_lens[b]; at most 2^31 - 16 */
     int window;             /* sliding window in tokens, 0 = whole context */
     int partition_size;     /* tokens per partition, a multiple of page_size */
     int num_partitions;     /* partitions per (sequence, KV head); 1 = no split, no merge */

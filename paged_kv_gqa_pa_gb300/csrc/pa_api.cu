@@ -245,16 +245,13 @@ int attend_ctas_per_sm(int kernel, int dtype, int D, int G, bool rope) {
     }
 }
 
-// Pages a sequence can attend: ceil(Lmax / ps), or with a window at most
-// ceil((window - 1) / ps) + 1 (the window need not start on a page edge).
+// Pages a sequence can attend, at least one: what a plan is made for.
 static int attended_span_pages(int max_context_len, int window) {
-    int span = (max_context_len + kPageSize - 1) / kPageSize;
-    if (window > 0) {
-        const int wspan = (window - 1 + kPageSize - 1) / kPageSize + 1;
-        if (wspan < span) span = wspan;
-    }
-    return span < 1 ? 1 : span;
+    return std::max(1, attended_pages(max_context_len, window));
 }
+
+// Positions, and lengths rounded up to whole pages, are counted in 32 bits.
+constexpr int kMaxContextLen = INT_MAX - (kPageSize - 1);
 
 // CTAs per (KV head, head chunk) of a work-balanced plan, or 0 where none can
 // be made: the tensor-core kernel without rotary embedding (its rotary
@@ -554,7 +551,7 @@ int pa_plan_ex(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
         return PA_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 256)
         return PA_ERR_UNSUPPORTED;
-    if (page_size != kPageSize) return PA_ERR_UNSUPPORTED;
+    if (page_size != kPageSize || max_context_len > kMaxContextLen) return PA_ERR_UNSUPPORTED;
     bool want_balanced = partition_size == PA_PARTITION_BALANCED;
     if (want_balanced) partition_size = 0;
     bool auto_split = false;  // the automatic plan is a whole-wave fixed split
@@ -816,6 +813,7 @@ static int check_plan(const pa_plan_t* plan) {
         plan->num_pages <= 0 ||
         plan->max_pages_per_seq <= 0 || plan->max_context_len < 0 || plan->window < 0)
         return PA_ERR_INVALID_ARG;
+    if (plan->max_context_len > kMaxContextLen) return PA_ERR_UNSUPPORTED;
     if (plan->head_dim != 64 && plan->head_dim != 96 && plan->head_dim != 128 &&
         plan->head_dim != 256)
         return PA_ERR_UNSUPPORTED;

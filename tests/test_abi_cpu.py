@@ -531,3 +531,33 @@ def test_deep_ring_cluster_instance_for_small_cluster_grids():
     d64 = plan(1, 64, 16384)
     d64.deep_ring = 1
     assert _call_decode(d64) == binding.PA_ERR_INVALID_ARG
+
+
+def _same_plan(a, b, but=()):
+    a, b = a.as_dict(), b.as_dict()
+    assert {k for k in a if a[k] != b[k]} <= set(but), (a, b)
+
+
+@pytest.mark.parametrize("B,L,S", [(1, 20, 0), (1, 3060, 0), (4, 100000, 0), (4, 8192, 512),
+                                   (8, 4096, binding.PA_PARTITION_BALANCED)])
+@pytest.mark.parametrize("rope", [0.0, 10000.0])
+def test_a_window_that_holds_everything_plans_like_none(B, L, S, rope):
+    if S < 0 and rope:
+        pytest.skip("work-balanced plans are without rotary embedding")
+    shapes = (B, 24, 4, 128, 16, 1 << 16, 6250, L)
+    want = pa.pa_plan_ex(*shapes, 0, S, 152, rope_theta=rope)
+    for window in (L + 16, 1 << 20, 2**31 - 16, 2**31 - 15, 2**31 - 1):
+        _same_plan(pa.pa_plan_ex(*shapes, window, S, 152, rope_theta=rope), want, ("window",))
+
+
+def test_the_longest_lengths():
+    # Lengths rounded up to whole pages have to fit an int.
+    long = (1, 8, 8, 128, 16, 1 << 16, 1 << 27)
+    p = pa.pa_plan(*long, 2**31 - 16, 4096, 0, 152)
+    _same_plan(p, pa.pa_plan(*long, 100000, 4096, 0, 152), ("max_context_len",))
+    for L in (2**31 - 15, 2**31 - 1):
+        with pytest.raises(pa.PAError) as e:
+            pa.pa_plan(*long, L, 4096, 0, 152)
+        assert e.value.status == binding.PA_ERR_UNSUPPORTED
+    p.max_context_len = 2**31 - 1  # an edited plan
+    assert _call_decode(p) == binding.PA_ERR_UNSUPPORTED

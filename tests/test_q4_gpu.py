@@ -625,3 +625,31 @@ def test_plans_for_other_sm_counts():
         pa.pa_q4_decode(plan, tq, cache, torch.from_numpy(bt).cuda(),
                         torch.from_numpy(lens).cuda(), 0.1, 0, out, lse, ws)
         check((out.double().cpu().numpy(), lse.double().cpu().numpy(), pa.pa_get_error(ws)), want)
+
+
+@pytest.mark.parametrize("short_by,window", [(0, 100), (1, 7), (15, 333), (16, 1), (37, 2)])
+def test_windows_at_the_longest_lengths(short_by, window):
+    # 2^31 - 16 tokens, a table of 2^27 entries whose last pages are there: the same rows as of a
+    # sequence of 400 tokens with these pages.  Both caches.
+    D, maxp, small = 128, 1 << 27, 25
+    q, cache, bt, lens = make_decode(47, [16 * small], 8, 2, D, "f16")
+    lens = lens - short_by
+    want = ref.decode(q, cache.cpu().numpy(), bt, lens, 0.1, window, "f16")
+    table = torch.zeros(1, maxp, dtype=torch.int32, device="cuda")
+    table[0, maxp - 1 - small:maxp - 1] = torch.from_numpy(bt[0]).cuda()
+    long = torch.full((1,), 2 ** 31 - 16 - short_by, dtype=torch.int32, device="cuda")
+    tq = to_t(q, "f16")
+    k, v = ref.unpack(cache.cpu().numpy().reshape(-1, 20 * D), D, "f16")
+    k, v = (to_t(np.nan_to_num(x), "f16").view(cache.shape[0], 2, 16, D) for x in (k, v))
+    for four in (True, False):
+        if four:
+            plan = pa.pa_q4_plan(1, 8, 2, D, 16, cache.shape[0], maxp, 2 ** 31 - 16, window)
+        else:
+            plan = pa.pa_plan(1, 8, 2, D, 16, cache.shape[0], maxp, 2 ** 31 - 16, window)
+        ws = pa.new_workspace(plan, "cuda")
+        out, lse = torch.full_like(tq, float("nan")), torch.empty(1, 8, device="cuda")
+        if four:
+            pa.pa_q4_decode(plan, tq, cache, table, long, 0.1, window, out, lse, ws)
+        else:
+            pa.pa_decode(plan, tq, k, v, table, long, 0.1, window, out, lse, ws)
+        check((out.double().cpu().numpy(), lse.double().cpu().numpy(), pa.pa_get_error(ws)), want)
