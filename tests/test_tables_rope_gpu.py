@@ -1,5 +1,9 @@
 """GPU tests of pa_extend_tables and pa_rope_axes, and of a serving loop that
 uses the operators of include/pa_q4.h together."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -79,6 +83,18 @@ def test_tables(B, maxp, past_max, new_max, pad):
 def test_tables_prompt_larger_than_a_grid_row():
     past, new, free, pages, bt, n = requests(3, 3, 5000, 10, 70000)
     check_tables(past, new, free, pages, bt, n)
+
+
+@pytest.mark.parametrize("B", [6015, 6016, 6135, 6136, 6139, 6143, 6144])
+def test_tables_of_a_batch_around_48_kb(B):
+    # In a process of its own: the kernel's shared memory limit, once raised, stays raised.
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = ("import sys; sys.path[:0] = [%r, %r]\n"
+            "import test_tables_rope_gpu as t\n"
+            "past, new, free, pages, bt, n = t.requests(%d, %d, 3, 40, 2)\n"
+            "assert t.check_tables(past, new, free, pages, bt, n)[6] == 0\n"
+            % (os.path.dirname(here), here, B, B))
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
 
 
 def test_tables_refusals():
