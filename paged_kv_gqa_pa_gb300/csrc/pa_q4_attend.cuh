@@ -71,6 +71,10 @@ constexpr int q4_short(int D) { return D == 256 ? 16 : 24; }
 // 37.8, 37.8, 256 of up to 512 45.5, 41.0, 39.7, 39.3, 38.4, 38.4.
 constexpr int kQ4Start = 12;
 constexpr int kQ4StagedPages = 512;  // page ids a CTA stages at a time
+// The running maximum (log2 domain) before any score: below every score that
+// counts, and finite, so that a score of -inf (a product beyond fp32) is further
+// below it and weighs nothing.
+constexpr float kQ4NoMax = -3e38f;
 
 struct Q4AttendParams {
     const void* q;
@@ -347,7 +351,7 @@ template <int D, typename T>
 __device__ __forceinline__ void q4_finish_unit(const Q4AttendParams& p, int b, int h0, int u,
                                                int lane, float top, float sum, float4 o) {
     if (2 * (lane & 3) + (u & 1) >= p.G || u >= Q4Cfg<D>::kUnits) return;
-    q4_store_unit<D, T>(p, b, h0, u, lane, o, 1.f / sum);
+    q4_store_unit<D, T>(p, b, h0, u, lane, o, sum == 0.f ? 0.f : 1.f / sum);
     if (u < 2 && lane < 4)
         p.lse[(size_t)b * p.Hq + h0 + 2 * lane + u] = (top + log2f(sum)) * 0.69314718055994531f;
 }
@@ -671,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
                 for (int i = 0; i < 4; ++i) acc[w][u][i] = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) lacc[i] = 0.f;
-        m0 = m1 = -INFINITY;
+        m0 = m1 = kQ4NoMax;
         l0 = l1 = 0.f;
         bad = dead;
     };
@@ -766,8 +770,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
                 x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, k));
             }
             const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-            const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0);
-            const float f1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
+            const float f0 = ex2(m0 - n0), f1 = ex2(m1 - n1);
             m0 = n0;
             m1 = n1;
             l0 *= f0;
@@ -904,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, Q4Cfg<D>::kMinBlocks)
                 wsum += f * x[2];
                 if (w == warp) own[k] = f;
             }
-            inv[k] = 1.f / wsum;
+            inv[k] = wsum == 0.f ? 0.f : 1.f / wsum;  // (0: no score above -inf)
         }
 #pragma unroll
         for (int u = 0; u < Cfg::kUnits; ++u)

@@ -653,3 +653,30 @@ def test_windows_at_the_longest_lengths(short_by, window):
         else:
             pa.pa_decode(plan, tq, k, v, table, long, 0.1, window, out, lse, ws)
         check((out.double().cpu().numpy(), lse.double().cpu().numpy(), pa.pa_get_error(ws)), want)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("n", [256, 1999])
+@pytest.mark.parametrize("where", ["first", "last", "alternate pages", "alternate tokens"])
+@pytest.mark.parametrize("cluster", [None, 0])
+def test_decode_scores_below_fp32(D, n, where, cluster):
+    # q k of some tokens is beyond fp32 (bf16 reaches that): -inf, which weighs nothing, also where
+    # it is all that a warp has met so far.  The rest of the row is as without these tokens.
+    dtype, g = "bf16", np.random.default_rng(n)
+    k, v = kv_values(g, (n, 2, D), dtype), kv_values(g, (n, 2, D), dtype)
+    at = np.arange(n)
+    low = {"first": at < 128, "last": at >= n - 128, "alternate pages": at // 16 % 2 == 0,
+           "alternate tokens": at % 2 == 1}[where]
+    k[:, :, :32] = 0
+    k[low, :, 0] = 2.0 ** 119
+    q = ref.rn(g.standard_normal((1, 8, D)), dtype)
+    q[:, :, 0] = -2.0 ** 20
+    pages = -(-n // 16)
+    cache = torch.full((pages, 2, 20 * D), 255, dtype=torch.uint8, device="cuda")
+    pa.pa_q4_write(to_t(k, dtype), to_t(v, dtype), torch.arange(n, device="cuda"), cache)
+    bt, lens = np.arange(pages, dtype=np.int32)[None], np.array([n], np.int32)
+    kk, vv = (x.reshape(pages, 2, 16, D).transpose(0, 2, 1, 3).reshape(-1, 2, D)[:n][~low]
+              for x in ref.unpack(cache.cpu().numpy().reshape(-1, 20 * D), D, dtype))
+    want = [ref.attend(q[0, 4 * h:4 * h + 4], kk[:, h], vv[:, h], D ** -0.5, dtype) for h in (0, 1)]
+    check(run_decode(q, cache, bt, lens, D ** -0.5, 0, dtype, cluster=cluster),
+          [np.concatenate([w[i] for w in want])[None] for i in range(4)])
