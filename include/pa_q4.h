@@ -24,9 +24,13 @@
  *     s = RN_T((mx - mn) / 15)
  *     z = RN_T(mn - 16 s)
  *     c = min(15, max(0, rint((x - z) / s - 16))), ties to even; 0 if s = 0
- * so that an element within the limits comes back within about half a step s:
- * rounding z and s moves the grid's ends by at most s / 64 in fp16 and s / 8
- * in bf16 where the group straddles zero, and the value itself is rounded.
+ * so that an element within the limits comes back within about half a step s,
+ * and the value itself is rounded.  Rounding z and s moves the grid's ends,
+ * where the group straddles zero and s is a normal number of T, by at most
+ *     fp16: s / 64 at the low end, s / 43 at the high end
+ *     bf16: s / 8 at the low end, s / 5 at the high end
+ * (u = 2^-11 or 2^-8 being half a step of rounding: z, at most 31 s (1 + u / 2),
+ * is off by u of that, and at the high end come 15 times s's own u s).
  * Elements beyond the limits, infinities among them, come back as the grid's
  * ends; a group that holds a NaN comes back as NaN.  The 16 in 16 + c is the
  * leading bit of a 16-bit float whose mantissa holds c, so the kernels make

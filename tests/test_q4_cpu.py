@@ -442,3 +442,25 @@ def test_plan_of_the_longest_lengths(lib):
     few.max_context_len = INT_MAX  # an edited plan
     assert lib.pa_q4_decode(ctypes.byref(few), FAKE, FAKE, FAKE, FAKE, 1.0, 100, FAKE, FAKE, FAKE,
                             None) == binding.PA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_the_grids_ends_move_no_further_than_the_header_says(dtype):
+    text = open(os.path.join(ROOT, "include", "pa_q4.h")).read()
+    name = {"f16": "fp16", "bf16": "bf16"}[dtype]
+    low, high = re.search(name + r": s / (\d+) at the low end, s / (\d+) at the high end", text).groups()
+    g = np.random.default_rng(2)
+    worst = [0.0, 0.0]
+    for i in range(60000):
+        mn, mx = -g.uniform(0.001, 1), g.uniform(0.001, 1)
+        if i % 3 == 0:  # a greatest element just above zero: z is largest there
+            mx = 10.0 ** g.uniform(-6, -2)
+        mn, mx = (float(ref.rn(v * 2.0 ** g.integers(-3, 8), dtype)) for v in (mn, mx))
+        s = float(ref.rn((mx - mn) / 15, dtype))
+        z = float(ref.rn(mn - 16 * s, dtype))
+        if s < 2.0 ** -14:
+            continue
+        worst = [max(worst[0], abs(z + 16 * s - mn) / s), max(worst[1], abs(z + 31 * s - mx) / s)]
+    assert worst[0] <= 1 / int(low) and worst[1] <= 1 / int(high), worst
+    # ... and not much less far
+    assert worst[0] > 0.7 / int(low) and worst[1] > 0.7 / int(high), worst
