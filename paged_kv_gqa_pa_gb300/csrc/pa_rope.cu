@@ -16,9 +16,11 @@
 //
 // Angles: the frequency as a fraction of a turn is a 64-bit fixed-point
 // number f = round(2^64 theta^(-2 i / R) / (2 pi)), so position * f modulo
-// 2^64 is the angle modulo one turn, exactly but for f's rounding (2^-33 of a
-// turn at the largest position); its top 32 bits, as a signed fraction, go to
-// fp32 and sincospif.
+// 2^64 is the angle modulo one turn, exactly but for f's rounding (2^-34 of a
+// turn at the largest position).  Its top 32 bits (2^-32 of a turn), as a signed
+// fraction, go to fp32 (half a step: 2^-26 of a turn next to half a turn, less
+// nearer to 0) and sincospif.  f has to be good to 64 bits, more than a double
+// holds: the host works it out in pairs of doubles.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -186,6 +188,54 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_axes_kernel(const RopeAx
     }
 }
 
+// A number as the unevaluated sum of two doubles, about 104 bits.  (Written with
+// explicit fma, so that every compiler gives the same bits.)
+struct Pair {
+    double hi, lo;
+};
+
+static Pair mul(const Pair& a, const Pair& b) {
+    const double p = a.hi * b.hi;
+    const double e = fma(a.hi, b.lo, fma(a.lo, b.hi, fma(a.hi, b.hi, -p)));
+    const double s = p + e;
+    return {s, e - (s - p)};
+}
+
+// 2^64 times x modulo one turn, rounded down, and what that leaves (0 <= rest < 1).
+static unsigned long long turn64(double x, double* rest) {
+    const double a = (x - rint(x)) * 18446744073709551616.0;  // exact, -2^63 .. 2^63
+    const double whole = floor(a);
+    *rest = a - whole;
+    return whole >= 9223372036854775808.0 ? 1ull << 63 : (unsigned long long)(long long)whole;
+}
+
+// round(2^64 theta^(-2 i / R) / (2 pi)) modulo 2^64, i < R / 2: all 64 bits for bases
+// from 1e-3 on (below, a position is so many turns that fewer are left behind the
+// point).  2 us for 128 frequencies; with a pow for each it was 4.
+static void rope_frequencies(float theta, int R, unsigned long long* freq) {
+    const int half = R / 2;
+    // r = theta^(-1 / half): the double r0 and one step of Newton's method,
+    // r0 (1 + (1 - theta r0^half) / half), whose error is the square of r0's.
+    const double r0 = pow((double)theta, -1.0 / half);
+    Pair power = {1.0, 0.0}, base = {r0, 0.0};
+    for (int n = half; n; n >>= 1) {
+        if (n & 1) power = mul(power, base);
+        base = mul(base, base);
+    }
+    const Pair one = mul(power, {(double)theta, 0.0});
+    const double step = ((1.0 - one.hi) - one.lo) / half * r0;
+    const double r_hi = r0 + step;
+    const Pair r = {r_hi, step - (r_hi - r0)};
+    Pair f = {0.15915494309189535, -9.839338337591243e-18};  // 1 / (2 pi)
+    for (int i = 0; i < half; ++i) {
+        double rest_hi, rest_lo;
+        freq[i] = turn64(f.hi, &rest_hi);
+        freq[i] += turn64(f.lo, &rest_lo);
+        freq[i] += (unsigned long long)rint(rest_hi + rest_lo);
+        f = mul(f, r);
+    }
+}
+
 }  // namespace pa
 
 using namespace pa;
@@ -247,16 +297,13 @@ extern "C" int pa_rope_axes(int num_tokens, int num_q_heads, int num_kv_heads, i
     if (has_k) bits |= (uintptr_t)k | (uintptr_t)k_out;
     if ((bits & 15u) || ((uintptr_t)positions & 3u)) return PA_ERR_INVALID_ARG;
     // Frequencies as 64-bit fractions of a turn; the table of the last (base,
-    // rotary dim) this thread used is kept.
+    // rotary dim) this thread used is kept.  (A model whose layers alternate
+    // between two bases pays the table, 2 us of host time, in every call.)
     thread_local float t_theta = 0.f;
     thread_local int t_R = 0;
     thread_local unsigned long long t_freq[kMaxRopePairs];
     if (t_theta != theta || t_R != rotary_dim) {
-        for (int i = 0; i < half; ++i) {
-            const double f = pow((double)theta, -2.0 * i / rotary_dim) / (2.0 * M_PI);
-            const double frac = f - floor(f);  // (a base below 1 turns more than once a position)
-            t_freq[i] = (unsigned long long)(frac * 18446744073709551616.0);
-        }
+        rope_frequencies(theta, rotary_dim, t_freq);
         t_theta = theta;
         t_R = rotary_dim;
     }

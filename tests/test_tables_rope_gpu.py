@@ -241,6 +241,40 @@ def test_rope_far_positions():
     rope_case(4, 50, 2, 1, 64, 64, (32,), "f32", top=1 << 24, theta=500000.0)
 
 
+PI_60 = "3.14159265358979323846264338327950288419716939937510582097494"
+
+
+@pytest.mark.parametrize("theta,rot", [(10000.0, 128), (500000.0, 128), (1e6, 256), (10000.0, 96),
+                                       (2.0, 16)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_rope_far_positions_are_turned_to_the_last_bit(theta, rot, sign):
+    """For each pair a position near 2^31 whose angle is almost a whole number of turns: its sine is
+    small, so fp32 hides nothing of what the angle is off by.  The frequencies are taken from 60
+    digits; 2^-65 of a turn of theirs times 2^31 positions, and the angle's 32 bits, are 2^-31.7 of
+    a turn; the sine itself is good to 2^-21."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    half = rot // 2
+    ln = Decimal(theta).ln()
+    freq = [int(((ln * Decimal(-2 * i) / Decimal(rot)).exp() / (2 * Decimal(PI_60)) *
+                 Decimal(2) ** 64).to_integral_value()) for i in range(half)]
+    near = np.arange(2 ** 31 - 2 ** 23, 2 ** 31, dtype=np.uint64)
+    pos, turns = [], []
+    for f in freq:
+        t = (near * np.uint64(f)).view(np.int64)  # modulo 2^64: signed fractions of a turn
+        j = int(np.argmin(np.abs(t)))
+        pos.append(int(near[j]))
+        turns.append(int(t[j]) / 2.0 ** 64)
+    x = torch.zeros(half, 1, rot, device="cuda")
+    x[:, :, :half] = torch.eye(half, device="cuda")[:, None]  # token i: only pair i
+    pa.pa_rope_axes(x, None, i32([[sign * p for p in pos]]), (half,), theta)
+    got = x[torch.arange(half), 0, half + torch.arange(half)].double().cpu().numpy()
+    want = np.sin(2 * np.pi * sign * np.array(turns))
+    assert np.abs(want).max() < 0.01
+    assert (np.abs(got - want) <= 2 * np.pi * 2.0 ** -31.7 + np.abs(want) * 2.0 ** -21).all(), \
+        np.abs(got - want).max()
+
+
 def test_rope_backward_is_the_inverse():
     # A rotation's transpose is its inverse: against the formula and against differences.
     g = np.random.default_rng(9)
