@@ -3,15 +3,20 @@
 Each translation unit under csrc/ compiles in parallel; the objects link into
 one shared library with the static CUDA runtime.  csrc/pa_pyfast.cpp, the
 argument marshalling of q4.py, becomes a Python extension beside it where the
-interpreter's and torch's headers are installed (q4.py works without it).  Usage:
+interpreter's and torch's headers are installed (q4.py works without it).  It reads
+torch's tensors by their layout and calls the library by the headers' prototypes, so
+its file is named by a digest of all that it was compiled from: one of other sources,
+another torch or another interpreter is never loaded.  Usage:
     python -m paged_kv_gqa_pa_gb300.build [--force] [--verbose]
 """
 from __future__ import annotations
 
 import argparse
 import glob
+import hashlib
 import importlib.util
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -23,7 +28,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpa_gb300.so")
 PYFAST_SRC = os.path.join(CSRC, "pa_pyfast.cpp")
-PYFAST = os.path.join(BUILD, "_pa_fast.so")
+PYFAST_HEADERS = [os.path.join(ROOT, "include", h) for h in ("pa.h", "pa_q4.h")]
+PYFAST_FLAGS = ["-O2", "-std=c++17", "-shared", "-fPIC"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -54,44 +60,60 @@ def _cuda_include():
     return os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
 
 
+def pyfast_path():
+    """Where the marshalling extension of these sources, this torch and this interpreter lies,
+    built or not; None without torch."""
+    torch_dir = _torch_dir()
+    version = os.path.join(torch_dir, "version.py") if torch_dir else ""  # (its git revision too)
+    if not os.path.exists(version):
+        return None
+    h = hashlib.sha256(repr((sys.implementation.cache_tag, platform.machine(),
+                             PYFAST_FLAGS)).encode())
+    for path in [version, PYFAST_SRC, *PYFAST_HEADERS]:
+        with open(path, "rb") as f:
+            h.update(hashlib.sha256(f.read()).digest())
+    return os.path.join(BUILD, f"_pa_fast-{h.hexdigest()[:16]}.so")
+
+
 def _start_pyfast(force: bool, verbose: bool):
     """A running compilation of the marshalling extension and its output file; None if it is
-    up to date, or without a C++ compiler or the interpreter's or torch's headers."""
+    there, or without a C++ compiler or the interpreter's or torch's headers.  Extensions of
+    other sources do not stay behind."""
+    path = pyfast_path()
+    for old in glob.glob(os.path.join(BUILD, "_pa_fast*.so")):
+        if old != path:
+            os.remove(old)
     inc, torch_dir = sysconfig.get_paths()["include"], _torch_dir()
     cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
-    if cxx is None or torch_dir is None or not os.path.exists(os.path.join(inc, "Python.h")):
+    if path is None or cxx is None or not os.path.exists(os.path.join(inc, "Python.h")):
         return None
-    header = os.path.join(torch_dir, "include", "torch", "csrc", "autograd", "python_variable.h")
-    if not os.path.exists(header):
+    if not os.path.exists(os.path.join(torch_dir, "include", "torch", "csrc", "autograd",
+                                       "python_variable.h")):
         return None
-    deps = [PYFAST_SRC, os.path.join(ROOT, "include", "pa.h"), header,
-            os.path.join(ROOT, "include", "pa_q4.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(PYFAST) and all(
-            os.path.getmtime(p) <= os.path.getmtime(PYFAST) for p in deps):
+    if not force and os.path.exists(path):
         return None
     os.makedirs(BUILD, exist_ok=True)
-    tmp = PYFAST + f".tmp{os.getpid()}"
-    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-I", inc,
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = [cxx, *PYFAST_FLAGS, "-I", inc,
            "-isystem", os.path.join(torch_dir, "include"),
            "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            "-isystem", _cuda_include(), "-o", tmp, PYFAST_SRC,
            "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
-    return subprocess.Popen(cmd), tmp
+    return subprocess.Popen(cmd), tmp, path
 
 
 def _finish_pyfast(job) -> None:
     if job is None:
         return
-    proc, tmp = job
+    proc, tmp, path = job
     if proc.wait() == 0:
-        os.replace(tmp, PYFAST)
-    else:  # (an older one must not stay behind)
+        os.replace(tmp, path)
+    else:
         print("the marshalling extension was not built; q4.py goes without it", file=sys.stderr)
-        for path in (tmp, PYFAST):
-            if os.path.exists(path):
-                os.remove(path)
+        if os.path.exists(tmp):
+            os.remove(tmp)
 
 
 def up_to_date() -> bool:

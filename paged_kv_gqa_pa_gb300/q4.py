@@ -65,10 +65,11 @@ _fast = None
 
 
 def _load_fast(lib):
-    if _raw_stream is None or not os.path.exists(_build.PYFAST):
+    path = _build.pyfast_path()  # (of these sources and this torch, or none)
+    if _raw_stream is None or path is None or not os.path.exists(path):
         return None
     try:
-        spec = importlib.util.spec_from_file_location("_pa_fast", _build.PYFAST)
+        spec = importlib.util.spec_from_file_location("_pa_fast", path)
         fast = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(fast)
     except ImportError:  # built for another interpreter

@@ -464,3 +464,44 @@ def test_the_grids_ends_move_no_further_than_the_header_says(dtype):
     assert worst[0] <= 1 / int(low) and worst[1] <= 1 / int(high), worst
     # ... and not much less far
     assert worst[0] > 0.7 / int(low) and worst[1] > 0.7 / int(high), worst
+
+
+@pytest.fixture
+def build_tree(tmp_path, monkeypatch):
+    """build.py over copies of the extension's sources, a torch of its own and an empty _build."""
+    for name in ("pa_pyfast.cpp", "pa.h", "pa_q4.h"):
+        (tmp_path / name).write_text("// " + name)
+    fake = tmp_path / "torch"
+    fake.mkdir()
+    (fake / "version.py").write_text("__version__ = '1.0'")
+    monkeypatch.setattr(pa_build, "BUILD", str(tmp_path / "_build"))
+    monkeypatch.setattr(pa_build, "PYFAST_SRC", str(tmp_path / "pa_pyfast.cpp"))
+    monkeypatch.setattr(pa_build, "PYFAST_HEADERS", [str(tmp_path / "pa.h"), str(tmp_path / "pa_q4.h")])
+    monkeypatch.setattr(pa_build, "_torch_dir", lambda: str(fake))
+    (tmp_path / "_build").mkdir()
+    return tmp_path
+
+
+def test_an_extension_of_other_sources_or_another_torch_is_not_loaded(build_tree, lib):
+    for changed in ("pa_pyfast.cpp", "pa.h", "pa_q4.h", os.path.join("torch", "version.py")):
+        there = pa_build.pyfast_path()
+        with open(there, "w") as f:  # (loading it would be an error)
+            f.write("an extension of the sources as they were")
+        with open(build_tree / changed, "a") as f:
+            f.write("\n# changed")
+        assert pa_build.pyfast_path() != there, changed
+        assert q4._load_fast(lib) is None, changed
+    os.remove(build_tree / "torch" / "version.py")
+    assert pa_build.pyfast_path() is None and q4._load_fast(lib) is None
+
+
+def test_a_stale_extension_goes_even_where_none_can_be_built(build_tree, monkeypatch):
+    old = [build_tree / "_build" / n for n in ("_pa_fast.so", "_pa_fast-0123456789abcdef.so")]
+    for path in old:
+        path.write_text("")
+    current = pa_build.pyfast_path()
+    open(current, "w").close()
+    monkeypatch.delenv("CXX", raising=False)
+    monkeypatch.setattr(pa_build.shutil, "which", lambda name: None)
+    assert pa_build._start_pyfast(False, False) is None
+    assert not any(p.exists() for p in old) and os.path.exists(current)
