@@ -147,8 +147,14 @@ int pa_q4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
  * arguments, windows, empty sequences (out = 0, lse = -inf), error word and
  * NaN rows for a bad page id or length.  Cells of tokens outside a sequence's
  * attended range are not used, whatever they hold.
- * The pages of the whole batch are shared out evenly over the CTAs on the
- * device, from the actual lengths.  workspace: plan->workspace_bytes, 16-byte
+ * Precision, as pa_decode's: scores, maxima, sums and the lse are fp32.  In the
+ * product with V the weights are rounded, to fp16 (11 bits) for fp16 caches and
+ * to two bf16, a head and a rest (16 bits), for bf16 ones, and normalised by the
+ * sum of the rounded weights; the sums are fp32 and rounded to T once.  An fp16
+ * row is then off by up to about 3e-4 of its norm, of which 2e-4 are its own
+ * rounding.
+ * The work of the whole batch is shared out over the CTAs on the device, from
+ * the actual lengths (see ctas_per_group and cluster).  workspace: plan->workspace_bytes, 16-byte
  * aligned, the first plan->ctrl_bytes zero before the first call; concurrent
  * calls must not share one, and one that served another plan must have its
  * ctrl_bytes zeroed first.
