@@ -95,7 +95,8 @@ int pa_q4_write(int num_tokens, int num_kv_heads, int head_dim, int page_size, i
 /*
  * The reverse: rows of K and V that the cache stands for, by slot.  A row
  * whose slot is -1 is filled with zeros, one with a bad slot with NaN
- * (PA_DEVERR_BAD_SLOT).  Slots may repeat.  k, v, strides as in pa_q4_write.
+ * (PA_DEVERR_BAD_SLOT).  Slots may repeat.  k, v, strides as in pa_q4_write;
+ * k and v must not overlap.
  */
 int pa_q4_read(int num_tokens, int num_kv_heads, int head_dim, int page_size, int num_pages,
                int dtype, const void* cache, const int64_t* slots, void* k, long long k_stride,
@@ -214,7 +215,8 @@ int pa_extend_tables(int batch, int max_pages_per_seq, int page_size, int num_pa
  *                consecutive tokens q_stride (k_stride) elements apart; 16-byte
  *                aligned, strides multiples of 16 bytes
  *   q_out, k_out the same, with strides of their own; may equal q and k
- *                (in place) with the same strides, must not overlap them otherwise
+ *                (in place) with the same strides, must not overlap them otherwise,
+ *                nor each other
  *   positions    int32 [num_axes, num_tokens], any value
  * num_q_heads or num_kv_heads may be 0 (then q or k is not used).
  * rotary_dim: a multiple of 16, at most head_dim (at most 256, a multiple of

@@ -328,6 +328,7 @@ static int q4_cache_call(bool write, int num_tokens, int num_kv_heads, int head_
         return PA_ERR_INVALID_ARG;
     if (num_tokens == 0) return PA_OK;
     if (!k || !v || !slots || !cache) return PA_ERR_INVALID_ARG;
+    if (!write && k == v) return PA_ERR_INVALID_ARG;  // (two outputs)
     if (((uintptr_t)k & 15u) || ((uintptr_t)v & 15u) || ((uintptr_t)cache & 15u) ||
         ((uintptr_t)slots & 7u) || ((uintptr_t)device_error & 3u))
         return PA_ERR_INVALID_ARG;

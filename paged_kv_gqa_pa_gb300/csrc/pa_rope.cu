@@ -292,6 +292,8 @@ extern "C" int pa_rope_axes(int num_tokens, int num_q_heads, int num_kv_heads, i
     if (num_tokens == 0 || (!has_q && !has_k)) return PA_OK;
     if (!positions || (has_q && (!q || !q_out)) || (has_k && (!k || !k_out)))
         return PA_ERR_INVALID_ARG;
+    // (in place with k = q, or into one output, q's rows and k's would be written over one another)
+    if (has_q && has_k && q_out == k_out) return PA_ERR_INVALID_ARG;
     uintptr_t bits = 0;
     if (has_q) bits |= (uintptr_t)q | (uintptr_t)q_out;
     if (has_k) bits |= (uintptr_t)k | (uintptr_t)k_out;

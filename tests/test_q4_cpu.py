@@ -505,3 +505,16 @@ def test_a_stale_extension_goes_even_where_none_can_be_built(build_tree, monkeyp
     monkeypatch.setattr(pa_build.shutil, "which", lambda name: None)
     assert pa_build._start_pyfast(False, False) is None
     assert not any(p.exists() for p in old) and os.path.exists(current)
+
+
+def test_outputs_on_one_another_are_refused(lib):
+    IA = binding.PA_ERR_INVALID_ARG
+    assert lib.pa_q4_read(4, 2, 128, 16, 8, 0, FAKE, FAKE, FAKE, 256, FAKE, 256, None, None) == IA
+    arr = (ctypes.c_int * 1)(64)
+
+    def rope(q, k, qo, ko):
+        return lib.pa_rope_axes(4, 2, 2, 128, 128, 1, arr, 0, 0, 1e4, 0, q, 256, k, 256, FAKE, qo, 256,
+                                ko, 256, None)
+
+    assert rope(FAKE, FAKE, FAKE, FAKE) == IA  # the same rows as q and as k, in place
+    assert rope(FAKE, FAKE + 4096, FAKE + 8192, FAKE + 8192) == IA
