@@ -136,7 +136,9 @@ typedef struct pa_q4_plan {
 /*
  * Plan decode calls over a 4-bit cache (host only, no device access unless
  * num_sms == 0, which queries the current device).  The arguments mean what
- * they mean to pa_plan_ex.
+ * they mean to pa_plan_ex.  More than 8 query heads per KV head go in the fewest
+ * equal chunks of at most 8, each of which reads the cache once: 9 as 3 x 3, 15
+ * as 3 x 5, 16 as 2 x 8; a prime above 8 is PA_ERR_UNSUPPORTED.
  */
 int pa_q4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
                int num_pages, int max_pages_per_seq, int max_context_len, int window,

@@ -150,8 +150,11 @@ int pa_q4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
     const int st = q4_check_shapes(&p);
     if (st != PA_OK) return st;
     const int g = num_q_heads / num_kv_heads;
-    const int nchunk = (g + kMaxHeadsPerCta - 1) / kMaxHeadsPerCta;
-    if (g % nchunk != 0) return PA_ERR_UNSUPPORTED;
+    // The fewest equal chunks of at most kMaxHeadsPerCta heads: each reads the cache
+    // once.  (One head at a time, what a prime above that comes to, is refused.)
+    int nchunk = (g + kMaxHeadsPerCta - 1) / kMaxHeadsPerCta;
+    while (g % nchunk != 0) ++nchunk;
+    if (nchunk > 1 && nchunk == g) return PA_ERR_UNSUPPORTED;
     const long long groups = (long long)num_kv_heads * nchunk;
     if (groups > 65535) return PA_ERR_UNSUPPORTED;
     const bool this_device = p.num_sms == 0;

@@ -518,3 +518,14 @@ def test_outputs_on_one_another_are_refused(lib):
 
     assert rope(FAKE, FAKE, FAKE, FAKE) == IA  # the same rows as q and as k, in place
     assert rope(FAKE, FAKE + 4096, FAKE + 8192, FAKE + 8192) == IA
+
+
+def test_plan_cuts_head_groups_into_the_fewest_equal_chunks():
+    for g in range(1, 65):
+        chunks = [n for n in range(1, g) if g % n == 0 and g // n <= 8] or ([1] if g == 1 else [])
+        if chunks:
+            assert _plan(num_q_heads=2 * g, num_kv_heads=2).heads_per_cta == g // chunks[0], g
+        else:  # 11, 13, 17, ...
+            with pytest.raises(pa.PAError) as e:
+                _plan(num_q_heads=2 * g, num_kv_heads=2)
+            assert e.value.status == binding.PA_ERR_UNSUPPORTED

@@ -680,3 +680,10 @@ def test_decode_scores_below_fp32(D, n, where, cluster):
     want = [ref.attend(q[0, 4 * h:4 * h + 4], kk[:, h], vv[:, h], D ** -0.5, dtype) for h in (0, 1)]
     check(run_decode(q, cache, bt, lens, D ** -0.5, 0, dtype, cluster=cluster),
           [np.concatenate([w[i] for w in want])[None] for i in range(4)])
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(9, 1), (30, 2), (18, 1), (22, 1), (50, 2)])
+def test_decode_head_chunks_of_other_sizes(Hq, Hkv):
+    # 3 x 3, 3 x 5, 3 x 6, 11 x 2 and 5 x 5 query heads of a KV head.
+    decode_case(Hq, [300, 17, 64, 0], Hq, Hkv, 96, "f16")
+    decode_case(Hq, [3000, 17, 600], Hq, Hkv, 128, "bf16", window=2000)
