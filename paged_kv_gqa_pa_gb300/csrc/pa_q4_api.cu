@@ -230,7 +230,7 @@ int pa_q4_decode(const pa_q4_plan_t* plan, const void* q, const void* cache,
     if (groups > 65535) return PA_ERR_UNSUPPORTED;
     const Q4WsLayout wl = q4_ws_layout(plan->batch, D, groups, X);
     if (plan->workspace_bytes < wl.total || plan->ctrl_bytes < 0 ||
-        plan->ctrl_bytes < 0 || (size_t)plan->ctrl_bytes < wl.ctrl_bytes)
+        (size_t)plan->ctrl_bytes < wl.ctrl_bytes)
         return PA_ERR_INVALID_ARG;
     if (!workspace) return PA_ERR_WORKSPACE;
     if ((uintptr_t)workspace & 15u) return PA_ERR_INVALID_ARG;
