@@ -10,10 +10,12 @@ element bytes (one K and one V row) per attended token, divided by the time
 per step.
 
 Besides the headline workload, every measured workload gets an entry in
-`per_workload` (graph-timed step, single-call time, plan, and the oracle timed
-on a bounded sample on the host cores), and the line ends with a compact
-`configs` table of the same figures and the pages' own numbers (`context`,
-another GPU under WebGPU: context only).
+`per_workload` (graph-timed step, partition kernel and single call of each
+kernel; compact, so that the line stays a few KB long) and a row in the
+`configs` tables (bandwidth, fractions, plan, and the oracle timed on a bounded
+sample on the host cores); the pages' own numbers are in `context` (another GPU
+under WebGPU: context only).  Everything measured per workload goes to stderr
+as a JSON line of its own.
 
 --impl reference times the fp64 CPU oracle on the host cores instead (the only
 other path that runs the oracle), on bounded samples of the same workload.
@@ -701,6 +703,16 @@ class OracleSampler:
         return 2 * ELEM_BYTES[c.dtype] * c.Hkv * c.D / per_token / 1e9
 
 
+def compact_per_workload(per):
+    """The printed line's `per_workload`: times in us, from the full entries.  (The full ones
+    come to 26 KB, and a reader that keeps the line's last 20 KB finds no JSON there.)"""
+    times = {"us_per_step": "us_per_step", "partition_kernel_us": "partition_kernel_us",
+             "single_call_us": "single_call_us", "host_us_prepared_call": "host_us"}
+    return {name: {"dtype": e["dtype"], "head_dim": e["head_dim"],
+                   **{k: {short: round(e[k][full], 2) for full, short in times.items()}
+                      for k in ("mma", "simt") if k in e}} for name, e in per.items()}
+
+
 def run_reference(args):
     world, rank, local = dist_setup()
     if rank != 0:
@@ -923,9 +935,11 @@ def run_gpu(args):
             "timed_loop": "CUDA graph replays of captured steps" if big else
                           "per-step launches, L2 flushed between steps",
             "clocks": clk.summary(),
-            "per_workload": per,
+            "per_workload": compact_per_workload(per) if per else None,
             "configs_extra": summary_extra,
         }
+        if per:
+            print(json.dumps({"per_workload_detail": per}), file=sys.stderr, flush=True)
         print(json.dumps(line), flush=True)
     if world > 1:
         torch.distributed.destroy_process_group()

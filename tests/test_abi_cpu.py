@@ -561,3 +561,19 @@ def test_the_longest_lengths():
         assert e.value.status == binding.PA_ERR_UNSUPPORTED
     p.max_context_len = 2**31 - 1  # an edited plan
     assert _call_decode(p) == binding.PA_ERR_UNSUPPORTED
+
+
+def test_bench_line_stays_short():
+    """The line's entries per workload: a few KB for all of them, every time there."""
+    import json
+
+    import bench
+    from paged_kv_gqa_pa_gb300 import workloads
+    times = {k: 123.456789 for k in ("us_per_step", "partition_kernel_us", "kv_gbs", "single_call_us",
+                                     "single_call_isolated_us", "host_us_prepared_call")}
+    full = {name: {"dtype": "bf16", "head_dim": 256, "rope_theta": 0.0, "timing": "x" * 700,
+                   "cpu_baseline": {"sample": "x" * 200}, "mma": dict(times), "simt": dict(times)}
+            for name in workloads.WORKLOAD_ORDER + workloads.EXTRA_ORDER}
+    per = bench.compact_per_workload(full)
+    assert list(per) == list(full) and len(json.dumps(per)) < 5000
+    assert all(e[k]["us_per_step"] == 123.46 for e in per.values() for k in ("mma", "simt"))
