@@ -236,7 +236,8 @@ int pa_q4_decode(const pa_q4_plan_t* plan, const void* q, const void* cache,
     if ((uintptr_t)workspace & 15u) return PA_ERR_INVALID_ARG;
     if (plan->batch == 0) return PA_OK;
     if (!q || !cache || !block_tables || !context_lens || !out || !lse) return PA_ERR_INVALID_ARG;
-    if (((uintptr_t)q & 15u) || ((uintptr_t)cache & 15u) || ((uintptr_t)out & 15u))
+    if (((uintptr_t)q & 15u) || ((uintptr_t)cache & 15u) || ((uintptr_t)out & 15u) ||
+        (((uintptr_t)block_tables | (uintptr_t)context_lens | (uintptr_t)lse) & 3u))
         return PA_ERR_INVALID_ARG;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     Q4AttendParams p;

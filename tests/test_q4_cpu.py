@@ -529,3 +529,12 @@ def test_plan_cuts_head_groups_into_the_fewest_equal_chunks():
             with pytest.raises(pa.PAError) as e:
                 _plan(num_q_heads=2 * g, num_kv_heads=2)
             assert e.value.status == binding.PA_ERR_UNSUPPORTED
+
+
+def test_decode_refuses_words_that_are_not_aligned(lib):
+    plan = _plan()
+    for i in (3, 4, 8):  # block_tables, context_lens, lse
+        for off in (1, 2, 3):
+            a = [ctypes.byref(plan), FAKE, FAKE, FAKE, FAKE, 1.0, 0, FAKE, FAKE, FAKE, None]
+            a[i] += off
+            assert lib.pa_q4_decode(*a) == binding.PA_ERR_INVALID_ARG, i
