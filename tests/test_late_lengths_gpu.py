@@ -15,6 +15,7 @@ import paged_kv_gqa_pa_gb300 as pa
 from gpu_helpers import assert_matches_oracle, ensure_built, to_device
 from paged_kv_gqa_pa_gb300 import binding, workloads
 from test_pdl_hints_gpu import _slack_pages, writer  # noqa: F401 (a fixture)
+from test_q4_gpu import make_decode, to_t
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +165,45 @@ def test_extend_tables_right_before_pa_decode(kind, window):
         graph.replay()
         assert same(run.rows(), want[i]), (kind, window, int(i))
     assert int(err[0]) == 0
+
+
+@pytest.mark.parametrize("window", [0, 1000])
+@pytest.mark.parametrize("lens,cluster", [(LENS, None), (LENS, 0), ([40, 3, 0, 300] * 33, None)])
+def test_the_4_bit_decode_behind_a_late_writer(writer, lens, cluster, window):  # noqa: F811
+    """The same sweep for pa_q4_decode, whose early start reads lengths and first ids too."""
+    q, cache, bt, lens = make_decode(1702, lens, 8, 2, 128, "f16")
+    plan = pa.pa_q4_plan(len(lens), 8, 2, 128, 16, cache.shape[0], bt.shape[1], int(lens.max()), window)
+    if cluster == 0:
+        plan.cluster = 0
+    ws, tq = pa.new_workspace(plan, "cuda"), to_t(q, "f16")
+    out, lse = torch.empty_like(tq), torch.empty(len(lens), 8, device="cuda")
+    new_bt, new_cl = torch.from_numpy(bt).cuda(), torch.from_numpy(lens).cuda()
+    now_bt, now_cl = new_bt.clone(), new_cl.clone()
+
+    def run():
+        pa.pa_q4_decode(plan, tq, cache, now_bt, now_cl, 0.1, window, out, lse, ws)
+
+    def rows():
+        torch.cuda.synchronize()
+        assert pa.pa_get_error(ws) == 0
+        return out.clone(), lse.clone()
+
+    run()
+    want = rows()
+    unused = sorted(set(range(cache.shape[0])) - set(bt.ravel().tolist()))  # (NaN scales)
+    old_bt = torch.full_like(new_bt, unused[0])
+    stream = torch.cuda.Stream()
+    for moved in (1, 16, 48, 640):
+        old_cl = (new_cl + moved).clamp(max=int(lens.max()))
+        for delay in range(0, 8001, 500):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                assert writer.launch_delayed_copy(
+                    new_bt.data_ptr(), now_bt.data_ptr(), new_bt.numel(), new_cl.data_ptr(),
+                    now_cl.data_ptr(), new_cl.numel(), delay, stream.cuda_stream) == 0
+                run()
+            for _ in range(2):
+                now_bt.copy_(old_bt)
+                now_cl.copy_(old_cl)
+                graph.replay()
+                assert same(rows(), want), (moved, delay)
