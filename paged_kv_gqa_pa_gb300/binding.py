@@ -212,7 +212,9 @@ class PreparedDecode:
     contents change, their addresses do not).  This object keeps the checked
     ctypes arguments and the plan, so each call is the C call alone: a few
     microseconds of host time instead of the per-tensor checks of pa_decode.
-    The tensors must stay alive and in place while it is used."""
+    The tensors must stay alive and in place while it is used.  Every call goes to
+    the stream of the preparation: `stream`, or without one the stream that was
+    current then (prepare inside torch.cuda.graph what a graph is to capture)."""
 
     def __init__(self, plan, q, k_cache, v_cache, block_tables, context_lens, scale, window, out,
                  lse, workspace, stream=None):

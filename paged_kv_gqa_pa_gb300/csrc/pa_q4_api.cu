@@ -188,8 +188,10 @@ int pa_q4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
     // Clusters against equal ranges, head_dim 128, 8 KV heads: one sequence of 1000
     // tokens 6.2 and 7.2 us, of 2500 7.9 and 7.9, of 4000 9.3 and 8.4; 4 of 1000 7.6
     // and 9.5, of 4000 11.9 and 12.0, of 6000 14.9 and 14.0; 16 of 2500 (bf16) 19.2
-    // and 20.7.  One longer than the rest, 8 in all, of 2000 8.9 and 9.0, of 4000
-    // 11.5 and 9.3.  Clusters that one wave does not hold cost 5 to 10 us (16
+    // and 20.7.  Lengths are known on the device only, so every sequence counts as
+    // the longest: a ragged batch pays for that.  One longer than the rest, 8 in
+    // all, of 2000 8.9 and 9.0, of 4000 11.5 and 9.3 (a caller that knows better
+    // sets cluster 0).  Clusters that one wave does not hold cost 5 to 10 us (16
     // sequences of 1000 tokens, bf16, by 4 CTAs 18.8, by 3 12.5).
     if (batch > 0 && span > q4_short(head_dim)) {
         int c = std::min(kQ4MaxCluster, (span + kWarps - 1) / kWarps);

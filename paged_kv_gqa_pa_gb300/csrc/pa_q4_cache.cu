@@ -9,10 +9,11 @@
 // head's rows are requested before the present ones are worked on.
 //
 // Measured on GB300, 16384 bf16 rows of 4 heads at D 256 (88 MB either way, 13
-// us at the measured copy rate): the writer 31.6 us, bound by what it issues
-// (73 % of the slots; the borders of exact codes are most of it), the reader
-// 16.7 us, bound by memory latency (0.78 of the copy rate).  64 rows of 8 heads
-// at D 128: 1.9 us each, a launch.
+// us at the measured copy rate): the writer 27.3 us, bound by what it issues
+// (71 % of the slots; the borders of exact codes are most of it), the reader
+// 19.1 us, bound by memory latency (0.68 of the copy rate); one behind the
+// other 43.2, since the cells just written are still in L2.  64 rows of 8 heads
+// at D 128: 1.9 and 1.4 us, a launch.
 #include <algorithm>
 
 #include "pa_q4.cuh"
@@ -343,8 +344,9 @@ static int q4_cache_call(bool write, int num_tokens, int num_kv_heads, int head_
     p.n = num_tokens;
     p.Hkv = num_kv_heads;
     p.num_slots = (long long)num_pages * kPageSize;
-    // As many heads in one thread as leave 608 CTAs (four per SM): what is worked
-    // out once per token is then shared, and short inputs still spread out.
+    // As many heads in one thread as leave 608 CTAs (four for each of GB300's 152
+    // SMs): what is worked out once per token is then shared, and short inputs still
+    // spread out.
     // 16384 rows of 4 heads at D 256, written and read: 4 heads a thread 45.4
     // us, 2 heads 49.1, 1 head 61.7.
     const long long ctas = ((long long)num_tokens * (head_dim / 8) + kQ4Threads - 1) / kQ4Threads;

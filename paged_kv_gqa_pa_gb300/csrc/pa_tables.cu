@@ -9,8 +9,8 @@
 // by bisection of the sums.  The token at the start of a page writes that
 // page's table entry; CTA 0 writes what there is per request.
 //
-// Measured on GB300: one request with one token 2.5 us, 512 requests with 52K
-// new tokens 5.5 us: a launch, the two dependent reads (lengths, then table or
+// Measured on GB300: one request with one token 2.4 us, 512 requests with 52K
+// new tokens 5.3 us: a launch, the two dependent reads (lengths, then table or
 // free list) and the scans between them; memory would need 0.2 us.
 #include <climits>
 

@@ -321,7 +321,9 @@ def pa_q4_decode(plan, q, cache, block_tables, context_lens, scale, window, out,
 class PreparedQ4Decode:
     """pa_q4_decode with its arguments checked and converted once, for a loop that
     calls it with the same buffers every step (as PreparedDecode for pa_decode).
-    The tensors must stay alive and in place while it is used."""
+    The tensors must stay alive and in place while it is used.  Every call goes to
+    the stream of the preparation: `stream`, or without one the stream that was
+    current then (prepare inside torch.cuda.graph what a graph is to capture)."""
 
     def __init__(self, plan, q, cache, block_tables, context_lens, scale, window, out, lse,
                  workspace, stream=None):
