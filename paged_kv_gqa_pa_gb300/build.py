@@ -12,6 +12,7 @@ another torch or another interpreter is never loaded.  Usage:
 from __future__ import annotations
 
 import argparse
+import contextlib
 import glob
 import hashlib
 import importlib.util
@@ -82,7 +83,8 @@ def _start_pyfast(force: bool, verbose: bool):
     path = pyfast_path()
     for old in glob.glob(os.path.join(BUILD, "_pa_fast*.so")):
         if old != path:
-            os.remove(old)
+            with contextlib.suppress(FileNotFoundError):  # (another build was first)
+                os.remove(old)
     inc, torch_dir = sysconfig.get_paths()["include"], _torch_dir()
     cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
     if path is None or cxx is None or not os.path.exists(os.path.join(inc, "Python.h")):

@@ -538,3 +538,11 @@ def test_decode_refuses_words_that_are_not_aligned(lib):
             a = [ctypes.byref(plan), FAKE, FAKE, FAKE, FAKE, 1.0, 0, FAKE, FAKE, FAKE, None]
             a[i] += off
             assert lib.pa_q4_decode(*a) == binding.PA_ERR_INVALID_ARG, i
+
+
+def test_a_stale_extension_that_another_build_has_removed(build_tree, monkeypatch):
+    gone = str(build_tree / "_build" / "_pa_fast-0123456789abcdef.so")
+    monkeypatch.setattr(pa_build.glob, "glob", lambda pattern: [gone])
+    monkeypatch.delenv("CXX", raising=False)
+    monkeypatch.setattr(pa_build.shutil, "which", lambda name: None)
+    assert pa_build._start_pyfast(False, False) is None
