@@ -157,10 +157,10 @@ int pa_q4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
  * of normal values measured 2.4e-4 to 2.9e-4 of their norm off, of which 2e-4
  * are their own rounding.)
  * The work of the whole batch is shared out over the CTAs on the device, from
- * the actual lengths (see ctas_per_group and cluster).  workspace: plan->workspace_bytes, 16-byte
- * aligned, the first plan->ctrl_bytes zero before the first call; concurrent
- * calls must not share one, and one that served another plan must have its
- * ctrl_bytes zeroed first.
+ * the actual lengths (see ctas_per_group and cluster).
+ * workspace: plan->workspace_bytes, 16-byte aligned, the first plan->ctrl_bytes
+ * zero before the first call; concurrent calls must not share one, and one that
+ * served another plan must have its ctrl_bytes zeroed first.
  */
 int pa_q4_decode(const pa_q4_plan_t* plan, const void* q, const void* cache,
                  const int32_t* block_tables, const int32_t* context_lens, float scale,

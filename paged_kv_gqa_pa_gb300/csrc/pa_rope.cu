@@ -211,7 +211,8 @@ static unsigned long long turn64(double x, double* rest) {
 
 // round(2^64 theta^(-2 i / R) / (2 pi)) modulo 2^64, i < R / 2: all 64 bits for bases
 // from 1e-3 on (below, a position is so many turns that fewer are left behind the
-// point).  2 us for 128 frequencies; with a pow for each it was 4.
+// point).  On the Grace host 1.0 us for 128 frequencies; with a pow for each it
+// was 1.8.
 static void rope_frequencies(float theta, int R, unsigned long long* freq) {
     const int half = R / 2;
     // r = theta^(-1 / half): the double r0 and one step of Newton's method,
@@ -300,7 +301,7 @@ extern "C" int pa_rope_axes(int num_tokens, int num_q_heads, int num_kv_heads, i
     if ((bits & 15u) || ((uintptr_t)positions & 3u)) return PA_ERR_INVALID_ARG;
     // Frequencies as 64-bit fractions of a turn; the table of the last (base,
     // rotary dim) this thread used is kept.  (A model whose layers alternate
-    // between two bases pays the table, 2 us of host time, in every call.)
+    // between two bases pays the table, up to 1 us of host time, in every call.)
     thread_local float t_theta = 0.f;
     thread_local int t_R = 0;
     thread_local unsigned long long t_freq[kMaxRopePairs];
