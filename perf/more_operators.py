@@ -237,7 +237,7 @@ def _prepare_rows(case, seed, dev, gen):
         had = torch.zeros(pages * PAGE, dtype=torch.bool, device=dev)
         had[old] = True
         codes = torch.where(had.view(pages, 1, PAGE, 1), c, codes)
-        s[name + "_cache"], s[name + "_scales"] = codes.view(_F8), scale
+        s[name + "_cache"], s[name + "_scales"] = codes.contiguous().view(_F8), scale
     rows = np.sort(np.concatenate([first, slots]))
     s["read"] = torch.from_numpy(rows).to(dev)
     s["k_out"] = torch.empty(rows.size, hkv, D, dtype=dt, device=dev)
