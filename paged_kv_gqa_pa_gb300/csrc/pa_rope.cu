@@ -21,14 +21,13 @@
 // fraction, go to fp32 (half a step: 2^-26 of a turn next to half a turn, less
 // nearer to 0) and sincospif.  f has to be good to 64 bits, more than a double
 // holds: the host works it out in pairs of doubles.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
 
 #include <algorithm>
 
 #include "pa_q4.cuh"
+#include "pa_rope.cuh"
 
 namespace pa {
 
@@ -46,64 +45,6 @@ struct RopeAxesParams {
     int inverse;
     unsigned long long freq[kMaxRopePairs];
     unsigned char axis[kMaxRopePairs];
-};
-
-template <typename T>
-struct RopeElem;
-template <>
-struct RopeElem<__half> {
-    static constexpr int kN = 8;  // elements of 16 bytes
-    __device__ static __forceinline__ void load(const uint4& u, float (&f)[8]) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            f[2 * i] = v.x;
-            f[2 * i + 1] = v.y;
-        }
-    }
-    __device__ static __forceinline__ uint4 store(const float (&f)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-template <>
-struct RopeElem<__nv_bfloat16> {
-    static constexpr int kN = 8;
-    __device__ static __forceinline__ void load(const uint4& u, float (&f)[8]) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-    __device__ static __forceinline__ uint4 store(const float (&f)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-template <>
-struct RopeElem<float> {
-    static constexpr int kN = 4;
-    __device__ static __forceinline__ void load(const uint4& u, float (&f)[4]) {
-        f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y);
-        f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
-    }
-    __device__ static __forceinline__ uint4 store(const float (&f)[4]) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                          __float_as_uint(f[3]));
-    }
 };
 
 template <typename T>
@@ -165,10 +106,8 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_axes_kernel(const RopeAx
     }
     for (int i = tid; i < half; i += nt) {
         const int pos = p.positions[(size_t)p.axis[i] * p.n + t];
-        const unsigned long long turns = (unsigned long long)(long long)pos * p.freq[i];
-        const float fr = (float)(int)(turns >> 32) * 4.656612873077393e-10f;  // 2^-31: half turns
-        float sn, cs;
-        sincospif(fr, &sn, &cs);
+        float cs, sn;
+        rope_angle(pos, p.freq[i], cs, sn);
         s_cos[i] = cs;
         s_sin[i] = p.inverse ? -sn : sn;
     }
@@ -237,6 +176,18 @@ static void rope_frequencies(float theta, int R, unsigned long long* freq) {
     }
 }
 
+const unsigned long long* rope_frequency_table(float theta, int R) {
+    thread_local float t_theta = 0.f;
+    thread_local int t_R = 0;
+    thread_local unsigned long long t_freq[kMaxRopePairs];
+    if (t_theta != theta || t_R != R) {
+        rope_frequencies(theta, R, t_freq);
+        t_theta = theta;
+        t_R = R;
+    }
+    return t_freq;
+}
+
 }  // namespace pa
 
 using namespace pa;
@@ -299,18 +250,7 @@ extern "C" int pa_rope_axes(int num_tokens, int num_q_heads, int num_kv_heads, i
     if (has_q) bits |= (uintptr_t)q | (uintptr_t)q_out;
     if (has_k) bits |= (uintptr_t)k | (uintptr_t)k_out;
     if ((bits & 15u) || ((uintptr_t)positions & 3u)) return PA_ERR_INVALID_ARG;
-    // Frequencies as 64-bit fractions of a turn; the table of the last (base,
-    // rotary dim) this thread used is kept.  (A model whose layers alternate
-    // between two bases pays the table, up to 1 us of host time, in every call.)
-    thread_local float t_theta = 0.f;
-    thread_local int t_R = 0;
-    thread_local unsigned long long t_freq[kMaxRopePairs];
-    if (t_theta != theta || t_R != rotary_dim) {
-        rope_frequencies(theta, rotary_dim, t_freq);
-        t_theta = theta;
-        t_R = rotary_dim;
-    }
-    memcpy(p.freq, t_freq, sizeof(unsigned long long) * half);
+    memcpy(p.freq, rope_frequency_table(theta, rotary_dim), sizeof(unsigned long long) * half);
     p.q = static_cast<const unsigned char*>(q);
     p.k = static_cast<const unsigned char*>(k);
     p.q_out = static_cast<unsigned char*>(q_out);
