@@ -57,28 +57,33 @@ struct RowLanes {
         const int turn = R / (2 * N);
         return c < turn ? c * N + R / 2 : R + (c - turn) * 2 * N + N;
     }
-    // x, y times w / sqrt(mean square + eps); every lane of the warp takes part.
-    __device__ static __forceinline__ void normalise(float (&x)[N], float (&y)[N],
-                                                     const unsigned char* w, int d0, int d1,
-                                                     bool has, float eps) {
-        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-        if (has) {
-            w0 = __ldg(reinterpret_cast<const uint4*>(w + d0 * ES));
-            w1 = __ldg(reinterpret_cast<const uint4*>(w + d1 * ES));
-        }
+    // x, y times w / sqrt(mean square + eps), w the weights as fp32 in shared memory; every
+    // lane of the warp takes part.
+    __device__ static __forceinline__ void normalise(float (&x)[N], float (&y)[N], const float* w,
+                                                     int d0, int d1, bool has, float eps) {
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < N; ++j) sum = fmaf(x[j], x[j], fmaf(y[j], y[j], sum));
 #pragma unroll
         for (int m = 1; m < kLanes; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
         const float f = rsqrtf(sum * (1.f / D) + eps);
-        float wx[N], wy[N];
-        E::load(w0, wx);
-        E::load(w1, wy);
+        if (!has) return;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            x[j] = x[j] * f * wx[j];
-            y[j] = y[j] * f * wy[j];
+        for (int j = 0; j < N; j += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(w + d0 + j);
+            const float4 b = *reinterpret_cast<const float4*>(w + d1 + j);
+            x[j] *= f * a.x, x[j + 1] *= f * a.y, x[j + 2] *= f * a.z, x[j + 3] *= f * a.w;
+            y[j] *= f * b.x, y[j + 1] *= f * b.y, y[j + 2] *= f * b.z, y[j + 3] *= f * b.w;
+        }
+    }
+    // Norm weights into shared memory (the caller's barrier follows).
+    __device__ static __forceinline__ void stage(const unsigned char* w, float* to) {
+        if (!w) return;
+        for (int i = threadIdx.x; i < D / N; i += blockDim.x) {
+            float f[N];
+            E::load(__ldg(reinterpret_cast<const uint4*>(w) + i), f);
+#pragma unroll
+            for (int j = 0; j < N; ++j) to[i * N + j] = f[j];
         }
     }
 };
@@ -91,28 +96,36 @@ __device__ __forceinline__ long long append_slot(const AppendParams& p, long lon
     return bad ? -1 : s;
 }
 
-// Rows h0 .. h1 - 1 of token t, rows being its q heads, its K heads, its V heads.
-template <int D, typename T>
-__device__ __forceinline__ void append_token(const AppendParams& p, long long t, int n_rows,
-                                             long long slot, float* s_cos, float* s_sin) {
+// What a CTA of a token has in shared memory.
+template <int D>
+struct AppendShared {
+    alignas(16) float cos[kMaxRopePairs];
+    alignas(16) float sin[kMaxRopePairs];
+    alignas(16) float w[2][D];  // norm weights of q and k
+};
+
+// The q heads of token t, or all its heads (ALL: q's, K's, then V's, into the cache too).
+template <int D, typename T, bool ALL>
+__device__ __forceinline__ void append_token(const AppendParams& p, long long t,
+                                             AppendShared<D>& sh) {
     using Rw = RowLanes<D, T>;
     using E = RopeElem<T>;
     constexpr int N = Rw::N, ES = Rw::ES, L = Rw::kLanes;
     const int tid = threadIdx.x, nt = blockDim.x;
+    const int n_rows = p.Hq + (ALL ? 2 * p.Hkv : 0);
     const int items = n_rows * L;
     const int c = tid % L;  // (blockDim is a multiple of 32)
     const bool has_lane = c < Rw::kHave;
     const int d0 = Rw::first(c, p.R), d1 = Rw::second(c, p.R);
     const bool turn = c < p.R / (2 * N);
+    const long long slot = ALL ? append_slot(p, t, tid == 0) : -1;
     for (int i0 = 0; i0 < items; i0 += kAppendItems * nt) {
         uint4 a[kAppendItems], b[kAppendItems];
-        bool has[kAppendItems];
 #pragma unroll
         for (int u = 0; u < kAppendItems; ++u) {
             const int h = (i0 + u * nt + tid) / L;
-            has[u] = has_lane && h < n_rows && (h < p.Hq || slot >= 0);
             a[u] = b[u] = make_uint4(0, 0, 0, 0);
-            if (has[u]) {
+            if (has_lane && h < n_rows) {  // (rows that are left out too: nobody waits for the slot)
                 const unsigned char* src =
                     h < p.Hq ? p.q + t * p.q_stride + (size_t)h * D * ES
                     : h < p.Hq + p.Hkv
@@ -122,36 +135,33 @@ __device__ __forceinline__ void append_token(const AppendParams& p, long long t,
                 b[u] = *reinterpret_cast<const uint4*>(src + d1 * ES);
             }
         }
-        if (i0 == 0 && p.R > 0) {  // (while the rows are on their way)
-            const int pos = p.positions[t];
-            for (int i = tid; i < p.R / 2; i += nt) rope_angle(pos, p.freq[i], s_cos[i], s_sin[i]);
+        if (i0 == 0) {  // (while the rows are on their way)
+            Rw::stage(p.q_norm, sh.w[0]);
+            if (ALL) Rw::stage(p.k_norm, sh.w[1]);
+            if (p.R > 0) {
+                const int pos = p.positions[t];
+                for (int i = tid; i < p.R / 2; i += nt)
+                    rope_angle(pos, p.freq[i], sh.cos[i], sh.sin[i]);
+            }
             __syncthreads();
         }
 #pragma unroll
         for (int u = 0; u < kAppendItems; ++u) {
             const int h = (i0 + u * nt + tid) / L;
-            const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-            const unsigned char* w = is_q ? p.q_norm : p.k_norm;
+            const bool is_q = !ALL || h < p.Hq, is_v = ALL && h >= p.Hq + p.Hkv;
+            const bool has = has_lane && h < n_rows && (is_q || slot >= 0);
             float x[N], y[N];
             E::load(a[u], x);
             E::load(b[u], y);
             // (rows of one warp may be q's and k's: the shuffles are for all of them)
-            if (p.q_norm || p.k_norm) {
-                float nx[N], ny[N];
-#pragma unroll
-                for (int j = 0; j < N; ++j) nx[j] = x[j], ny[j] = y[j];
-                const bool norm = w && !is_v;
-                Rw::normalise(nx, ny, w, d0, d1, norm && has[u], p.eps);
-                if (norm) {
-#pragma unroll
-                    for (int j = 0; j < N; ++j) x[j] = nx[j], y[j] = ny[j];
-                }
-            }
-            if (!has[u]) continue;
+            if (p.q_norm || (ALL && p.k_norm))
+                Rw::normalise(x, y, sh.w[is_q ? 0 : 1], d0, d1,
+                              has && !is_v && (is_q ? p.q_norm : p.k_norm), p.eps);
+            if (!has) continue;
             if (turn && !is_v) {
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const float cs = s_cos[c * N + j], sn = s_sin[c * N + j];
+                    const float cs = sh.cos[c * N + j], sn = sh.sin[c * N + j];
                     const float xr = fmaf(x[j], cs, -(y[j] * sn));
                     y[j] = fmaf(y[j], cs, x[j] * sn);
                     x[j] = xr;
@@ -174,14 +184,11 @@ __device__ __forceinline__ void append_token(const AppendParams& p, long long t,
 
 // A CTA for each token.
 template <int D, typename T>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
-    __shared__ float s_cos[kMaxRopePairs];
-    __shared__ float s_sin[kMaxRopePairs];
+__global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const AppendParams p) {
+    __shared__ AppendShared<D> sh;
     allow_dependent_launch();
     wait_for_prerequisite_grid();
-    const long long t = blockIdx.x;
-    const long long slot = append_slot(p, t, threadIdx.x == 0);
-    append_token<D, T>(p, t, p.Hq + (slot >= 0 ? 2 * p.Hkv : 0), slot, s_cos, s_sin);
+    append_token<D, T, true>(p, blockIdx.x, sh);
 }
 
 // ---- The 8-bit cache.
@@ -244,20 +251,20 @@ __device__ __forceinline__ void q8_store_codes(unsigned char* p, const uint32_t 
 // new one, one that was there, or none.  The largest magnitude goes through the CTA,
 // the scale follows, codes are stored.  The other CTAs serve a token's q each.
 template <int D, typename T>
-__global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes)) q8_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes), 64 / RowLanes<D, T>::kLanes)
+    q8_append_kernel(const AppendParams p) {
     using Rw = RowLanes<D, T>;
     using E = RopeElem<T>;
     constexpr int N = Rw::N, ES = Rw::ES, L = Rw::kLanes, W = N / 4;
     constexpr int kWarpsHere = 16 * L / 32;
-    __shared__ float s_cos[kMaxRopePairs];
-    __shared__ float s_sin[kMaxRopePairs];
+    __shared__ AppendShared<D> sh;
     __shared__ uint32_t s_max[2][kWarpsHere];
     __shared__ unsigned long long s_freq[kMaxRopePairs];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     allow_dependent_launch();
     wait_for_prerequisite_grid();
     if ((int)blockIdx.x >= p.kv_ctas) {
-        append_token<D, T>(p, blockIdx.x - p.kv_ctas, p.Hq, -1, s_cos, s_sin);
+        append_token<D, T, false>(p, blockIdx.x - p.kv_ctas, sh);
         return;
     }
     const int is_v = blockIdx.x & 1, group = (blockIdx.x >> 1) % p.groups;
@@ -275,16 +282,15 @@ __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes)) q8_append_kerne
     const uint32_t on = __ballot_sync(0xffffffffu, goes_on);
     uint32_t leads = __ballot_sync(0xffffffffu, slot >= 0 && !goes_on && lane >= 1 && lane <= p.tile);
     if (!leads) return;
-    const bool rotate = !is_v && p.R > 0;
-    if (rotate) {
+    const bool rotate = !is_v && p.R > 0, norm = !is_v && p.k_norm;
+    if (norm) Rw::stage(p.k_norm, sh.w[1]);
+    if (rotate)
         for (int i = tid; i < p.R / 2; i += blockDim.x) s_freq[i] = p.freq[i];
-        __syncthreads();
-    }
+    if (norm || rotate) __syncthreads();
     const unsigned char* src0 = is_v ? p.v : p.k;
     const long long stride = is_v ? p.v_stride : p.k_stride;
     unsigned char* cache = is_v ? p.v_cache : p.k_cache;
     float* scales = is_v ? p.v_scales : p.k_scales;
-    const unsigned char* w = is_v ? nullptr : p.k_norm;
     const int r = tid / L, c = tid % L;
     const int d0 = Rw::first(c, p.R), d1 = Rw::second(c, p.R);
     const bool turn = rotate && c < p.R / (2 * N);
@@ -333,7 +339,7 @@ __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes)) q8_append_kerne
             float x[N], y[N];
             E::load(a, x);
             E::load(b, y);
-            if (w) Rw::normalise(x, y, w, d0, d1, fresh, p.eps);
+            if (norm) Rw::normalise(x, y, sh.w[1], d0, d1, fresh, p.eps);
             if (turn && fresh) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {

@@ -20,7 +20,7 @@
 
 namespace pa {
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyCluster = 8;    // CTAs of a sequence, at most
 constexpr int kVerifyMaxVocab = 1 << 19;  // (sums of 2^19 weights of 1 fit 64 bits)
@@ -56,22 +56,27 @@ __device__ __forceinline__ float verify_float(__nv_bfloat16 x) {
     return __bfloat162float(x);
 }
 
-// A probability limited to [0, 1], NaN as 0.
-__device__ __forceinline__ float verify_limit(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
-
-// w in units of 2^-44, to nearest: the multiple of 2^-21 next to it and what that
-// leaves, each made an integer by adding 1.5 times the power of two whose unit in the
-// last place it counts in.
-__device__ __forceinline__ unsigned long long verify_units(float w) {
-    constexpr float kHigh = 6.f;        // 1.5 * 2^2: unit 2^-21
-    constexpr float kLow = 12582912.f;  // 1.5 * 2^23: unit 1
-    const float a = w + kHigh;
-    const int hi = __float_as_int(a) - __float_as_int(kHigh);
-    const float rest = w - (a - kHigh);  // exact, at most 2^-22
-    const float b = fmaf(rest, 17592186044416.f, kLow);
-    const int lo = __float_as_int(b) - __float_as_int(kLow);
-    return (unsigned long long)((long long)hi * (1ll << 23) + lo);
-}
+// A weight in units of 2^-44, to nearest, as two numbers: the multiple of 2^-21 next to
+// it and what that leaves, each made an integer by adding 1.5 times the power of two
+// whose unit in the last place it counts in.  Sums of the floats' bits, modulo 2^32, are
+// sums of those integers and of the constants' bits.
+struct VerifySum {
+    static constexpr float kHigh = 6.f;        // 1.5 * 2^2: unit 2^-21
+    static constexpr float kLow = 12582912.f;  // 1.5 * 2^23: unit 1
+    uint32_t hi = 0, lo = 0;
+    __device__ __forceinline__ void add(float w) {
+        const float a = w + kHigh;
+        const float rest = w - (a - kHigh);  // exact, at most 2^-22
+        hi += __float_as_uint(a);
+        lo += __float_as_uint(fmaf(rest, 17592186044416.f, kLow));
+    }
+    // Of n weights, at most 256 (so that the sums of 2^21 and 2^22 at most fit 32 bits).
+    __device__ __forceinline__ unsigned long long units(int n) const {
+        const int h = (int)(hi - (uint32_t)n * __float_as_uint(kHigh));
+        const int l = (int)(lo - (uint32_t)n * __float_as_uint(kLow));
+        return (unsigned long long)((long long)h * (1ll << 23) + l);
+    }
+};
 
 __device__ __forceinline__ unsigned long long verify_warp_sum(unsigned long long x) {
 #pragma unroll
@@ -79,21 +84,26 @@ __device__ __forceinline__ unsigned long long verify_warp_sum(unsigned long long
     return x;
 }
 
-// Rows of weights: p, less q where there is one, and none at `hole`.
+// Rows of weights: p, less q where there is one, and none at `hole`.  (Saturating
+// limits a number to [0, 1], NaN to 0.)
 template <typename T>
 struct VerifyRow {
     const T* p;
     const T* q;  // null: p itself
     int hole;    // -1: none
     __device__ __forceinline__ unsigned long long at(int i) const {
-        float w = verify_limit(verify_float(p[i]));
-        if (q) w = fmaxf(w - verify_limit(verify_float(q[i])), 0.f);
-        return i == hole ? 0ull : verify_units(w);
+        float w = __saturatef(verify_float(p[i]));
+        if (q) w = __saturatef(w - __saturatef(verify_float(q[i])));
+        VerifySum s;
+        s.add(i == hole ? 0.f : w);
+        return s.units(1);
     }
-    // This lane's share of elements lo .. hi - 1.
+    // This lane's share of elements lo .. hi - 1 (a hole counted like the others).
+    template <bool Q>
     __device__ __forceinline__ unsigned long long sum(int lo, int hi, int lane, bool vec) const {
-        unsigned long long s = 0;
-        constexpr int N = 16 / sizeof(T), U = 4;
+        VerifySum s;
+        int n = 0;
+        constexpr int N = 16 / sizeof(T), U = sizeof(T) == 4 ? 4 : 2;
         int i = lo;
         if (vec) {  // (lo is a multiple of 8)
             for (; i + 32 * N * U <= hi; i += 32 * N * U) {
@@ -101,7 +111,7 @@ struct VerifyRow {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     a[u] = __ldcs(reinterpret_cast<const uint4*>(p + i + (u * 32 + lane) * N));
-                    if (q) b[u] = __ldcs(reinterpret_cast<const uint4*>(q + i + (u * 32 + lane) * N));
+                    if (Q) b[u] = __ldcs(reinterpret_cast<const uint4*>(q + i + (u * 32 + lane) * N));
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -109,36 +119,52 @@ struct VerifyRow {
                     const T* y = reinterpret_cast<const T*>(&b[u]);
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
-                        float w = verify_limit(verify_float(x[k]));
-                        if (q) w = fmaxf(w - verify_limit(verify_float(y[k])), 0.f);
-                        if (i + (u * 32 + lane) * N + k != hole) s += verify_units(w);
+                        float w = __saturatef(verify_float(x[k]));
+                        if (Q) w = __saturatef(w - __saturatef(verify_float(y[k])));
+                        s.add(w);
                     }
                 }
-            }
-        } else {
-            constexpr int M = 8;
-            for (; i + 32 * M <= hi; i += 32 * M) {
-                T a[M], b[M];
-#pragma unroll
-                for (int u = 0; u < M; ++u) {
-                    a[u] = p[i + u * 32 + lane];
-                    if (q) b[u] = q[i + u * 32 + lane];
-                }
-#pragma unroll
-                for (int u = 0; u < M; ++u) {
-                    float w = verify_limit(verify_float(a[u]));
-                    if (q) w = fmaxf(w - verify_limit(verify_float(b[u])), 0.f);
-                    if (i + u * 32 + lane != hole) s += verify_units(w);
-                }
+                n += N * U;
             }
         }
-        for (i += lane; i < hi; i += 32) s += at(i);
-        return s;
+        constexpr int M = 8;
+        for (; i + 32 * M <= hi; i += 32 * M) {
+            T a[M], b[M];
+#pragma unroll
+            for (int u = 0; u < M; ++u) {
+                a[u] = p[i + u * 32 + lane];
+                if (Q) b[u] = q[i + u * 32 + lane];
+            }
+#pragma unroll
+            for (int u = 0; u < M; ++u) {
+                float w = __saturatef(verify_float(a[u]));
+                if (Q) w = __saturatef(w - __saturatef(verify_float(b[u])));
+                s.add(w);
+            }
+            n += M;
+        }
+        for (i += lane; i < hi; i += 32) {
+            float w = __saturatef(verify_float(p[i]));
+            if (Q) w = __saturatef(w - __saturatef(verify_float(q[i])));
+            s.add(w);
+            ++n;
+        }
+        return s.units(n);
+    }
+    // Of a warp's elements lo .. hi - 1.
+    __device__ __forceinline__ unsigned long long warp_sum(int lo, int hi, int lane, bool vec) const {
+        unsigned long long x = q ? sum<true>(lo, hi, lane, vec) : sum<false>(lo, hi, lane, vec);
+        if (lane == 0 && hole >= lo && hole < hi) {
+            VerifyRow all = *this;
+            all.hole = -1;
+            x -= all.at(hole);
+        }
+        return verify_warp_sum(x);
     }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const VerifyParams p) {
     __shared__ int s_stop[2];                                // j, and the draft there
     __shared__ unsigned long long s_warp[kVerifyWarps];      // sums of the warps' stretches
     __shared__ unsigned long long s_cta[2][kVerifyCluster];  // of the cluster's CTAs (by pass)
@@ -154,23 +180,22 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     const T* target = static_cast<const T*>(p.target) + (size_t)b * (p.T + 1) * p.V;
     const T* draft = static_cast<const T*>(p.draft);
     if (draft) draft += (size_t)b * p.T * p.V;
-    unsigned bad = 0;
+    const float u = p.sample_u[b];
     const int asked = p.num_drafts ? p.num_drafts[b] : p.T;
     const int n = min(max(asked, 0), p.T);
-    if (n != asked) bad = PA_DEVERR_BAD_TOKEN;
     if (warp == 0) {  // (at most 32 drafts)
         int x = -1;
-        bool ok = false;
-        if (lane < n) {
+        float ua = 0.f, px = 0.f, qx = 1.f;
+        if (lane < p.T) {  // (before the number of drafts is there)
             x = p.draft_tokens[(size_t)b * p.T + lane];
-            if (x >= 0 && x < p.V) {
-                const float px = verify_limit(verify_float(target[(size_t)lane * p.V + x]));
-                const float qx = draft ? verify_limit(verify_float(draft[(size_t)lane * p.V + x])) : 1.f;
-                ok = (double)p.accept_u[(size_t)b * p.T + lane] * (double)qx < (double)px;
-            } else {
-                bad = PA_DEVERR_BAD_TOKEN;
-            }
+            ua = p.accept_u[(size_t)b * p.T + lane];
         }
+        const bool known = x >= 0 && x < p.V;
+        if (lane < p.T && known) {
+            px = __saturatef(verify_float(target[(size_t)lane * p.V + x]));
+            if (draft) qx = __saturatef(verify_float(draft[(size_t)lane * p.V + x]));
+        }
+        const bool ok = lane < n && known && (double)ua * (double)qx < (double)px;
         const unsigned no = __ballot_sync(0xffffffffu, !ok);
         const int j = no ? min(n, __ffs(no) - 1) : n;
         const int xj = __shfl_sync(0xffffffffu, x, j & 31);
@@ -178,9 +203,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             s_stop[0] = j;
             s_stop[1] = j < n ? xj : -1;
         }
-        // (a draft behind the first that is not accepted is not looked at)
         if (rank == 0) {
-            if (bad && p.err && (lane <= j || n != asked)) atomicOr(p.err, bad);
+            // (a draft behind the first that is not accepted is not looked at)
+            if (p.err && (n != asked || (lane == j && lane < n && !known)))
+                atomicOr(p.err, PA_DEVERR_BAD_TOKEN);
             for (int i = lane; i <= p.T; i += 32)
                 if (i != j) p.tokens[(size_t)b * (p.T + 1) + i] = i < j ? x : -1;  // (i < j: lane i)
             if (lane == 0) p.accepted[b] = j;
@@ -202,7 +228,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             row.q = nullptr;
             row.hole = -1;
         }
-        const unsigned long long sum = verify_warp_sum(row.sum(lo, hi, lane, p.vec != 0));
+        const unsigned long long sum = row.warp_sum(lo, hi, lane, p.vec != 0);
         if (lane == 0) s_warp[warp] = sum;
         __syncthreads();
         mine = 0;
@@ -238,7 +264,6 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         }
         return;
     }
-    const float u = p.sample_u[b];
     unsigned long long at = 0;
     if (u > 0.f) {
         const double x = floor((double)u * (double)total);
