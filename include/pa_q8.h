@@ -12,8 +12,8 @@
  *   k_scales  fp32 [num_pages, Hkv]                (v_scales the same)
  * A code c of KV head h in page p stands for k_scales[p][h] * c.  e4m3 is the
  * 8-bit float with 4 exponent and 3 mantissa bits, largest value 448, NaN 0x7F and
- * 0xFF, no infinities (torch.float8_e4m3fn).  pa_q8_decode takes any finite
- * positive scales; those that pa_q8_append makes are powers of two, so that a
+ * 0xFF, no infinities (torch.float8_e4m3fn).  pa_q8_decode takes any
+ * positive scales up to 2^126; those that pa_q8_append makes are powers of two, so that a
  * scale costs no precision and raising it later is a shift of the exponent.
  */
 #ifndef PA_GB300_Q8_H
@@ -157,10 +157,10 @@ int pa_q8_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
  * the workspace's error word, as in pa_decode (PA_DEVERR_BAD_LENGTH for starts more
  * than max_query_len apart too, and for starts that do not ascend or lie outside
  * [0, num_rows], where it is not known which rows the sequence has: none is written).
- * Precision: K's and V's codes and q are exact in the products (fp16; bf16 rows of
- * q are scaled by a power of two), scores, maxima and sums fp32; the weights are
- * rounded to fp16's 11 bits for the product with V and normalised by the sum of
- * the rounded weights.
+ * Precision: the codes of K and V and q are exact in the products (bf16 rows of q are
+ * scaled by a power of two), scores, maxima and sums fp32; the weights are rounded to
+ * fp16's 11 bits for the product with V and normalised by the sum of the rounded
+ * weights.
  * workspace as for pa_q4_decode.
  */
 int pa_q8_decode(const pa_q8_plan_t* plan, int num_rows, const void* q, const int32_t* starts,

@@ -56,7 +56,7 @@ static Q8WsLayout q8_ws_layout(int B, int D, int tiles, long long groups, int X)
 static int q8_ctas_per_sm(int D, int tiles, int B) {
     int smem = 0, most = 0;  // shared memory of a CTA, CTAs that the registers allow
     q8_pick(D, tiles).size(B, &smem, &most);
-    return std::max(1, std::min(most, 228 * 1024 / (smem + 1024 + 512)));
+    return std::max(1, std::min(most, 228 * 1024 / (smem + 1024 + 384)));
 }
 
 // Clusters of c CTAs held at once: the current device's answer (asked for once
@@ -335,6 +335,7 @@ int pa_q8_decode(const pa_q8_plan_t* plan, int num_rows, const void* q, const in
     p.rows = num_rows;
     p.nchunk = g / G;
     p.G = G;
+    p.ginv = 65536 / G + 1;
     p.X = X;
     p.stall_tx = plan->test_stall_bytes;
     p.bf16 = plan->dtype == PA_DTYPE_BF16;

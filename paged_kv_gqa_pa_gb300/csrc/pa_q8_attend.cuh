@@ -30,7 +30,6 @@ constexpr int q8_short(int D) { return D == 256 ? 16 : 24; }
 // What a sequence's start and end cost a CTA, in pages: equal ranges are equal
 // in this cost, not in pages.
 constexpr int kQ8Start = 12;
-constexpr int kQ8StagedPages = 512;  // page ids and scales a CTA stages at a time
 // The running maximum (log2 domain) before any score: below every score that
 // counts, and finite, so that a score of -inf is further below it.
 constexpr float kQ8NoMax = -3e38f;
@@ -67,6 +66,7 @@ struct Q8AttendParams {
     unsigned* err;
     int B, Hq, Hkv, g, num_pages, maxp, max_ctx, window, max_t, rows;
     int nchunk, G, X;
+    int ginv;          // 65536 / G + 1: r / G = r ginv >> 16 for rows r below kQ8MaxRows
     int merge_kernel;  // 1: q8_merge_kernel merges, 0: the last to leave a partial
     int cluster;       // > 0: CTAs of a sequence's cluster (X = B clusters of them)
     int stall_tx;      // test hook
@@ -77,8 +77,7 @@ struct Q8AttendParams {
 template <int D, int NT>
 struct Q8Cfg {
     static constexpr int kPage = 16 * D;           // bytes of a page of K, or of V
-    static constexpr int kPair = 1;                // pages of a ring slot
-    static constexpr int kSlotBytes = kPair * 2 * kPage;
+    static constexpr int kSlotBytes = 2 * kPage;   // a ring slot: a page's K and V
     static constexpr int kStages = D == 256 ? 2 : (D == 64 ? 4 : 3);
     static constexpr int kRingBytes = kWarps * kStages * kSlotBytes;
     // q's fragments: in registers, or in shared memory where the accumulators
@@ -90,13 +89,15 @@ struct Q8Cfg {
     static constexpr int kUnits = NT * kTileUnits;
     static constexpr int kRows = 8 * NT;
     static_assert(kUnits * 512 <= kRingBytes, "a cluster's CTA leaves its state in the ring");
-    static constexpr int kXBytes = kTileUnits * (kWarps - 1) * 512;
-    static constexpr int kSmemBytes = 1024 + kRingBytes + kQBytes + kXBytes +
-                                      kQ8StagedPages * 12 + kWarps * kRows * 2 * 4 +
-                                      kWarps * kRows * 4 + kWarps * kStages * 8;
+    static constexpr int kXBytes = kTileUnits * kWarps * 512;
+    // Page ids and scales that a CTA stages at a time.
+    static constexpr int kStaged = NT == 2 && D >= 128 ? 256 : 512;
+    static constexpr int kSmemBytes = 1024 + kRingBytes + kXBytes + kQBytes + kStaged * 12 +
+                                      kWarps * kRows * 8 + kWarps * kStages * 8;
     // CTAs per SM by registers.
     static constexpr int kMinBlocks = D == 256 || NT > 2 ? 2 : 3;
-    static_assert(kMinBlocks * (kSmemBytes + 1024 + 512) <= 228 * 1024, "CTAs per SM");
+    static constexpr int kStaticBytes = kRows * 8 + 128;  // (beside the dynamic ones)
+    static_assert(kMinBlocks * (kSmemBytes + kStaticBytes + 1024) <= 228 * 1024, "CTAs per SM");
     // (five words per sequence follow: s_base, s_rank, s_row, s_page0, s_len)
     static int smem(int B) { return kSmemBytes + (5 * B + 3) * 4; }
 };
@@ -202,6 +203,14 @@ __device__ __forceinline__ void q8_tma(uint32_t dst, const CUtensorMap* map, int
         : "memory");
 }
 
+__device__ __forceinline__ void q8_prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2_line(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
 template <int D>
 __device__ __forceinline__ void q8_load_page(uint32_t dst, const CUtensorMap* map, int row,
                                              uint32_t bar) {
@@ -247,24 +256,30 @@ __device__ __forceinline__ uint32_t q8_out2(int bf16, float x, float y) {
     return q8_pack(x, y);
 }
 
+// Row r of those that begin at row0, head h0: its place among out's and lse's rows.
+__device__ __forceinline__ size_t q8_out_row(const Q8AttendParams& p, int row0, int h0, int r) {
+    const int t = (r * p.ginv) >> 16;
+    return (size_t)(row0 + t) * p.Hq + h0 + (r - t * p.G);
+}
+
 // Unit u of the rows that begin at row0, head h0.
 template <int D, int NT>
 __device__ __forceinline__ void q8_store_unit(const Q8AttendParams& p, int row0, int h0, int u,
                                               int lane, float4 o, float inv) {
-    const int r = q8_unit_row<D, NT>(u, lane);
-    const int t = r / p.G, h = r - t * p.G;
     uint32_t* at = reinterpret_cast<uint32_t*>(
-        reinterpret_cast<__half*>(p.out) + ((size_t)(row0 + t) * p.Hq + h0 + h) * D +
-        q8_unit_dim<D, NT>(u, lane));
+        reinterpret_cast<__half*>(p.out) +
+        q8_out_row(p, row0, h0, q8_unit_row<D, NT>(u, lane)) * D + q8_unit_dim<D, NT>(u, lane));
     at[0] = q8_out2(p.bf16, o.x * inv, o.y * inv);
     at[8] = q8_out2(p.bf16, o.z * inv, o.w * inv);
 }
 
 __device__ __forceinline__ void q8_store_lse(const Q8AttendParams& p, int row0, int h0, int r,
                                              float top, float sum) {
-    const int t = r / p.G, h = r - t * p.G;
-    p.lse[(size_t)(row0 + t) * p.Hq + h0 + h] = (top + log2f(sum)) * 0.69314718055994531f;
+    p.lse[q8_out_row(p, row0, h0, r)] = (top + log2f(sum)) * 0.69314718055994531f;
 }
+
+// 1 / x (a sum of weights), 0 for 0.
+__device__ __forceinline__ float q8_inverse(float x) { return x == 0.f ? 0.f : __fdividef(1.f, x); }
 
 // A cluster's barrier, and reads of a peer's shared memory.
 __device__ __forceinline__ void q8_cluster_barrier() {
@@ -352,7 +367,7 @@ __device__ __forceinline__ void q8_finish_unit(const Q8AttendParams& p, int row0
                                                int h0, int u, int lane, const Q8Merge& m) {
     const int r = q8_unit_row<D, NT>(u, lane);
     if (r >= nrows) return;
-    q8_store_unit<D, NT>(p, row0, h0, u, lane, m.o, m.sum == 0.f ? 0.f : 1.f / m.sum);
+    q8_store_unit<D, NT>(p, row0, h0, u, lane, m.o, q8_inverse(m.sum));
     if (u % Q8Cfg<D, NT>::kTileUnits < 2 && lane < 4) q8_store_lse(p, row0, h0, r, m.top, m.sum);
 }
 
@@ -400,7 +415,7 @@ __global__ void __launch_bounds__(kQ8MergeWarps * 32) q8_merge_kernel(const Q8At
     for (int w = 0; w < kQ8MergeWarps; ++w) {
         ml[w] = s_ml[w][lane];
         v[w] = s_o[w][lane];
-        const float inv = ml[w].y == 0.f ? 0.f : 1.f / ml[w].y;
+        const float inv = q8_inverse(ml[w].y);
         v[w].x *= inv, v[w].y *= inv, v[w].z *= inv, v[w].w *= inv;
     }
     Q8Merge all;
@@ -435,7 +450,6 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
     q8_attend_kernel(const Q8AttendParams p, const __grid_constant__ Q8Maps maps) {
     using Cfg = Q8Cfg<D, NT>;
     constexpr int NS = Cfg::kStages;
-    constexpr int NP = Cfg::kPair;
     constexpr int PB = Cfg::kPage;
     constexpr int NC = D / 16;  // 16-byte chunks of a token: k steps of q.K, m tiles of P.V
 
@@ -445,11 +459,11 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
     float4* xbuf = reinterpret_cast<float4*>(ring + Cfg::kRingBytes);
     uint2* s_q = reinterpret_cast<uint2*>(xbuf + Cfg::kXBytes / 16);  // [tile][chunk][lane]
     float2* s_sc = reinterpret_cast<float2*>(s_q + Cfg::kQBytes / 8);  // K's and V's scale
-    float2* s_ml = s_sc + kQ8StagedPages;                              // [warp][row] m, sum
+    float2* s_ml = s_sc + Cfg::kStaged;                                // [warp][row] m, sum
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_ml + kWarps * Cfg::kRows);
-    float* s_qmax = reinterpret_cast<float*>(bars + kWarps * NS);  // [warp][row]
-    int* s_pid = reinterpret_cast<int*>(s_qmax + kWarps * Cfg::kRows);
-    int* s_base = s_pid + kQ8StagedPages;
+    float* s_qmax = reinterpret_cast<float*>(xbuf);  // [warp][row] (while xbuf is idle)
+    int* s_pid = reinterpret_cast<int*>(bars + kWarps * NS);
+    int* s_base = s_pid + Cfg::kStaged;
     int* s_rank = s_base + p.B + 1;
     int* s_row = s_rank + p.B + 1;
     int* s_page0 = s_row + p.B + 1;
@@ -466,6 +480,10 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
     const uint32_t ring_u = smem_u32(ring) + warp * NS * Cfg::kSlotBytes;
 
     allow_dependent_launch();
+    if (threadIdx.x == 0) {  // (the first copies would wait for them)
+        q8_prefetch_map(&maps.k);
+        q8_prefetch_map(&maps.v);
+    }
     if (lane == 0) {
 #pragma unroll
         for (int s = 0; s < NS; ++s) mbar_init(bar_w + s * 8, 1);
@@ -560,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         if constexpr (kCluster) {  // an even share of a sequence
             b = blockIdx.x / p.cluster;
             const int first = s_base[b], n = s_base[b + 1] - first;
-            range = max(NP, ((n + p.cluster - 1) / p.cluster + NP - 1) / NP * NP);
+            range = max(1, (n + p.cluster - 1) / p.cluster);
             const int at = (int)(blockIdx.x - b * p.cluster) * range;
             lo = first + min(n, at);
             hi = first + min(n, at + range);
@@ -574,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             return;
         }
         const int cost = total + kQ8Start * s_rank[p.B];
-        range = max(NP * kWarps, (cost + p.X - 1) / p.X);
+        range = max(kWarps, (cost + p.X - 1) / p.X);
         from = (int)min((long long)cost, (long long)blockIdx.x * range);
         lo = page_at(from);
         hi = page_at((long long)from + range);
@@ -592,32 +610,39 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
     // first ids are read again, in one round trip, and the work stands if no
     // length has changed.
     const bool early = p.B <= kThreads;
+    constexpr int kIds = Cfg::kStaged / kThreads;  // ids of a stretch per thread
+    const int* entry[kIds];  // where the ids of the first stretch lie
     int len = 0, s0 = 0, s1 = 0;
     if (early) {
         if (tid < p.B) read_sequence(tid, len, s0, s1);
         locate(scan(true, len, s0, s1));
-        const int f = lo + (lane / NP) * (NP * kWarps) + NP * warp + lane % NP;
-        if (lane < NS * NP && f < hi) {
-            const int id = __ldcg(table_entry(f));
-            if (id >= 0 && id < p.num_pages) {
-                const size_t at = ((size_t)id * p.Hkv + kvh) * (size_t)PB;
-                prefetch_l2(p.k + at, PB);
-                prefetch_l2(p.v + at, PB);
+        int hint[kIds];
+#pragma unroll
+        for (int i = 0; i < kIds; ++i) {
+            const int f = lo + tid + i * kThreads;
+            entry[i] = f < hi ? table_entry(f) : nullptr;
+            hint[i] = entry[i] ? __ldcg(entry[i]) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kIds; ++i) {
+            if (hint[i] < 0 || hint[i] >= p.num_pages) continue;
+            const size_t at = (size_t)hint[i] * p.Hkv + kvh;
+            prefetch_l2_line(p.k_scales + at);
+            prefetch_l2_line(p.v_scales + at);
+            if (i == 0 && tid < NS * kWarps) {  // the ring's first pages
+                prefetch_l2(p.k + at * PB, PB);
+                prefetch_l2(p.v + at * PB, PB);
             }
         }
     }
     wait_for_prerequisite_grid();
-    constexpr int kIds = kQ8StagedPages / kThreads;  // ids of a stretch per thread
     int ids[kIds];
     bool again = true;
     if (early) {
         int now = 0, now0 = 0, now1 = 0;
         if (tid < p.B) read_sequence(tid, now, now0, now1);
 #pragma unroll
-        for (int i = 0; i < kIds; ++i) {
-            const int f = lo + tid + i * kThreads;
-            ids[i] = f < hi ? __ldcg(table_entry(f)) : 0;
-        }
+        for (int i = 0; i < kIds; ++i) ids[i] = entry[i] ? __ldcg(entry[i]) : 0;
         again = __syncthreads_or(now != len || now0 != s0 || now1 != s1);
         if (again) len = now, s0 = now0, s1 = now1;
     }
@@ -666,15 +691,15 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
     bool dead = false;     // a copy timed out
     bool bad = false;      // this sequence met a bad page id or a timeout
 
-    // The q of a sequence is requested first, and again for the next sequence
-    // before the states of the present one are joined, which hides the loads.
+    // The q of a sequence is requested before the states of the one before it are joined,
+    // which hides the loads.
     auto load_q = [&](int seq) PA_INLINE_LAMBDA {
         const int n_rows = tokens_of(seq) * p.G, first = s_row[seq];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = 8 * n + g, qt = r / p.G;
+            const int r = 8 * n + g;
             const __half* row = reinterpret_cast<const __half*>(p.q) +
-                                ((size_t)(first + qt) * p.Hq + h0 + (r - qt * p.G)) * D + 4 * t;
+                                q8_out_row(p, first, h0, r) * D + 4 * t;
 #pragma unroll
             for (int i = 0; i < QL; ++i) {
                 const int c = Cfg::kQShared ? warp + i * kWarps : i;
@@ -695,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         seq_rows = T * p.G;
 #pragma unroll
         for (int n = 0; n < NT; ++n) crow[n][0] = crow[n][1] = p.scale_log2;
+        if (Cfg::kQShared) __syncthreads();  // (the previous sequence's q and xbuf are done with)
         if (p.bf16) {
             float most[NT];
 #pragma unroll
@@ -745,7 +771,6 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             }
         }
         if (Cfg::kQShared) {
-            __syncthreads();  // (no warp still reads the previous sequence's)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -770,76 +795,131 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
     // This lane's place in an ldmatrix: token and half of a pair of chunks.
     const int lm_row = (lane & 7) + (lane & 8), lm_half = lane >> 4;
 
-    // ---- N pages in shared memory, K at `at`, V PB behind it; MASK: some of
-    // their tokens may be hidden from some rows (their cells may hold anything).
-    auto pages = [&](uint32_t at0, int f0, int tok0, auto n_pages, auto mask) PA_INLINE_LAMBDA {
-        constexpr int N = decltype(n_pages)::value;
-        constexpr bool MASK = decltype(mask)::value;
-        static_assert(!MASK || N == 1, "masked pages go one at a time");
-        float s[N][NT][4];
+    // ---- What a page needs before its products where some of its tokens are hidden
+    // from some rows (their cells may hold anything): V's rows of tokens that no row
+    // sees become zeros, for 0 * NaN would be NaN; and where rows see different tokens, a
+    // NaN among V's codes of a token that only some of them see becomes NaN in those
+    // rows' sums at once (found by a product of indicators) and a zero.  Returns which
+    // scores count: bit 4 n + i for score i of tile n.
+    auto prepare_masked = [&](uint32_t kat, int tok0) PA_INLINE_LAMBDA {
+        uint32_t seen = 0;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int c = 0; c < NC; c += 2) {
-                uint32_t x[4];
-                q8_ldmatrix(x, at0 + j * 2 * PB + q8_chunk<D>(lm_row, c + lm_half));
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * n + 2 * t + i;
+                const int end = r < seq_rows ? seq_end0 + ((r * p.ginv) >> 16) : 0;
+                const int begin = p.window > 0 ? end - p.window : 0;
+                const int ta = tok0 + g, tb = ta + 8;
+                if (ta < end && ta >= begin) seen |= 1u << (4 * n + i);
+                if (tb < end && tb >= begin) seen |= 1u << (4 * n + i + 2);
+            }
+        const uint32_t vat = kat + PB;
+        const int begin0 = p.window > 0 ? seq_end0 - p.window : 0;  // the first row's
+        bool nan = false;
+#pragma unroll 1
+        for (int i = lane; i < 16 * NC; i += 32) {  // 16-byte chunks
+            const int r = i / NC, tok = tok0 + r;
+            const uint32_t at = vat + q8_chunk<D>(r, i - r * NC);
+            if (tok < begin0 || tok >= seq_L)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+            else if (seq_rows > p.G) {
+                uint4 x;
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                             : "r"(at)
+                             : "memory");
+                nan |= (q8_nan_bytes(x.x) | q8_nan_bytes(x.y) | q8_nan_bytes(x.z) | q8_nan_bytes(x.w)) != 0;
+            }
+        }
+        __syncwarp();
+        if (__any_sync(0xffffffffu, nan)) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t a0 = q8_low(x[2 * k]), a1 = q8_low(x[2 * k + 1]);
-                    const uint32_t a2 = q8_high(x[2 * k]), a3 = q8_high(x[2 * k + 1]);
+            for (int n = 0; n < NT; ++n) {
+                const uint32_t on = seen >> (4 * n);
+                const uint32_t b0 = q8_movmatrix((on & 1 ? 0x3C00u : 0u) | (on & 2 ? 0x3C000000u : 0u));
+                const uint32_t b1 = q8_movmatrix((on & 4 ? 0x3C00u : 0u) | (on & 8 ? 0x3C000000u : 0u));
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const uint2 q = Cfg::kQShared ? s_q[(n * NC + c + k) * 32 + lane]
-                                                      : qf[Cfg::kQShared ? 0 : c + k];
-                        if (c + k == 0)
-                            q8_mma0(s[j][n], a0, a1, a2, a3, q.x, q.y);
-                        else
-                            q8_mma(s[j][n], a0, a1, a2, a3, q.x, q.y);
+                for (int c = 0; c < NC; c += 2) {
+                    uint32_t x[4];
+                    q8_ldmatrix_trans(x, vat + q8_chunk<D>(lm_row, c + lm_half));
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        // (the code of 1 where there is a NaN)
+                        const uint32_t ya = (q8_nan_bytes(__byte_perm(x[2 * k], 0, 0x3120)) >> 7) * 0x38u;
+                        const uint32_t yb = (q8_nan_bytes(__byte_perm(x[2 * k + 1], 0, 0x3120)) >> 7) * 0x38u;
+                        float d[4];
+                        q8_mma0(d, q8_low(ya), q8_high(ya), q8_low(yb), q8_high(yb), b0, b1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (d[i] > 0.f) acc[n][c + k][i] = NAN;
                     }
                 }
             }
+            __syncwarp();
+#pragma unroll 1
+            for (int i = lane; i < 16 * D / 4; i += 32) {  // (words, in whatever order they lie)
+                uint32_t x;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(vat + 4 * i) : "memory");
+                x &= ~((q8_nan_bytes(x) >> 7) * 0xffu);
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(vat + 4 * i), "r"(x) : "memory");
+            }
+            __syncwarp();
         }
-        // Tokens g and g + 8 of a masked page are seen by rows whose tokens end
-        // behind them and whose window has begun.
-        [[maybe_unused]] uint32_t seen = 0;  // bit 4 n + i: score i of tile n
-        if constexpr (MASK) {
+        fence_proxy_async_smem();  // (a copy writes here next)
+        return seen;
+    };
+
+    // ---- A page in shared memory, K at `at`, V PB behind it; `masked`: see above.
+    auto page = [&](uint32_t at, int f, int tok0, bool masked) PA_INLINE_LAMBDA {
+        uint32_t seen = 0xffffffffu;
+        if (masked) seen = prepare_masked(at, tok0);
+        float s[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+        for (int c = 0; c < NC; c += 2) {
+            uint32_t x[4];
+            q8_ldmatrix(x, at + q8_chunk<D>(lm_row, c + lm_half));
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = 8 * n + 2 * t + i;
-                    const int end = r < seq_rows ? seq_end0 + r / p.G : 0;
-                    const int begin = p.window > 0 ? end - p.window : 0;
-                    const int ta = tok0 + g, tb = ta + 8;
-                    if (ta < end && ta >= begin) seen |= 1u << (4 * n + i);
-                    if (tb < end && tb >= begin) seen |= 1u << (4 * n + i + 2);
-                }
-        }
-        // s: the scores in the log2 domain; above the running maximum?
-        float2 sc[N];
-        bool over = false;
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t a0 = q8_low(x[2 * k]), a1 = q8_low(x[2 * k + 1]);
+                const uint32_t a2 = q8_high(x[2 * k]), a3 = q8_high(x[2 * k + 1]);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            sc[j] = s_sc[f0 + j];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float k0 = sc[j].x * crow[n][0], k1 = sc[j].x * crow[n][1];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[j][n][i] *= i & 1 ? k1 : k0;
-                    if (MASK && !(seen >> (4 * n + i) & 1)) s[j][n][i] = -INFINITY;
-                    over |= s[j][n][i] - m[n][i & 1] > kQ8Most;
+                for (int n = 0; n < NT; ++n) {
+                    const uint2 q = Cfg::kQShared ? s_q[(n * NC + c + k) * 32 + lane]
+                                                  : qf[Cfg::kQShared ? 0 : c + k];
+                    if (c + k == 0)
+                        q8_mma0(s[n], a0, a1, a2, a3, q.x, q.y);
+                    else
+                        q8_mma(s[n], a0, a1, a2, a3, q.x, q.y);
                 }
             }
         }
+        // s: the scores in the log2 domain, above the running maximum.
+        const float2 sc = s_sc[f];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float k0 = sc.x * crow[n][0], k1 = sc.x * crow[n][1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[n][i] *= i & 1 ? k1 : k0;
+        }
+        if (masked) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!(seen >> (4 * n + i) & 1)) s[n][i] = -INFINITY;
+        }
+        bool over = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) over |= s[n][i] - m[n][i & 1] > kQ8Most;
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float x = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < N; ++j) x = fmaxf(x, fmaxf(s[j][n][i], s[j][n][i + 2]));
+                    float x = fmaxf(s[n][i], s[n][i + 2]);
 #pragma unroll
                     for (int k = 4; k < 32; k <<= 1)
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
@@ -854,135 +934,70 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                     }
                 }
         }
-        // Weights; P^T's fragments are S^T's, each 8 x 8 block transposed.
+        // The page's V scale against the reference, which only rises.
+        if (!(sc.y <= vref)) {
+            const float f = __fdividef(vref, sc.y);
+            vref = sc.y;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            // The page's V scale against the reference, which only rises.
-            if (!(sc[j].y <= vref)) {
-                const float f = vref / sc[j].y;
-                vref = sc[j].y;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int c = 0; c < NC; ++c)
 #pragma unroll
-                    for (int c = 0; c < NC; ++c)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[n][c][i] *= f;
-            }
-            const float ratio = sc[j].y == vref ? 1.f : sc[j].y / vref;
-            const bool direct = ratio >= kQ8LeastRatio;
-            const uint32_t r2 = direct ? q8_pack(ratio, ratio) : 0x3C003C00u;
-            uint32_t b0[NT], b1[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float e[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] = ex2(s[j][n][i] - m[n][i & 1]);
-                const uint32_t ha = q8_pack(e[0], e[1]), hb = q8_pack(e[2], e[3]);
-                const float2 fa = q8_unpack(ha), fb = q8_unpack(hb);
-                l[n][0] += fa.x + fb.x;
-                l[n][1] += fa.y + fb.y;
-                b0[n] = q8_movmatrix(q8_hmul2(ha, r2));
-                b1[n] = q8_movmatrix(q8_hmul2(hb, r2));
-            }
-            // V: tokens 2 t, 2 t + 1 and 8 on, dims 2 g and 2 g + 1 of a chunk.  A token
-            // that no row sees gets the code 0: 0 * NaN would be NaN.
-            uint32_t keep_a = 0xffffffffu, keep_b = 0xffffffffu;
-            bool some = false;  // rows of their own tokens: a NaN may be hidden from some
-            if constexpr (MASK) {
-                const int begin0 = p.window > 0 ? seq_end0 - p.window : 0;
-                auto in = [&](int k) { return k >= begin0 && k < seq_L; };
-                const int k0 = tok0 + 2 * t;
-                keep_a = (in(k0) ? 0x00ff00ffu : 0u) | (in(k0 + 1) ? 0xff00ff00u : 0u);
-                keep_b = (in(k0 + 8) ? 0x00ff00ffu : 0u) | (in(k0 + 9) ? 0xff00ff00u : 0u);
-                some = seq_rows > p.G;
-            }
-            const uint32_t vat = at0 + j * 2 * PB + PB;
-            [[maybe_unused]] uint32_t nans = 0;
-            auto products = [&](auto straight) PA_INLINE_LAMBDA {
-                constexpr bool STRAIGHT = decltype(straight)::value;
-#pragma unroll
-                for (int c = 0; c < NC; c += 2) {
-                    uint32_t x[4];
-                    q8_ldmatrix_trans(x, vat + q8_chunk<D>(lm_row, c + lm_half));
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t ya = __byte_perm(x[2 * k], 0, 0x3120);
-                        uint32_t yb = __byte_perm(x[2 * k + 1], 0, 0x3120);
-                        if constexpr (MASK) {
-                            ya &= keep_a, yb &= keep_b;
-                            if (some) {
-                                const uint32_t na = q8_nan_bytes(ya), nb = q8_nan_bytes(yb);
-                                nans |= na | nb;
-                                ya &= ~((na >> 7) * 0xffu), yb &= ~((nb >> 7) * 0xffu);
-                            }
-                        }
-                        const uint32_t a0 = q8_low(ya), a1 = q8_high(ya);
-                        const uint32_t a2 = q8_low(yb), a3 = q8_high(yb);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            if constexpr (STRAIGHT) {
-                                q8_mma(acc[n][c + k], a0, a1, a2, a3, b0[n], b1[n]);
-                            } else {
-                                float d[4];
-                                q8_mma0(d, a0, a1, a2, a3, b0[n], b1[n]);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    acc[n][c + k][i] = fmaf(ratio, d[i], acc[n][c + k][i]);
-                            }
-                        }
-                    }
-                }
-            };
-            if (direct)
-                products(std::true_type{});
-            else
-                products(std::false_type{});
-            // NaN among V's codes of tokens that some rows may not see: the dims of
-            // the rows that do see them become NaN, found by a product of indicators.
-            if constexpr (MASK) {
-                if (__any_sync(0xffffffffu, nans != 0)) {
-#pragma unroll 1
-                    for (int n = 0; n < NT; ++n) {
-                        const uint32_t on = seen >> (4 * n);
-                        const uint32_t ia = (on & 1 ? 0x3C00u : 0u) | (on & 2 ? 0x3C000000u : 0u);
-                        const uint32_t ib = (on & 4 ? 0x3C00u : 0u) | (on & 8 ? 0x3C000000u : 0u);
-                        b0[0] = q8_movmatrix(ia);
-                        b1[0] = q8_movmatrix(ib);
-#pragma unroll
-                        for (int c = 0; c < NC; c += 2) {
-                            uint32_t x[4];
-                            q8_ldmatrix_trans(x, vat + q8_chunk<D>(lm_row, c + lm_half));
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                // (the code of 1 where there is a NaN)
-                                const uint32_t ya =
-                                    (q8_nan_bytes(__byte_perm(x[2 * k], 0, 0x3120) & keep_a) >> 7) * 0x38u;
-                                const uint32_t yb =
-                                    (q8_nan_bytes(__byte_perm(x[2 * k + 1], 0, 0x3120) & keep_b) >> 7) * 0x38u;
-                                float d[4];
-                                q8_mma0(d, q8_low(ya), q8_high(ya), q8_low(yb), q8_high(yb), b0[0],
-                                        b1[0]);
-#pragma unroll
-                                for (int q = 0; q < NT; ++q)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        if (q == n && d[i] > 0.f) acc[q][c + k][i] = NAN;
-                            }
-                        }
-                    }
-                }
-            }
+                    for (int i = 0; i < 4; ++i) acc[n][c][i] *= f;
         }
+        const float ratio = sc.y == vref ? 1.f : __fdividef(sc.y, vref);
+        const bool direct = ratio >= kQ8LeastRatio;
+        const uint32_t r2 = direct ? q8_pack(ratio, ratio) : 0x3C003C00u;
+        // Weights; P^T's fragments are S^T's, each 8 x 8 block transposed.
+        uint32_t b0[NT], b1[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = ex2(s[n][i] - m[n][i & 1]);
+            const uint32_t ha = q8_pack(e[0], e[1]), hb = q8_pack(e[2], e[3]);
+            const float2 fa = q8_unpack(ha), fb = q8_unpack(hb);
+            l[n][0] += fa.x + fb.x;
+            l[n][1] += fa.y + fb.y;
+            b0[n] = q8_movmatrix(q8_hmul2(ha, r2));
+            b1[n] = q8_movmatrix(q8_hmul2(hb, r2));
+        }
+        // V: tokens 2 t, 2 t + 1 and 8 on, dims 2 g and 2 g + 1 of a chunk.
+        auto products = [&](auto straight) PA_INLINE_LAMBDA {
+            constexpr bool STRAIGHT = decltype(straight)::value;
+#pragma unroll
+            for (int c = 0; c < NC; c += 2) {
+                uint32_t x[4];
+                q8_ldmatrix_trans(x, at + PB + q8_chunk<D>(lm_row, c + lm_half));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t ya = __byte_perm(x[2 * k], 0, 0x3120);
+                    const uint32_t yb = __byte_perm(x[2 * k + 1], 0, 0x3120);
+                    const uint32_t a0 = q8_low(ya), a1 = q8_high(ya);
+                    const uint32_t a2 = q8_low(yb), a3 = q8_high(yb);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if constexpr (STRAIGHT) {
+                            q8_mma(acc[n][c + k], a0, a1, a2, a3, b0[n], b1[n]);
+                        } else {
+                            float d[4];
+                            q8_mma0(d, a0, a1, a2, a3, b0[n], b1[n]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                acc[n][c + k][i] = fmaf(ratio, d[i], acc[n][c + k][i]);
+                        }
+                    }
+                }
+            }
+        };
+        if (direct)
+            products(std::true_type{});
+        else
+            products(std::false_type{});
     };
 
     const int group = blockIdx.y;
     const size_t wrow0 = ((size_t)group * p.X + blockIdx.x) * 2;
-    auto unit_of = [&](int n, int u, float f) PA_INLINE_LAMBDA {  // (constants where this is called)
-        const int c = u >> 1 << 1, k = u & 1;
-        return make_float4(acc[n][c][k] * f, acc[n][c][2 + k] * f, acc[n][c + 1][k] * f,
-                           acc[n][c + 1][2 + k] * f);
-    };
-
     // ---- The end of sequence b in this CTA.  Sequences that a border cuts (at
     // most two) are noted.  The one at the range's head is counted at once,
     // long before the CTA that has its front gets there; thread 0 looks at the
@@ -1011,67 +1026,72 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                 for (int i = 0; i < 2; ++i)
                     s_ml[warp * Cfg::kRows + 8 * n + 2 * t + i] = make_float2(m[n][i], l[n][i]);
         }
+        __syncthreads();
+        // A lane for each row: maximum and sum over the warps, and this warp's factor.
+        // (A sum of 0: the warp had no page.  NaN is kept.)
+        float top = -INFINITY, sum = 0.f, own = 0.f;
+        {
+            float2 ml[kWarps];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            __syncthreads();
-            // Maximum and sum over the warps of rows 2 t, 2 t + 1 of the tile, and this
-            // warp's factor.  (A sum of 0: the warp had no page.  NaN is kept.)
-            float top[2], sum[2], inv[2], own[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float2* ml = s_ml + 8 * n + 2 * t + k;
-                top[k] = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    if (ml[w * Cfg::kRows].y != 0.f) top[k] = fmaxf(top[k], ml[w * Cfg::kRows].x);
-                sum[k] = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float2 x = ml[w * Cfg::kRows];
-                    const float f = x.y == 0.f ? 0.f : (x.y != x.y ? NAN : ex2(x.x - top[k]));
-                    sum[k] += f * x.y;
-                    if (w == warp) own[k] = f == 0.f ? 0.f : f * vref;
-                }
-                inv[k] = sum[k] == 0.f ? 0.f : 1.f / sum[k];
+            for (int w = 0; w < kWarps; ++w) {
+                ml[w] = s_ml[w * Cfg::kRows + min(lane, Cfg::kRows - 1)];
+                if (ml[w].y != 0.f) top = fmaxf(top, ml[w].x);
             }
 #pragma unroll
-            for (int u = 0; u < Cfg::kTileUnits; ++u)
-                if ((u & 3) != warp)
-                    xbuf[(u * (kWarps - 1) + ((warp - u - 1) & 3)) * 32 + lane] =
-                        unit_of(n, u, own[u & 1]);
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ml[w].y == 0.f ? 0.f : (ml[w].y != ml[w].y ? NAN : ex2(ml[w].x - top));
+                sum += f * ml[w].y;
+                if (w == warp) own = f == 0.f ? 0.f : f * vref;
+            }
+        }
+        const float inv = q8_inverse(sum);
+        if (warp == 0 && lane < seq_rows) {
+            if (kCluster)
+                s_sum[lane] = make_float2(top, sum);
+            else if (!cut)
+                q8_store_lse(p, row0, h0, lane, top, sum);
+            else
+                reinterpret_cast<float2*>(p.ws_ml)[wrow * Cfg::kRows + lane] = make_float2(top, sum);
+        }
+        // Tile by tile the warps' shares meet in shared memory; a warp adds up units of it.
+        // (Rolled: this runs once a sequence, from instructions that have to be fetched.)
+#pragma unroll 1
+        for (int n = 0; n < NT; ++n) {
+            if (n > 0) __syncthreads();
+            const float f0 = __shfl_sync(0xffffffffu, own, 8 * n + 2 * t);
+            const float f1 = __shfl_sync(0xffffffffu, own, 8 * n + 2 * t + 1);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                if (i != n) continue;
+#pragma unroll
+                for (int u = 0; u < Cfg::kTileUnits; ++u) {
+                    const int c = u >> 1 << 1, k = u & 1;
+                    const float f = k ? f1 : f0;
+                    xbuf[(u * kWarps + warp) * 32 + lane] =
+                        make_float4(acc[i][c][k] * f, acc[i][c][2 + k] * f, acc[i][c + 1][k] * f,
+                                    acc[i][c + 1][2 + k] * f);
+                }
+            }
             __syncthreads();
+#pragma unroll 1
+            for (int u = warp; u < Cfg::kTileUnits; u += kWarps) {
+                const int r = 8 * n + 2 * t + (u & 1), un = n * Cfg::kTileUnits + u;
+                const float iv = __shfl_sync(0xffffffffu, inv, r);
+                if (r >= seq_rows) continue;
+                float4 o = xbuf[u * kWarps * 32 + lane];
 #pragma unroll
-            for (int u = 0; u < Cfg::kTileUnits; ++u) {
-                const int k = u & 1, un = n * Cfg::kTileUnits + u;
-                if ((u & 3) != warp || 8 * n + 2 * t + k >= seq_rows) continue;
-                float4 o = unit_of(n, u, own[k]);
-#pragma unroll
-                for (int x = 0; x < kWarps - 1; ++x) {
-                    const float4 v = xbuf[(u * (kWarps - 1) + x) * 32 + lane];
+                for (int w = 1; w < kWarps; ++w) {
+                    const float4 v = xbuf[(u * kWarps + w) * 32 + lane];
                     o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
                 }
                 if (!cut && !kCluster) {
-                    q8_store_unit<D, NT>(p, row0, h0, un, lane, o, inv[k]);
+                    q8_store_unit<D, NT>(p, row0, h0, un, lane, o, iv);
                 } else {
-                    o.x *= inv[k], o.y *= inv[k], o.z *= inv[k], o.w *= inv[k];
+                    o.x *= iv, o.y *= iv, o.z *= iv, o.w *= iv;
                     if (kCluster)  // (the ring is idle: this is the range's end)
                         reinterpret_cast<float4*>(ring)[un * 32 + lane] = o;
                     else
                         reinterpret_cast<float4*>(p.ws_o)[(wrow * Cfg::kUnits + un) * 32 + lane] = o;
-                }
-            }
-            if (warp == 0 && g == 0) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int r = 8 * n + 2 * t + k;
-                    if (r >= seq_rows) continue;
-                    if (kCluster)
-                        s_sum[r] = make_float2(top[k], sum[k]);
-                    else if (!cut)
-                        q8_store_lse(p, row0, h0, r, top[k], sum[k]);
-                    else
-                        reinterpret_cast<float2*>(p.ws_ml)[wrow * Cfg::kRows + r] =
-                            make_float2(top[k], sum[k]);
                 }
             }
         }
@@ -1081,17 +1101,18 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         }
     };
 
-    // ---- The range, kQ8StagedPages at a time.  Slots of NP pages go to the
-    // warps in turn; a warp's copies take its ring slots round.
+    // ---- The range, kStaged pages at a time.  Pages go to the warps in turn; a warp's
+    // copies take its ring slots round.
     constexpr int SB = Cfg::kSlotBytes;
-    using One = std::integral_constant<int, 1>;
-    using Slot = std::integral_constant<int, NP>;
     int in_slot = 0, out_slot = 0;    // ring slots of the next copy and of the next page
     uint32_t out_phase = 0;
     int pending = 0;                  // slots requested and not yet waited for
     int stall = p.stall_tx;
-    for (int c0 = lo; c0 < hi; c0 += kQ8StagedPages) {
-        const int c1 = min(hi, c0 + kQ8StagedPages);
+    bool have = false;   // the registers hold sequence b
+    int next = b;        // the sequence whose turn it is at the next border, -1: none
+    bool border = true;  // a sequence ends or the first begins
+    for (int c0 = lo; c0 < hi; c0 += Cfg::kStaged) {
+        const int c1 = min(hi, c0 + Cfg::kStaged);
         __syncthreads();  // the previous stretch's ids have been used
         bool bad_id = false;
         int mine[kIds];
@@ -1108,117 +1129,97 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             s_pid[f - c0] = mine[i] = id;
         }
         if (bad_id) atomicOr(p.err, PA_DEVERR_BAD_PAGE);
-        // With a bad id in the stretch its pages are looked at one by one.
-        const bool careful = __syncthreads_or(bad_id);
+        __syncthreads();
 
-        int ask = NP * warp;  // first page (from c0) of the next slot to request
+        int ask = warp;  // page (from c0) of the next request
         const int n_ids = c1 - c0;
         auto request = [&]() PA_INLINE_LAMBDA {
             if (lane == 0) {
                 const uint32_t bar = bar_w + in_slot * 8, dst = ring_u + in_slot * SB;
-                int id[NP], n = 0;
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    id[j] = j == 0 || ask + j < n_ids ? s_pid[ask + j] : -1;
-                    n += id[j] >= 0 ? 2 * PB : 0;
+                const int id = s_pid[ask];
+                mbar_arrive_expect_tx(bar, (id >= 0 ? 2 * PB : 0) + stall);
+                if (id >= 0) {
+                    const int row = (id * p.Hkv + kvh) * kPageSize;  // (below 2^31: checked)
+                    q8_load_page<D>(dst, &maps.k, row, bar);
+                    q8_load_page<D>(dst + PB, &maps.v, row, bar);
                 }
-                mbar_arrive_expect_tx(bar, n + stall);
-#pragma unroll
-                for (int j = 0; j < NP; ++j)
-                    if (id[j] >= 0) {
-                        const int row = (id[j] * p.Hkv + kvh) * kPageSize;  // (below 2^31: checked)
-                        q8_load_page<D>(dst + j * 2 * PB, &maps.k, row, bar);
-                        q8_load_page<D>(dst + j * 2 * PB + PB, &maps.v, row, bar);
-                    }
                 stall = 0;
             }
-            ask += NP * kWarps;
+            ask += kWarps;
             in_slot = in_slot + 1 == NS ? 0 : in_slot + 1;
             ++pending;
         };
-        // The next slot's pages are there (or the wait for them ran out).
-        auto wait = [&]() PA_INLINE_LAMBDA {
-            const uint32_t bar = bar_w + out_slot * 8;
-            if (!__all_sync(0xffffffffu, mbar_try_wait(bar, out_phase)) &&
-                !__all_sync(0xffffffffu, mbar_wait_bounded(bar, out_phase))) {
-                if (lane == 0) atomicOr(p.err, PA_DEVERR_TIMEOUT);
-                dead = bad = true;
-            }
-        };
-        auto release = [&]() PA_INLINE_LAMBDA {
-            --pending;
-            __syncwarp();  // every lane has read the slot
-            if (ask < n_ids) request();
-            if (++out_slot == NS) {
-                out_slot = 0;
-                out_phase ^= 1;
-            }
-        };
-        if (!dead)
-            for (int i = 0; i < NS && ask < n_ids; ++i) request();
         // (scales and the first q are fetched while the first pages are on their way)
+        if (!dead) {
+#pragma unroll 1
+            for (int i = 0; i < NS && ask < n_ids; ++i) request();
+        }
+        float2 scales[kIds];
 #pragma unroll
         for (int i = 0; i < kIds; ++i)
             if (mine[i] >= 0) {
                 const size_t at = (size_t)mine[i] * p.Hkv + kvh;
-                s_sc[tid + i * kThreads] = make_float2(p.k_scales[at], p.v_scales[at]);
+                scales[i] = make_float2(p.k_scales[at], p.v_scales[at]);
             }
-        if (c0 == lo) {
-            load_q(b);
-            begin_sequence();
-        }
-        __syncthreads();
+        bool staged = false;
 
-        int f = dead ? c1 : c0 + NP * warp;  // next page of this warp
+        int f = dead ? c1 : c0 + warp;  // next page of this warp
         while (true) {
+            if (border && next >= 0) load_q(next);
+            if (!staged) {
+#pragma unroll
+                for (int i = 0; i < kIds; ++i)
+                    if (mine[i] >= 0) s_sc[tid + i * kThreads] = scales[i];
+                __syncthreads();
+                staged = true;
+            }
+            if (border) {
+                if (have) end_sequence();
+                if (next < 0) break;
+                b = next;
+                begin_sequence();
+                have = true;
+                border = false;
+            }
             const int seg_end = min(c1, s_base[b + 1]);
             // Pages that all rows see whole lie in [whole0, whole1).
             const int base = -s_page0[b];  // page of token 0
             const int begin = p.window > 0 ? max(0, seq_L - p.window) : 0;  // the last row's
-            const int whole0 = careful ? INT_MAX : base + (begin + kPageSize - 1) / kPageSize;
-            const int whole1 = min(seg_end, base + max(seq_end0, 0) / kPageSize);
+            const int whole0 = base + (begin + kPageSize - 1) / kPageSize;
+            const int whole1 = base + max(seq_end0, 0) / kPageSize;
             while (f < seg_end) {
-                if (((f - c0) & (NP - 1)) == 0) {
-                    // Slots of whole pages, the bulk of a long sequence.
-                    if (f >= whole0) {
-                        for (; f + NP <= whole1; f += NP * kWarps) {
-                            wait();
-                            if (dead) break;
-                            pages(ring_u + out_slot * SB, f - c0, 0, Slot{}, std::false_type{});
-                            release();
-                        }
-                        if (!dead && f >= seg_end) break;
-                    }
-                    if (!dead) wait();
-                    if (dead) {
-                        f = c1;
-                        break;
-                    }
+                // The page is there (or the wait for it ran out).
+                const uint32_t bar = bar_w + out_slot * 8;
+                if (!__all_sync(0xffffffffu, mbar_try_wait(bar, out_phase)) &&
+                    !__all_sync(0xffffffffu, mbar_wait_bounded(bar, out_phase))) {
+                    if (lane == 0) atomicOr(p.err, PA_DEVERR_TIMEOUT);
+                    dead = bad = true;
+                    f = c1;
+                    break;
                 }
-                // One page, with some of its tokens masked or a bad id near.
-                if (careful && s_pid[f - c0] < 0)
+                if (s_pid[f - c0] < 0)
                     bad = true;
                 else
-                    pages(ring_u + out_slot * SB + ((f - c0) & (NP - 1)) * 2 * PB, f - c0,
-                          (f - base) * kPageSize, One{}, std::true_type{});
-                ++f;
-                if (((f - c0) & (NP - 1)) == 0 || f == c1) {  // the slot is used up
-                    f += NP * (kWarps - 1);
-                    release();
+                    page(ring_u + out_slot * SB, f - c0, (f - base) * kPageSize,
+                         f < whole0 || f >= whole1);
+                f += kWarps;
+                --pending;
+                __syncwarp();  // every lane has read the slot
+                if (ask < n_ids) request();
+                if (++out_slot == NS) {
+                    out_slot = 0;
+                    out_phase ^= 1;
                 }
             }
             if (s_base[b + 1] > c1 && c1 < hi) break;  // goes on in the next stretch
+            border = true;
             if (s_base[b + 1] >= hi) {  // the range's last
-                end_sequence();
-                break;
+                next = -1;
+                continue;
             }
-            int next = b + 1;
+            next = b + 1;
             while (s_base[next + 1] == s_base[next]) ++next;
-            load_q(next);
-            end_sequence();
-            b = next;
-            begin_sequence();
-            if (s_base[b] >= c1) break;
+            if (s_base[next] >= c1) break;  // begins in the next stretch
         }
     }
     if constexpr (kCluster) {
@@ -1229,6 +1230,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         q8_cluster_barrier();
         const int rank = blockIdx.x - b * p.cluster;
         const int rows = (s_base[b + 1] - s_base[b] + range - 1) / range;
+#pragma unroll 1
         for (int u = rank * kWarps + warp; u < Cfg::kUnits; u += p.cluster * kWarps) {
             const int r = q8_unit_row<D, NT>(u, lane), n_rows = tokens_of(b) * p.G;
             Q8Merge mg;
@@ -1238,10 +1240,12 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                 float4 v[N];
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const int peer = min(r0 + i, rows - 1);
-                    ml[i] = q8_ld_peer2(q8_peer(s_sum + r, peer));
-                    v[i] = q8_ld_peer4(q8_peer(ring + (u * 32 + lane) * 16, peer));
-                    if (r0 + i >= rows || r >= n_rows) ml[i] = make_float2(-INFINITY, 0.f);
+                    ml[i] = make_float2(-INFINITY, 0.f);
+                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (r0 + i < rows && r < n_rows) {
+                        ml[i] = q8_ld_peer2(q8_peer(s_sum + r, r0 + i));
+                        v[i] = q8_ld_peer4(q8_peer(ring + (u * 32 + lane) * 16, r0 + i));
+                    }
                 }
                 mg.add(ml, v);
             }
