@@ -2,8 +2,8 @@
 
 Each translation unit under csrc/ compiles in parallel; the objects link into
 one shared library with the static CUDA runtime.  csrc/pa_pyfast.cpp, the
-argument marshalling of q4.py, becomes a Python extension beside it where the
-interpreter's and torch's headers are installed (q4.py works without it).  It reads
+argument marshalling of q4.py and q8.py, becomes a Python extension beside it where the
+interpreter's and torch's headers are installed (both work without it).  It reads
 torch's tensors by their layout and calls the library by the headers' prototypes, so
 its file is named by a digest of all that it was compiled from: one of other sources,
 another torch or another interpreter is never loaded.  Usage:
@@ -29,7 +29,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpa_gb300.so")
 PYFAST_SRC = os.path.join(CSRC, "pa_pyfast.cpp")
-PYFAST_HEADERS = [os.path.join(ROOT, "include", h) for h in ("pa.h", "pa_q4.h")]
+PYFAST_HEADERS = [os.path.join(ROOT, "include", h) for h in ("pa.h", "pa_q4.h", "pa_q8.h")]
 PYFAST_FLAGS = ["-O2", "-std=c++17", "-shared", "-fPIC"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -113,7 +113,7 @@ def _finish_pyfast(job) -> None:
     if proc.wait() == 0:
         os.replace(tmp, path)
     else:
-        print("the marshalling extension was not built; q4.py goes without it", file=sys.stderr)
+        print("the marshalling extension was not built; q4.py and q8.py go without it", file=sys.stderr)
         if os.path.exists(tmp):
             os.remove(tmp)
 

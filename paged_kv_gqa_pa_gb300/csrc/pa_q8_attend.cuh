@@ -78,7 +78,7 @@ template <int D, int NT>
 struct Q8Cfg {
     static constexpr int kPage = 16 * D;           // bytes of a page of K, or of V
     static constexpr int kSlotBytes = 2 * kPage;   // a ring slot: a page's K and V
-    static constexpr int kStages = D == 256 ? 2 : (D == 64 ? 4 : 3);
+    static constexpr int kStages = D == 64 ? 4 : (NT > 2 ? 3 : 2);
     static constexpr int kRingBytes = kWarps * kStages * kSlotBytes;
     // q's fragments: in registers, or in shared memory where the accumulators
     // leave no room for them.
@@ -91,7 +91,7 @@ struct Q8Cfg {
     static_assert(kUnits * 512 <= kRingBytes, "a cluster's CTA leaves its state in the ring");
     static constexpr int kXBytes = kTileUnits * kWarps * 512;
     // Page ids and scales that a CTA stages at a time.
-    static constexpr int kStaged = NT == 2 && D >= 128 ? 256 : 512;
+    static constexpr int kStaged = NT == 2 && D == 256 ? 256 : 512;
     static constexpr int kSmemBytes = 1024 + kRingBytes + kXBytes + kQBytes + kStaged * 12 +
                                       kWarps * kRows * 8 + kWarps * kStages * 8;
     // CTAs per SM by registers.
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_ml + kWarps * Cfg::kRows);
     float* s_qmax = reinterpret_cast<float*>(xbuf);  // [warp][row] (while xbuf is idle)
     int* s_pid = reinterpret_cast<int*>(bars + kWarps * NS);
-    int* s_base = s_pid + Cfg::kStaged;
+    int* s_base = s_pid + Cfg::kStaged;  // (s_pid: first row of the page in the cache's maps)
     int* s_rank = s_base + p.B + 1;
     int* s_row = s_rank + p.B + 1;
     int* s_page0 = s_row + p.B + 1;
@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
     };
 
     // ---- A page in shared memory, K at `at`, V PB behind it; `masked`: see above.
-    auto page = [&](uint32_t at, int f, int tok0, bool masked) PA_INLINE_LAMBDA {
+    auto page = [&](uint32_t at, float2 sc, int tok0, bool masked) PA_INLINE_LAMBDA {
         uint32_t seen = 0xffffffffu;
         if (masked) seen = prepare_masked(at, tok0);
         float s[NT][4];
@@ -894,38 +894,43 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                 }
             }
         }
-        // s: the scores in the log2 domain, above the running maximum.
-        const float2 sc = s_sc[f];
+        // e: the scores in the log2 domain, above the running maximum.
+        float e[NT][4], most = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float k0 = sc.x * crow[n][0], k1 = sc.x * crow[n][1];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][i] *= i & 1 ? k1 : k0;
+            for (int i = 0; i < 4; ++i) e[n][i] = fmaf(s[n][i], i & 1 ? k1 : k0, -m[n][i & 1]);
         }
         if (masked) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (!(seen >> (4 * n + i) & 1)) s[n][i] = -INFINITY;
+                    if (!(seen >> (4 * n + i) & 1)) e[n][i] = -INFINITY;
         }
-        bool over = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) over |= s[n][i] - m[n][i & 1] > kQ8Most;
-        if (__any_sync(0xffffffffu, over)) {
+            for (int i = 0; i < 4; ++i) most = fmaxf(most, e[n][i]);
+        if (__any_sync(0xffffffffu, most > kQ8Most)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float x = fmaxf(s[n][i], s[n][i + 2]);
+                    // (again from the products: against no maximum yet, e has lost them)
+                    const float k = sc.x * crow[n][i];
+                    const float xa = e[n][i] == -INFINITY ? -INFINITY : s[n][i] * k;
+                    const float xb = e[n][i + 2] == -INFINITY ? -INFINITY : s[n][i + 2] * k;
+                    float x = fmaxf(xa, xb);
 #pragma unroll
-                    for (int k = 4; k < 32; k <<= 1)
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+                    for (int k2 = 4; k2 < 32; k2 <<= 1)
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k2));
                     const float top = fmaxf(m[n][i], x - kQ8Room);
                     const float f = ex2(m[n][i] - top);
                     m[n][i] = top;
+                    e[n][i] = xa - top;
+                    e[n][i + 2] = xb - top;
                     l[n][i] *= f;
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
@@ -952,10 +957,8 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         uint32_t b0[NT], b1[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float e[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = ex2(s[n][i] - m[n][i & 1]);
-            const uint32_t ha = q8_pack(e[0], e[1]), hb = q8_pack(e[2], e[3]);
+            const uint32_t ha = q8_pack(ex2(e[n][0]), ex2(e[n][1]));
+            const uint32_t hb = q8_pack(ex2(e[n][2]), ex2(e[n][3]));
             const float2 fa = q8_unpack(ha), fb = q8_unpack(hb);
             l[n][0] += fa.x + fb.x;
             l[n][1] += fa.y + fb.y;
@@ -1126,7 +1129,8 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                 id = -1;
                 bad_id = true;
             }
-            s_pid[f - c0] = mine[i] = id;
+            mine[i] = id;
+            s_pid[f - c0] = id < 0 ? -1 : (id * p.Hkv + kvh) * kPageSize;  // (below 2^31: checked)
         }
         if (bad_id) atomicOr(p.err, PA_DEVERR_BAD_PAGE);
         __syncthreads();
@@ -1136,10 +1140,9 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         auto request = [&]() PA_INLINE_LAMBDA {
             if (lane == 0) {
                 const uint32_t bar = bar_w + in_slot * 8, dst = ring_u + in_slot * SB;
-                const int id = s_pid[ask];
-                mbar_arrive_expect_tx(bar, (id >= 0 ? 2 * PB : 0) + stall);
-                if (id >= 0) {
-                    const int row = (id * p.Hkv + kvh) * kPageSize;  // (below 2^31: checked)
+                const int row = s_pid[ask];
+                mbar_arrive_expect_tx(bar, (row >= 0 ? 2 * PB : 0) + stall);
+                if (row >= 0) {
                     q8_load_page<D>(dst, &maps.k, row, bar);
                     q8_load_page<D>(dst + PB, &maps.v, row, bar);
                 }
@@ -1149,23 +1152,25 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             in_slot = in_slot + 1 == NS ? 0 : in_slot + 1;
             ++pending;
         };
-        // (scales and the first q are fetched while the first pages are on their way)
-        if (!dead) {
-#pragma unroll 1
-            for (int i = 0; i < NS && ask < n_ids; ++i) request();
-        }
+        // Scales and the first q are asked for before the first pages: behind them they
+        // would wait for all that the ring holds.
         float2 scales[kIds];
 #pragma unroll
         for (int i = 0; i < kIds; ++i)
             if (mine[i] >= 0) {
                 const size_t at = (size_t)mine[i] * p.Hkv + kvh;
-                scales[i] = make_float2(p.k_scales[at], p.v_scales[at]);
+                scales[i] = make_float2(__ldcg(p.k_scales + at), __ldcg(p.v_scales + at));
             }
+        if (border && next >= 0) load_q(next);
+        if (!dead) {
+#pragma unroll 1
+            for (int i = 0; i < NS && ask < n_ids; ++i) request();
+        }
         bool staged = false;
 
         int f = dead ? c1 : c0 + warp;  // next page of this warp
         while (true) {
-            if (border && next >= 0) load_q(next);
+            if (border && next >= 0 && staged) load_q(next);
             if (!staged) {
 #pragma unroll
                 for (int i = 0; i < kIds; ++i)
@@ -1190,6 +1195,8 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             while (f < seg_end) {
                 // The page is there (or the wait for it ran out).
                 const uint32_t bar = bar_w + out_slot * 8;
+                const float2 sc = s_sc[f - c0];
+                const int row = s_pid[f - c0];
                 if (!__all_sync(0xffffffffu, mbar_try_wait(bar, out_phase)) &&
                     !__all_sync(0xffffffffu, mbar_wait_bounded(bar, out_phase))) {
                     if (lane == 0) atomicOr(p.err, PA_DEVERR_TIMEOUT);
@@ -1197,10 +1204,10 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                     f = c1;
                     break;
                 }
-                if (s_pid[f - c0] < 0)
+                if (row < 0)
                     bad = true;
                 else
-                    page(ring_u + out_slot * SB, f - c0, (f - base) * kPageSize,
+                    page(ring_u + out_slot * SB, sc, (f - base) * kPageSize,
                          f < whole0 || f >= whole1);
                 f += kWarps;
                 --pending;

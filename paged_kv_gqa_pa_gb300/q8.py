@@ -17,9 +17,10 @@ import ctypes
 
 import torch
 
+from . import q4 as _q4
 from .binding import PA_DTYPE_F16, PA_OK, PAError, new_workspace, pa_get_error
-from .q4 import (_DTYPE, _TORCH, PAGE_SIZE, _call, _check, _check_device, _device_of,
-                 _error_ptr, _lib as _q4_lib, _rows, _stream)
+from .q4 import (_DTYPE, _TORCH, PAGE_SIZE, _answer, _call, _check, _check_device, _device_of,
+                 _error_ptr, _rows, _stream)
 
 PA_DEVERR_BAD_TOKEN = 32
 PA_VERIFY_MAX_DRAFTS = 32
@@ -61,7 +62,7 @@ def _lib():
     global _bound
     if _bound is not None:
         return _bound
-    lib = _q4_lib()
+    lib = _q4._lib()
     P, i, ll, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
     plan = ctypes.POINTER(pa_q8_plan_t)
     rows = [i] * 8 + [f, f] + [P, ll] * 3 + [P] * 5 + [ll, P, P]
@@ -77,8 +78,17 @@ def _lib():
     lib.pa_q8_decode.restype = i
     lib.pa_verify_drafts.argtypes = [i] * 4 + [P] * 10
     lib.pa_verify_drafts.restype = i
+    if _q4._fast is not None:
+        names = ("pa_append", "pa_q8_append", "pa_q8_read", "pa_q8_decode", "pa_verify_drafts")
+        _q4._fast.setup_q8(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                                 for n in names))
     _bound = lib
     return lib
+
+
+def _fast():
+    """The marshalling extension (as q4.py's), once the library is loaded."""
+    return _q4._fast if _bound is not None else None
 
 
 def new_q8_cache(num_pages, num_kv_heads, head_dim, device=None):
@@ -150,6 +160,10 @@ def pa_append(q, k, v, slots, positions, k_cache, v_cache, q_out=None, q_norm=No
     and rotated (theta > 0, positions int32 [tokens]), q written to q_out (default: in place),
     k and v into the paged cache [num_pages, Hkv, 16, D] of their type at `slots` (int64
     [tokens], distinct; -1: left out).  q may be None."""
+    if device_error is None and stream is None and (fast := _fast()) is not None and _answer(
+            "pa_append", fast.append(q, k, v, slots, positions, k_cache, v_cache, q_out, q_norm,
+                                     k_norm, eps, theta, rotary_dim)):
+        return
     dev, _, args = _append_args(q, k, v, slots, positions, k_cache, v_cache, q_out, q_norm,
                                 k_norm, eps, theta, rotary_dim, None)
     _call(_lib().pa_append, dev, (*args, _error_ptr(device_error, dev), _stream(stream, dev)))
@@ -160,6 +174,11 @@ def pa_q8_append(q, k, v, slots, positions, k_cache, v_cache, k_scales, v_scales
                  device_error=None, stream=None) -> None:
     """pa_append into an 8-bit cache (``new_q8_cache``).  A page's rows lie next to one another
     among the tokens, at ascending slots; see include/pa_q8.h."""
+    if device_error is None and stream is None and (fast := _fast()) is not None and _answer(
+            "pa_q8_append", fast.q8_append(q, k, v, slots, positions, k_cache, v_cache, q_out,
+                                           q_norm, k_norm, eps, theta, rotary_dim, k_scales,
+                                           v_scales)):
+        return
     dev, shape, args = _append_args(q, k, v, slots, positions, k_cache, v_cache, q_out, q_norm,
                                     k_norm, eps, theta, rotary_dim, _F8)
     _call(_lib().pa_q8_append, dev,
@@ -172,6 +191,9 @@ def pa_q8_read(k_cache, v_cache, k_scales, v_scales, slots, k_out, v_out, device
                stream=None) -> None:
     """Rows an 8-bit cache stands for at `slots`, into k_out, v_out [tokens, Hkv, D] (fp16, bf16
     or fp32; slot -1: zeros)."""
+    if device_error is None and stream is None and (fast := _fast()) is not None and _answer(
+            "pa_q8_read", fast.q8_read(k_cache, v_cache, k_scales, v_scales, slots, k_out, v_out)):
+        return
     dev = _three(k_out, "k_out")
     n, hkv, D = k_out.shape
     et = k_out.dtype
@@ -238,6 +260,11 @@ def pa_q8_decode(plan, q, starts, k_cache, v_cache, k_scales, v_scales, block_ta
     """Attention of rows starts[b] .. starts[b + 1] - 1 of q [rows, Hq, D], sequence b's last
     tokens, over an 8-bit cache (starts int32 [B + 1], as pa_extend_tables makes them; None: one
     row per sequence); the other arguments as pa_decode's."""
+    if stream is None and (fast := _fast()) is not None and _answer(
+            "pa_q8_decode", fast.q8_decode(plan, q, starts, k_cache, v_cache, k_scales, v_scales,
+                                           block_tables, context_lens, scale, window, out, lse,
+                                           workspace)):
+        return
     dev, args = _q8_decode_args(plan, q, starts, k_cache, v_cache, k_scales, v_scales,
                                 block_tables, context_lens, scale, window, out, lse, workspace,
                                 stream)
@@ -313,6 +340,10 @@ def pa_verify_drafts(target_probs, draft_probs, draft_tokens, num_drafts, accept
     target_probs [B, T + 1, V] and draft_probs [B, T, V] (None: certain drafts), and `tokens`
     (int32 [B, T + 1]) gets them, one drawn token and -1.  num_drafts int32 [B] (None: T each),
     random numbers accept_u [B, T] and sample_u [B] float32 of [0, 1); see include/pa_q8.h."""
+    if device_error is None and stream is None and (fast := _fast()) is not None and _answer(
+            "pa_verify_drafts", fast.verify(target_probs, draft_probs, draft_tokens, num_drafts,
+                                            accept_u, sample_u, accepted, tokens)):
+        return
     dev = _three(target_probs, "target_probs")
     B, T1, V = target_probs.shape
     T, et, i32, f32 = T1 - 1, target_probs.dtype, torch.int32, torch.float32

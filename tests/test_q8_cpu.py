@@ -287,3 +287,149 @@ def test_binding_refuses_host_tensors_and_wrong_arguments():
         pa.q8_decode(k.float(), None, kc, vc, ks, vs, i, i, 1.0)
     with pytest.raises(ValueError, match="CUDA"):
         pa.pa_verify_drafts(k.float(), None, i, None, k, k, i, i)
+
+
+# ---------------------------------------------------------------- the marshalling extension
+
+def tens(dtype, shape, stride=None):
+    """A CPU tensor of this form (its device, -1, is the stand-in's current one)."""
+    return torch.empty(shape, dtype=dtype) if stride is None else \
+        torch.empty_strided(shape, stride, dtype=dtype)
+
+
+@pytest.fixture
+def marshalled(lib):
+    """The extension with recording stand-ins for the five C functions; yields (module, calls)."""
+    from paged_kv_gqa_pa_gb300 import q4
+    if q4._fast is None:
+        pytest.skip("the marshalling extension is not built here")
+    calls = []
+    P, i, ll, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
+    rows = [i] * 8 + [f, f] + [P, ll] * 3 + [P] * 5 + [ll, P, P]
+    protos = dict(append=ctypes.CFUNCTYPE(i, *rows, P, P), q8_append=ctypes.CFUNCTYPE(i, *rows, *[P] * 4),
+                  q8_read=ctypes.CFUNCTYPE(i, *[i] * 6, *[P] * 5, P, ll, P, ll, P, P),
+                  q8_decode=ctypes.CFUNCTYPE(i, P, i, *[P] * 8, f, i, *[P] * 4),
+                  verify=ctypes.CFUNCTYPE(i, *[i] * 4, *[P] * 10))
+    keep = []
+    for name, proto in protos.items():
+        def fn(*a, name=name):
+            if name == "q8_decode":
+                a = (ctypes.string_at(a[0], ctypes.sizeof(q8.pa_q8_plan_t)),) + a[1:]
+            calls.append((name, a))
+            return 4 if name == "q8_read" else 0
+        keep.append(proto(fn))
+    q4._fast.setup((1, 2, 3, 4, 5), lambda: -1, lambda d: 4096 + d)
+    q4._fast.setup_q8(tuple(ctypes.cast(fn, P).value for fn in keep))
+    yield q4._fast, calls
+    q4._load_fast(lib)  # the real functions again
+    q4._fast.setup_q8(tuple(ctypes.cast(getattr(lib, n), P).value for n in
+                            ("pa_append", "pa_q8_append", "pa_q8_read", "pa_q8_decode",
+                             "pa_verify_drafts")))
+
+
+def at(*t):
+    return tuple(None if x is None else x.data_ptr() for x in t)
+
+
+F16, F32, I32, I64, F8 = (torch.float16, torch.float32, torch.int32, torch.int64,
+                          torch.float8_e4m3fn)
+
+
+def test_marshalling_of_the_usual_calls(marshalled):
+    fast, calls = marshalled
+    wide = (8 * 128, 128, 1)
+    q, k, v = tens(F16, (5, 4, 128), wide), tens(F16, (5, 2, 128), wide), tens(F16, (5, 2, 128), wide)
+    qo, qn, kn = tens(F16, (5, 4, 128)), tens(F16, (128,)), tens(F16, (128,))
+    sl, pos = tens(I64, (5,)), tens(I32, (5,))
+    k16, v16 = tens(F16, (9, 2, 16, 128)), tens(F16, (9, 2, 16, 128))
+    assert fast.append(q, k, v, sl, pos, k16, v16, qo, qn, kn, 0.5, 1e4, 64) == 0
+    assert calls.pop() == ("append", (5, 4, 2, 128, 64, 16, 9, 0, 1e4, 0.5, *at(q), 1024, *at(k), 1024,
+                                      *at(v), 1024, *at(qn, kn, pos, sl, qo), 512, *at(k16, v16), None,
+                                      4095))
+    assert fast.append(None, k, v, sl, None, k16, v16, None, None, None, 0.5, 0.0, None) == 0
+    assert calls.pop() == ("append", (5, 0, 2, 128, 128, 16, 9, 0, 0.0, 0.5, None, 0, *at(k), 1024,
+                                      *at(v), 1024, None, None, None, *at(sl), None, 0,
+                                      *at(k16, v16), None, 4095))
+    kc, vc = tens(F8, (9, 2, 16, 128)), tens(F8, (9, 2, 16, 128))
+    ks, vs = tens(F32, (9, 2)), tens(F32, (9, 2))
+    assert fast.q8_append(q, k, v, sl, pos, kc, vc, None, None, kn, 0.5, 1e4, None, ks, vs) == 0
+    assert calls.pop() == ("q8_append", (5, 4, 2, 128, 128, 16, 9, 0, 1e4, 0.5, *at(q), 1024, *at(k),
+                                         1024, *at(v), 1024, None, *at(kn, pos, sl, q), 1024,
+                                         *at(kc, vc, ks, vs), None, 4095))
+    assert fast.q8_read(kc, vc, ks, vs, sl, k, v) == 4  # the status comes back
+    assert calls.pop() == ("q8_read", (5, 2, 128, 16, 9, 0, *at(kc, vc, ks, vs, sl, k), 1024, *at(v), 1024,
+                                       None, 4095))
+    plan = _plan(num_pages=9, max_query_len=3)
+    dq, do, lse = tens(F16, (7, 8, 128)), tens(F16, (7, 8, 128)), tens(F32, (7, 8))
+    st, bt, cl = tens(I32, (5,)), tens(I32, (4, 16)), tens(I32, (4,))
+    ws = tens(torch.uint8, (plan.workspace_bytes,))
+    for s in (st, None):
+        assert fast.q8_decode(plan, dq, s, kc, vc, ks, vs, bt, cl, 0.5, 3, do, lse, ws) == 0
+        assert calls.pop() == ("q8_decode", (bytes(plan), 7, *at(dq, s, kc, vc, ks, vs, bt, cl), 0.5, 3,
+                                             *at(do, lse, ws), 4095))
+    p, d = tens(F32, (2, 4, 50)), tens(F32, (2, 3, 50))
+    x, n, u, s = tens(I32, (2, 3)), tens(I32, (2,)), tens(F32, (2, 3)), tens(F32, (2,))
+    acc, tok = tens(I32, (2,)), tens(I32, (2, 4))
+    for dd, nn in ((d, n), (None, None)):
+        assert fast.verify(p, dd, x, nn, u, s, acc, tok) == 0
+        assert calls.pop() == ("verify", (2, 3, 50, 2, *at(p, dd, x, nn, u, s, acc, tok), None, 4095))
+    assert not calls
+
+
+def test_marshalling_leaves_everything_else_alone(marshalled):
+    fast, calls = marshalled
+    k, q = tens(F16, (5, 2, 128)), tens(F16, (5, 4, 128))
+    sl, pos, w = tens(I64, (5,)), tens(I32, (5,)), tens(F16, (128,))
+    k16, kc, ks = tens(F16, (9, 2, 16, 128)), tens(F8, (9, 2, 16, 128)), tens(F32, (9, 2))
+    base = [q, k, k, sl, pos, k16, k16, q, w, w, 0.5, 1e4, 64]
+    assert fast.append(*base) == 0
+    assert fast.q8_append(*base[:5], kc, kc, *base[7:], ks, ks) == 0
+    calls.clear()
+    for i, bad in [(0, tens(F16, (4, 4, 128))), (0, tens(F32, (5, 4, 128))), (0, None), (0, 3),
+                   (1, tens(F16, (5, 256))), (1, tens(F16, (5, 2, 128), (256, 1, 2))),
+                   (2, tens(F16, (5, 3, 128))), (2, tens(torch.bfloat16, (5, 2, 128))),
+                   (3, tens(I32, (5,))), (3, tens(I64, (6,))), (4, None), (4, tens(I64, (5,))),
+                   (7, tens(F16, (5, 2, 128))), (8, tens(F16, (64,))), (9, tens(F32, (128,))),
+                   (10, 1), (11, 10000), (12, 64.0), (12, True)]:
+        a = list(base)
+        a[i] = bad
+        assert fast.append(*a) is None, (i, bad)
+        assert fast.q8_append(*a[:5], kc, kc, *a[7:], ks, ks) is None, (i, bad)
+    for cache in (kc, tens(F16, (9, 3, 16, 128)), tens(F16, (9, 2, 8, 128)), tens(F16, (9, 2, 16, 64)),
+                  tens(F16, (9, 2, 16, 128), (4096, 2048, 1, 16))):
+        assert fast.append(*base[:5], cache, k16, *base[7:]) is None
+        assert fast.append(*base[:5], k16, cache, *base[7:]) is None
+    for a in ((k16, kc, ks, ks), (kc, tens(F8, (8, 2, 16, 128)), ks, ks), (kc, kc, tens(F32, (9, 3)), ks),
+              (kc, kc, ks, tens(F16, (9, 2)))):
+        assert fast.q8_append(*base[:5], *a[:2], *base[7:], *a[2:]) is None
+        assert fast.q8_read(*a, sl, k, k) is None
+    assert fast.q8_read(kc, kc, ks, ks, tens(I64, (4,)), k, k) is None
+    assert fast.q8_read(kc, kc, ks, ks, sl, k, tens(F32, (5, 2, 128))) is None
+    plan = _plan(num_pages=9)
+    base = [plan, tens(F16, (7, 8, 128)), tens(I32, (5,)), kc, kc, ks, ks, tens(I32, (4, 16)),
+            tens(I32, (4,)), 0.5, 0, tens(F16, (7, 8, 128)), tens(F32, (7, 8)),
+            tens(torch.uint8, (plan.workspace_bytes,))]
+    assert fast.q8_decode(*base) == 0
+    calls.clear()
+    for i, bad in [(0, object()), (0, b"x" * 8), (1, tens(F16, (7, 4, 128))), (1, tens(F16, (8, 128))),
+                   (2, tens(I32, (4,))), (2, tens(I64, (5,))), (3, k16), (5, tens(F32, (9,))),
+                   (7, tens(I32, (4, 15))), (8, tens(I64, (4,))), (9, 1), (10, 0.0),
+                   (11, tens(F16, (6, 8, 128))), (12, tens(F32, (7, 4))),
+                   (13, tens(torch.uint8, (plan.workspace_bytes - 1,)))]:
+        a = list(base)
+        a[i] = bad
+        assert fast.q8_decode(*a) is None, (i, bad)
+    few = [plan, tens(F16, (3, 8, 128)), None, *base[3:11], tens(F16, (3, 8, 128)), tens(F32, (3, 8)), base[13]]
+    assert fast.q8_decode(*few) is None  # fewer rows than sequences without starts
+    base = [tens(F32, (2, 4, 50)), tens(F32, (2, 3, 50)), tens(I32, (2, 3)), tens(I32, (2,)),
+            tens(F32, (2, 3)), tens(F32, (2,)), tens(I32, (2,)), tens(I32, (2, 4))]
+    assert fast.verify(*base) == 0
+    calls.clear()
+    for i, bad in [(0, tens(F32, (2, 50))), (0, tens(I32, (2, 4, 50))), (1, tens(F16, (2, 3, 50))),
+                   (1, tens(F32, (2, 4, 50))), (2, None), (2, tens(I64, (2, 3))), (3, tens(I32, (3,))),
+                   (4, tens(F32, (2, 4))), (5, None), (6, tens(F32, (2,))), (7, tens(I32, (2, 3)))]:
+        a = list(base)
+        a[i] = bad
+        assert fast.verify(*a) is None, (i, bad)
+    assert fast.verify(*base[:7]) is None and fast.q8_read(1) is None
+    assert not calls

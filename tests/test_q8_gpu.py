@@ -1303,3 +1303,31 @@ def test_a_loop_of_drafts_and_verification(dtype, D, graph):
         hp = hp + a + 1
         assert np.array_equal(past.cpu().numpy(), hp)
         assert pa.pa_get_error_ex(err) == 0 and pa.pa_get_error(b["ws"]) == 0
+
+
+def test_calls_without_the_marshalling_extension(monkeypatch):
+    """The same calls through the Python checks alone give the same bits."""
+    if q4._fast is None:
+        pytest.skip("the marshalling extension is not built here")
+    fast = q4._fast
+    n, hq, hkv, D = 40, 4, 2, 128
+    r = Rows(50, n, hq, hkv, D, "f16", True, 1e4, 64)
+    slots, results = i64(np.arange(n)), []
+    d = Decode(51, [100, 20], hq, hkv, D, "f16", T=2)
+    c = verify_case(52, 3, 700, 2, "f32")
+    for ext in (fast, None):
+        monkeypatch.setattr(q4, "_fast", ext)
+        q_out = torch.empty(n, hq, D, dtype=torch.float16, device="cuda")
+        kc, vc = (torch.zeros(3, hkv, 16, D, dtype=torch.float16, device="cuda") for _ in range(2))
+        pa.pa_append(r.tq, r.tk, r.tv, slots, i32(r.pos), kc, vc, q_out=q_out, **r.kw)
+        cache = pa.new_q8_cache(3, hkv, D)
+        q2 = torch.empty_like(q_out)
+        pa.pa_q8_append(r.tq, r.tk, r.tv, slots, i32(r.pos), *cache, q_out=q2, **r.kw)
+        k, v = (torch.empty(n, hkv, D, dtype=torch.float16, device="cuda") for _ in range(2))
+        pa.pa_q8_read(*cache, slots, k, v)
+        out, lse, err = d.run(0.1)
+        acc, tok = run_verify(c, "f32")
+        results.append([q_out, kc, vc, q2, k, v, *cache[2:], cache[0].view(torch.uint8),
+                        cache[1].view(torch.uint8), *map(torch.from_numpy, (out, lse, acc, tok))])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
