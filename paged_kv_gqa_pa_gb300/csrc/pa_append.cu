@@ -9,6 +9,7 @@
 #include <float.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include "../../include/pa_q8.h"
@@ -19,6 +20,7 @@ namespace pa {
 
 constexpr int kAppendThreads = 256;  // at most, of pa_append
 constexpr int kAppendItems = 2;      // items a thread requests before it waits for the angles
+constexpr int kMaxTileBytes = 48 << 10;  // of rows that a CTA holds at a time
 constexpr int kAppendCtas = 608;     // CTAs that fill the GPU: four for each of 152 SMs
 
 struct AppendParams {
@@ -68,12 +70,17 @@ struct RowLanes {
         for (int m = 1; m < kLanes; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
         const float f = rsqrtf(sum * (1.f / D) + eps);
         if (!has) return;
+        const float2 f2 = make_float2(f, f);
+        auto times = [&](float* v, const float* by) {
+            const float4 w4 = *reinterpret_cast<const float4*>(by);
+            const float2 lo = __fmul2_rn(__fmul2_rn(make_float2(v[0], v[1]), f2), make_float2(w4.x, w4.y));
+            const float2 hi = __fmul2_rn(__fmul2_rn(make_float2(v[2], v[3]), f2), make_float2(w4.z, w4.w));
+            v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
+        };
 #pragma unroll
         for (int j = 0; j < N; j += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(w + d0 + j);
-            const float4 b = *reinterpret_cast<const float4*>(w + d1 + j);
-            x[j] *= f * a.x, x[j + 1] *= f * a.y, x[j + 2] *= f * a.z, x[j + 3] *= f * a.w;
-            y[j] *= f * b.x, y[j + 1] *= f * b.y, y[j + 2] *= f * b.z, y[j + 3] *= f * b.w;
+            times(x + j, w + d0 + j);
+            times(y + j, w + d1 + j);
         }
     }
     // Norm weights into shared memory (the caller's barrier follows).
@@ -88,9 +95,12 @@ struct RowLanes {
     }
 };
 
-// The slot of token t, -1 where its K and V are left out; reported by `tell`.
-__device__ __forceinline__ long long append_slot(const AppendParams& p, long long t, bool tell) {
-    const long long s = p.slots[t];
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// A token's slot, -1 where its K and V are left out; reported by `tell`.
+__device__ __forceinline__ long long append_slot(const AppendParams& p, long long s, bool tell) {
     const bool bad = s < -1 || s >= p.num_slots;
     if (bad && tell && p.err) atomicOr(p.err, PA_DEVERR_BAD_SLOT);
     return bad ? -1 : s;
@@ -118,7 +128,7 @@ __device__ __forceinline__ void append_token(const AppendParams& p, long long t,
     const bool has_lane = c < Rw::kHave;
     const int d0 = Rw::first(c, p.R), d1 = Rw::second(c, p.R);
     const bool turn = c < p.R / (2 * N);
-    const long long slot = ALL ? append_slot(p, t, tid == 0) : -1;
+    const long long slot = ALL ? append_slot(p, p.slots[t], tid == 0) : -1;
     for (int i0 = 0; i0 < items; i0 += kAppendItems * nt) {
         uint4 a[kAppendItems], b[kAppendItems];
 #pragma unroll
@@ -184,27 +194,230 @@ __device__ __forceinline__ void append_token(const AppendParams& p, long long t,
 
 // A CTA for each token.
 template <int D, typename T>
-__global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendParams p) {
     __shared__ AppendShared<D> sh;
     allow_dependent_launch();
     wait_for_prerequisite_grid();
     append_token<D, T, true>(p, blockIdx.x, sh);
 }
 
+// ---- Many tokens: persistent CTAs whose groups of four warps each have a ring of tokens in
+// shared memory, filled by bulk copies.
+
+constexpr int kRingGroups = 3;     // groups of a CTA
+constexpr int kRingThreads = 128;  // threads of a group
+constexpr int kRingStages = 8;     // tokens of a group's ring, at most
+constexpr int kRingFill = 96 << 10;  // bytes of the CTA's rings, about
+// Bytes of rows from which the ring pays: in pa_append, and for the q rows of pa_q8_append,
+// where it is one more launch.
+constexpr long long kRingBytes = 12 << 20, kRingBytesQ8 = 48 << 20;
+
+// What turns a row's pairs, weights included: (x, y) becomes (x a + y b, y c + x d) times
+// the norm's factor.  Entry i is element i % N of lane i / N; four consecutive elements lie
+// side by side, those of the next lane behind them.
+template <int D>
+struct RingTable {
+    float a[D / 2], b[D / 2], c[D / 2], d[D / 2];
+};
+
+template <int D>
+struct RingShared {
+    alignas(16) RingTable<D> table[2][2];  // [token, alternating][q, k]
+    alignas(8) uint64_t full[kRingStages];
+    int dead[2];  // a copy timed out, seen at a token (alternating)
+};
+
+__device__ __forceinline__ void ring_barrier(int group) {
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(kRingThreads) : "memory");
+}
+
+// ALL: rows are q's, K's and V's, as in append_token; otherwise q's alone.
+template <int D, typename T, bool ALL>
+__global__ void __launch_bounds__(kRingGroups * kRingThreads, 1)
+    append_ring_kernel(const AppendParams p, const int stages, const int token_bytes) {
+    using Rw = RowLanes<D, T>;
+    using E = RopeElem<T>;
+    constexpr int N = Rw::N, ES = Rw::ES, L = Rw::kLanes, F = N / 2;
+    constexpr int kRows = kRingThreads / L;  // rows of a pass
+    extern __shared__ __align__(128) unsigned char ring_smem[];
+    __shared__ RingShared<D> shared[kRingGroups];
+    const int group = threadIdx.x / kRingThreads, tid = threadIdx.x % kRingThreads;
+    RingShared<D>& sh = shared[group];
+    unsigned char* ring = ring_smem + (size_t)group * stages * token_bytes;
+    const long long step = gridDim.x * kRingGroups, t0 = blockIdx.x * kRingGroups + group;
+    const uint32_t full = smem_u32(sh.full);
+    allow_dependent_launch();
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(full + 8 * i, 1);
+        fence_mbar_init();
+        sh.dead[0] = sh.dead[1] = 0;
+    }
+    __syncthreads();
+    // Entry tid of the tables: its pair's weights and frequency.
+    const bool has_pair = tid < D / 2;
+    const bool turns = tid < p.R / 2;
+    const unsigned long long freq = turns ? p.freq[tid] : 0;
+    const int at = (tid % N) / 4 * (D * 2 / N) + tid / N * 4 + tid % 4;  // (its place in a table)
+    wait_for_prerequisite_grid();
+    float w[2][2];  // [q, k][x, y]
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const unsigned char* wp = i == 0 ? p.q_norm : p.k_norm;
+        w[i][0] = w[i][1] = 1.f;
+        if (wp && has_pair) {
+            const int c = tid / N, j = tid % N;
+            w[i][0] = to_float(reinterpret_cast<const T*>(wp)[Rw::first(c, p.R) + j]);
+            w[i][1] = to_float(reinterpret_cast<const T*>(wp)[Rw::second(c, p.R) + j]);
+        }
+    }
+    const uint32_t q_bytes = p.Hq * D * ES, kv_bytes = ALL ? p.Hkv * D * ES : 0;
+    auto request = [&](long long t, int slot) {  // (one thread)
+        const uint32_t dst = smem_u32(ring + (size_t)slot * token_bytes), bar = full + 8 * slot;
+        mbar_arrive_expect_tx(bar, q_bytes + 2 * kv_bytes);
+        if (q_bytes) bulk_g2s(dst, p.q + t * p.q_stride, q_bytes, bar);
+        if (ALL) {
+            bulk_g2s(dst + q_bytes, p.k + t * p.k_stride, kv_bytes, bar);
+            bulk_g2s(dst + q_bytes + kv_bytes, p.v + t * p.v_stride, kv_bytes, bar);
+        }
+    };
+    if (tid == 0)
+        for (int i = 0; i < stages && t0 + i * step < p.n; ++i)
+            request(t0 + i * step, i);
+    const int n_rows = p.Hq + (ALL ? 2 * p.Hkv : 0);
+    const int c = tid % L, r0 = tid / L;
+    const bool has_lane = c < Rw::kHave, turn = c < p.R / (2 * N);
+    const int d0 = Rw::first(c, p.R) * ES, d1 = Rw::second(c, p.R) * ES;
+    int pos = 0;
+    long long row_slot = -1;
+    auto look = [&](long long t) {  // (a token ahead)
+        if (p.R > 0) pos = p.positions[t];
+        if (ALL) row_slot = p.slots[t];
+    };
+    if (t0 < p.n) look(t0);
+    int slot = 0, before = -1, k = 0;  // ring slot, the one of the token before, tokens so far
+    uint32_t phase = 0;
+    bool dead = false;
+    for (long long t = t0; t < p.n; t += step, ++k) {
+        float cs = 1.f, sn = 0.f;
+        if (turns) rope_angle(pos, freq, cs, sn);
+        if (has_pair) {
+#pragma unroll
+            for (int i = 0; i < (ALL ? 2 : 1); ++i) {
+                RingTable<D>& tb = sh.table[k & 1][i];
+                tb.a[at] = w[i][0] * cs, tb.b[at] = -w[i][1] * sn;
+                tb.c[at] = w[i][1] * cs, tb.d[at] = w[i][0] * sn;
+            }
+        }
+        const long long cell = ALL ? append_slot(p, row_slot, tid == 0) : -1;
+        if (t + step < p.n) look(t + step);
+        if (!mbar_wait_bounded(full + 8 * slot, phase)) sh.dead[k & 1] = 1;
+        ring_barrier(group);
+        if (sh.dead[k & 1]) {
+            dead = true;
+            break;
+        }
+        // (all are through with the token before: its slot takes the next one)
+        if (tid == 0 && before >= 0 && t + step * (stages - 1) < p.n)
+            request(t + step * (stages - 1), before);
+        const unsigned char* rows = ring + (size_t)slot * token_bytes;
+        float2 ta[F], tb[F], tc[F], td[F];
+        auto table = [&](int i) {
+            const RingTable<D>& s = sh.table[k & 1][i];
+#pragma unroll
+            for (int f = 0; f < F; f += 2) {
+                const int e = f / 2 * (D * 2 / N) + c * 4;
+                const float4 va = *reinterpret_cast<const float4*>(s.a + e);
+                const float4 vb = *reinterpret_cast<const float4*>(s.b + e);
+                const float4 vc = *reinterpret_cast<const float4*>(s.c + e);
+                const float4 vd = *reinterpret_cast<const float4*>(s.d + e);
+                ta[f] = make_float2(va.x, va.y), ta[f + 1] = make_float2(va.z, va.w);
+                tb[f] = make_float2(vb.x, vb.y), tb[f + 1] = make_float2(vb.z, vb.w);
+                tc[f] = make_float2(vc.x, vc.y), tc[f + 1] = make_float2(vc.z, vc.w);
+                td[f] = make_float2(vd.x, vd.y), td[f + 1] = make_float2(vd.z, vd.w);
+            }
+        };
+        int kind = -1;  // whose table the registers hold
+#pragma unroll 1
+        for (int h0 = 0; h0 < n_rows; h0 += kRows) {
+            const int h = h0 + r0;
+            const bool is_q = !ALL || h < p.Hq, is_v = ALL && h >= p.Hq + p.Hkv;
+            const bool has = has_lane && h < n_rows && (is_q || cell >= 0);
+            uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
+            if (has) {
+                ra = *reinterpret_cast<const uint4*>(rows + (size_t)h * (D * ES) + d0);
+                rb = *reinterpret_cast<const uint4*>(rows + (size_t)h * (D * ES) + d1);
+                const int want = is_q ? 0 : 1;
+                if (!is_v && kind != want) {
+                    table(want);
+                    kind = want;
+                }
+            }
+            float2 x[F], y[F];
+            E::load(ra, reinterpret_cast<float(&)[N]>(x));
+            E::load(rb, reinterpret_cast<float(&)[N]>(y));
+            float factor = 1.f;
+            if (p.q_norm || (ALL && p.k_norm)) {  // (the shuffles are for all rows of the warp)
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int f = 0; f < F; ++f) sum = __ffma2_rn(x[f], x[f], __ffma2_rn(y[f], y[f], sum));
+                float ss = sum.x + sum.y;
+#pragma unroll
+                for (int m = 1; m < L; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                if (is_q ? p.q_norm : p.k_norm) factor = rsqrtf(ss * (1.f / D) + p.eps);
+            }
+            if (!has) continue;
+            if (!is_v) {
+                const float2 f2 = make_float2(factor, factor);
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    const float2 xf = __fmul2_rn(x[f], f2), yf = __fmul2_rn(y[f], f2);
+                    x[f] = __fmul2_rn(xf, ta[f]);
+                    y[f] = __fmul2_rn(yf, tc[f]);
+                    if (turn) {
+                        x[f] = __ffma2_rn(yf, tb[f], x[f]);
+                        y[f] = __ffma2_rn(xf, td[f], y[f]);
+                    }
+                }
+                ra = E::store(reinterpret_cast<const float(&)[N]>(x));
+                rb = E::store(reinterpret_cast<const float(&)[N]>(y));
+            }
+            unsigned char* dst;
+            if (is_q) {
+                dst = p.q_out + t * p.q_out_stride + (size_t)h * (D * ES);
+            } else {
+                const size_t block = (size_t)(cell / kPageSize) * p.Hkv +
+                                     (is_v ? h - p.Hq - p.Hkv : h - p.Hq);
+                dst = (is_v ? p.v_cache : p.k_cache) +
+                      (block * kPageSize + (int)(cell % kPageSize)) * (size_t)(D * ES);
+            }
+            *reinterpret_cast<uint4*>(dst + d0) = ra;
+            *reinterpret_cast<uint4*>(dst + d1) = rb;
+        }
+        before = slot;
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    if (dead && tid == 0) {  // (copies on their way must not outlive the shared memory)
+        if (p.err) atomicOr(p.err, PA_DEVERR_TIMEOUT);
+        for (int i = 0; i < stages; ++i) mbar_wait_bounded(full + 8 * i, i < slot ? phase ^ 1 : phase);
+    }
+}
+
 // ---- The 8-bit cache.
 
-// Codes of N values times f (non-finite ones become NaN), first one lowest.
-template <int N>
-__device__ __forceinline__ void q8_codes(const float (&x)[N], float f, uint32_t (&c)[N / 4]) {
+// Codes of N values times f, first one lowest (NaN stays NaN, beyond 448: 448).
+template <int F>
+__device__ __forceinline__ void q8_codes(const float2 (&x)[F], float f, uint32_t (&c)[F / 2]) {
+    const float2 f2 = make_float2(f, f);
 #pragma unroll
-    for (int j = 0; j < N; j += 4) {
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = fabsf(x[j + i]) <= FLT_MAX ? x[j + i] * f : NAN;
-        uint16_t lo, hi;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1]), "f"(v[0]));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3]), "f"(v[2]));
-        c[j / 4] = (uint32_t)lo | ((uint32_t)hi << 16);
+    for (int j = 0; j < F; j += 2) {
+        const float2 a = __fmul2_rn(x[j], f2), b = __fmul2_rn(x[j + 1], f2);
+        asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
+            " cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}"
+            : "=r"(c[j / 2])
+            : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     }
 }
 
@@ -246,16 +459,18 @@ __device__ __forceinline__ void q8_store_codes(unsigned char* p, const uint32_t 
 }
 
 // The first kv_ctas CTAs go by (tile of rows, group of KV heads, K or V): in its tile a
-// CTA finds the rows that begin a run (rows at consecutive slots of a page), and for
-// each run and head every thread has its two pieces of one of the page's 16 rows: a
-// new one, one that was there, or none.  The largest magnitude goes through the CTA,
-// the scale follows, codes are stored.  The other CTAs serve a token's q each.
+// CTA finds the rows that begin a run (rows at consecutive slots of a page).  For each
+// run and head a thread has its two pieces of a new row, and of a row that was there
+// before, if there are so many.  The largest magnitude goes through the CTA, the scale
+// follows, codes are stored.  The rows of the tile come by bulk copies, asked for beside
+// the slots; those of a run that goes on behind the tile (it is the tile's last) take the
+// places of rows before it, which are done with.  The other CTAs serve a token's q each.
 template <int D, typename T>
 __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes), 64 / RowLanes<D, T>::kLanes)
     q8_append_kernel(const AppendParams p) {
     using Rw = RowLanes<D, T>;
     using E = RopeElem<T>;
-    constexpr int N = Rw::N, ES = Rw::ES, L = Rw::kLanes, W = N / 4;
+    constexpr int N = Rw::N, ES = Rw::ES, L = Rw::kLanes, W = N / 4, F = N / 2;
     constexpr int kWarpsHere = 16 * L / 32;
     __shared__ AppendShared<D> sh;
     __shared__ uint32_t s_max[2][kWarpsHere];
@@ -270,128 +485,177 @@ __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes), 64 / RowLanes<D
     const int is_v = blockIdx.x & 1, group = (blockIdx.x >> 1) % p.groups;
     const long long row0 = (long long)((blockIdx.x >> 1) / p.groups) * p.tile;
     const int h0 = group * p.heads, h1 = min(p.Hkv, h0 + p.heads);
+    const unsigned char* rows = is_v ? p.v : p.k;
+    const long long stride = is_v ? p.v_stride : p.k_stride;
+    unsigned char* cache = is_v ? p.v_cache : p.k_cache;
+    float* scales = is_v ? p.v_scales : p.k_scales;
+    const bool rotate = !is_v && p.R > 0, norm = !is_v && p.k_norm;
+    const int i_row = tid / L, c = tid % L;  // row of a run, and lane of the row
+    const bool have = c < Rw::kHave;
+    const int d0 = Rw::first(c, p.R), d1 = Rw::second(c, p.R);
+    const bool turn = rotate && c < p.R / (2 * N);
+    // Row i of the tile, heads h0 .. h1 - 1, at i modulo 16.
+    extern __shared__ __align__(128) unsigned char tile_smem[];
+    __shared__ __align__(8) uint64_t s_full;
+    const int row_bytes = (h1 - h0) * D * ES;
+    const uint32_t full = smem_u32(&s_full);
+    auto fetch = [&](int from, int to) {  // (warp 0)
+        if (lane == 0) mbar_arrive_expect_tx(full, (to - from) * row_bytes);
+        __syncwarp();
+        if (from + lane < to)
+            bulk_g2s(smem_u32(tile_smem) + (from + lane) % kPageSize * row_bytes,
+                     rows + (row0 + from + lane) * stride + (size_t)h0 * D * ES, row_bytes, full);
+    };
+    if (warp == 0) {
+        if (lane == 0) {
+            mbar_init(full, 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
+        fetch(0, (int)min((long long)p.tile, p.n - row0));
+    }
+    uint32_t phase = 0;
+    auto arrived = [&]() {  // (every thread; false: the wait ran out)
+        const bool late = !mbar_wait_bounded(full, phase);
+        if (late) {  // (a copy on its way must not outlive the shared memory)
+            if (p.err) atomicOr(p.err, PA_DEVERR_TIMEOUT);
+            mbar_wait_bounded(full, phase);
+        }
+        phase ^= 1;
+        return !__syncthreads_or(late);
+    };
+    const int first_pos = rotate && row0 + i_row < p.n ? p.positions[row0 + i_row] : 0;
     // Lane j looks at row row0 - 1 + j: runs begin at lanes 1 .. tile and have at most 16
     // rows.
     const long long at = row0 - 1 + lane;
     long long slot = -1;
     if (at >= 0 && at < p.n)
-        slot = append_slot(p, at, !is_v && group == 0 && warp == 0 && lane >= 1 && lane <= p.tile);
+        slot = append_slot(p, p.slots[at], !is_v && group == 0 && warp == 0 && lane >= 1 && lane <= p.tile);
+    if (norm) Rw::stage(p.k_norm, sh.w[1]);
+    if (rotate)
+        for (int i = tid; i < p.R / 2; i += blockDim.x) s_freq[i] = p.freq[i];
+    __syncthreads();  // (the barrier's initial state as well)
     const long long before = __shfl_up_sync(0xffffffffu, slot, 1);
     const bool goes_on = lane > 0 && slot >= 0 && before >= 0 && slot == before + 1 &&
                          slot % kPageSize != 0;
     const uint32_t on = __ballot_sync(0xffffffffu, goes_on);
     uint32_t leads = __ballot_sync(0xffffffffu, slot >= 0 && !goes_on && lane >= 1 && lane <= p.tile);
+    // Rows of the last run behind the tile; fetched at once where no other run is in the
+    // way, else when the others are done.
+    const int last = 31 - __clz(leads);
+    const int last_end = leads ? last - 1 + __ffs(~(last == 31 ? 0u : on >> (last + 1))) : 0;
+    bool behind = last_end > p.tile;
+    if (!arrived()) return;
     if (!leads) return;
-    const bool rotate = !is_v && p.R > 0, norm = !is_v && p.k_norm;
-    if (norm) Rw::stage(p.k_norm, sh.w[1]);
-    if (rotate)
-        for (int i = tid; i < p.R / 2; i += blockDim.x) s_freq[i] = p.freq[i];
-    if (norm || rotate) __syncthreads();
-    const unsigned char* src0 = is_v ? p.v : p.k;
-    const long long stride = is_v ? p.v_stride : p.k_stride;
-    unsigned char* cache = is_v ? p.v_cache : p.k_cache;
-    float* scales = is_v ? p.v_scales : p.k_scales;
-    const int r = tid / L, c = tid % L;
-    const int d0 = Rw::first(c, p.R), d1 = Rw::second(c, p.R);
-    const bool turn = rotate && c < p.R / (2 * N);
+    if (behind && (leads & (leads - 1)) == 0) {
+        if (warp == 0) fetch(p.tile, last_end);
+        if (!arrived()) return;
+        behind = false;
+    }
     int turn_of = 0;  // buffer of s_max
     for (; leads; leads &= leads - 1) {
         const int j = __ffs(leads) - 1;
         const uint32_t rest = j == 31 ? 0u : on >> (j + 1);
         const int cnt = __ffs(~rest);  // 1 + the rows that go on
-        const long long first = __shfl_sync(0xffffffffu, slot, j);
+        const long long first = __shfl_sync(0xffffffffu, slot, j), run = row0 - 1 + j;
+        if (behind && j == last) {
+            __syncthreads();  // (every thread has read the rows whose places these take)
+            if (warp == 0) fetch(p.tile, last_end);
+            if (!arrived()) return;
+        }
         const int r0 = (int)(first % kPageSize);
-        const size_t page = (size_t)(first / kPageSize);
-        const bool have = c < Rw::kHave;
-        const bool fresh = have && r >= r0 && r < r0 + cnt, kept = have && r < r0;
-        const long long row = row0 - 1 + j + (r - r0);
-        const unsigned char* src = src0 + row * stride + (size_t)h0 * D * ES;
-        const size_t block0 = page * p.Hkv + h0;
-        unsigned char* dst = cache + (block0 * kPageSize + r) * D;
-        float cs[N], sn[N];
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        uint32_t ca[W] = {}, cb[W] = {};
-        float old = 0.f;
-        auto request = [&](int h, uint4& a_, uint4& b_, uint32_t (&ca_)[W], uint32_t (&cb_)[W],
-                           float& old_) {
-            const size_t step = h - h0;
-            if (fresh) {
-                a_ = *reinterpret_cast<const uint4*>(src + step * D * ES + d0 * ES);
-                b_ = *reinterpret_cast<const uint4*>(src + step * D * ES + d1 * ES);
-            }
-            if (kept) {
-                q8_load_codes(ca_, dst + step * (kPageSize * D) + d0);
-                q8_load_codes(cb_, dst + step * (kPageSize * D) + d1);
-            }
-            if (r0 > 0) old_ = scales[block0 + step];
-        };
-        request(h0, a, b, ca, cb, old);
+        const bool fresh = have && i_row < cnt, kept = have && i_row < r0;
+        const size_t block0 = (size_t)(first / kPageSize) * p.Hkv;
+        const unsigned char* src = tile_smem + (j - 1 + i_row) % kPageSize * row_bytes;
+        float2 cs[F], sn[F];
         if (turn && fresh) {
-            const int pos = p.positions[row];
+            const int pos = j == 1 ? first_pos : p.positions[run + i_row];
 #pragma unroll
-            for (int i = 0; i < N; ++i) rope_angle(pos, s_freq[c * N + i], cs[i], sn[i]);
+            for (int i = 0; i < F; ++i) {
+                rope_angle(pos, s_freq[c * N + 2 * i], cs[i].x, sn[i].x);
+                rope_angle(pos, s_freq[c * N + 2 * i + 1], cs[i].y, sn[i].y);
+            }
         }
         for (int h = h0; h < h1; ++h) {
-            uint4 an = a, bn = b;
-            uint32_t can[W] = {}, cbn[W] = {};
-            float old_n = 0.f;
-            if (h + 1 < h1) request(h + 1, an, bn, can, cbn, old_n);
-            float x[N], y[N];
-            E::load(a, x);
-            E::load(b, y);
-            if (norm) Rw::normalise(x, y, sh.w[1], d0, d1, fresh, p.eps);
+            unsigned char* page = cache + (block0 + h) * (size_t)(kPageSize * D);
+            uint32_t ka[W] = {}, kb[W] = {};
+            if (kept) {  // (asked for now, wanted if the scale rises)
+                q8_load_codes(ka, page + i_row * D + d0);
+                q8_load_codes(kb, page + i_row * D + d1);
+            }
+            const float was = r0 > 0 ? scales[block0 + h] : 0.f;
+            uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+            if (fresh) {
+                xa = *reinterpret_cast<const uint4*>(src + (h - h0) * (D * ES) + d0 * ES);
+                xb = *reinterpret_cast<const uint4*>(src + (h - h0) * (D * ES) + d1 * ES);
+            }
+            float2 x[F], y[F];
+            float(&xs)[N] = reinterpret_cast<float(&)[N]>(x);
+            float(&ys)[N] = reinterpret_cast<float(&)[N]>(y);
+            E::load(xa, xs);
+            E::load(xb, ys);
+            if (norm) Rw::normalise(xs, ys, sh.w[1], d0, d1, fresh, p.eps);
             if (turn && fresh) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float xr = fmaf(x[i], cs[i], -(y[i] * sn[i]));
-                    y[i] = fmaf(y[i], cs[i], x[i] * sn[i]);
+                for (int i = 0; i < F; ++i) {
+                    const float2 minus = make_float2(-sn[i].x, -sn[i].y);
+                    const float2 xr = __ffma2_rn(x[i], cs[i], __fmul2_rn(y[i], minus));
+                    y[i] = __ffma2_rn(y[i], cs[i], __fmul2_rn(x[i], sn[i]));
                     x[i] = xr;
                 }
             }
-            float most = 0.f;
+            auto largest = [&]() {  // (NaN does not count)
+                float most = 0.f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float ax = fabsf(x[i]), ay = fabsf(y[i]);
-                most = fmaxf(most, fmaxf(ax <= FLT_MAX ? ax : 0.f, ay <= FLT_MAX ? ay : 0.f));
+                for (int i = 0; i < F; ++i)
+                    most = fmaxf(fmaxf(most, fmaxf(fabsf(x[i].x), fabsf(x[i].y))),
+                                 fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
+                // over the CTA, as bits: numbers from 0 on are in the order of their bits
+                uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(fresh ? most : 0.f));
+                if (lane == 0) s_max[turn_of][warp] = all;
+                __syncthreads();
+                all = __reduce_max_sync(0xffffffffu, s_max[turn_of][lane % kWarpsHere]);
+                turn_of ^= 1;
+                return all;
+            };
+            uint32_t all = largest();
+            if (all == 0x7F800000u) {  // an infinity somewhere: NaN in its place, and again
+#pragma unroll
+                for (int i = 0; i < F; ++i) {
+                    if (fabsf(x[i].x) > FLT_MAX) x[i].x = NAN;
+                    if (fabsf(x[i].y) > FLT_MAX) x[i].y = NAN;
+                    if (fabsf(y[i].x) > FLT_MAX) y[i].x = NAN;
+                    if (fabsf(y[i].y) > FLT_MAX) y[i].y = NAN;
+                }
+                all = largest();
             }
-            if (!fresh) most = 0.f;
-            const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
-            if (lane == 0) s_max[turn_of][warp] = wmax;
-            __syncthreads();
-            uint32_t all = 0;
-#pragma unroll
-            for (int i = 0; i < kWarpsHere; ++i) all = max(all, s_max[turn_of][i]);
-            turn_of ^= 1;
-            if (!(old > 0.f && old <= FLT_MAX)) old = 0.f;
+            const float old = was > 0.f && was <= FLT_MAX ? was : 0.f;
             const float scale = fmaxf(old, q8_scale_for(__uint_as_float(all)));
-            const size_t step = h - h0;
-            unsigned char* to = dst + step * (kPageSize * D);
             if (fresh) {
-                const float inv = 1.f / scale;
+                const float inv = __frcp_rn(scale);
+                uint32_t ca[W], cb[W];
                 q8_codes(x, inv, ca);
                 q8_codes(y, inv, cb);
-            } else if (kept && scale != old) {
-                const float ratio = old / scale;
+                q8_store_codes(page + (r0 + i_row) * D + d0, ca);
+                q8_store_codes(page + (r0 + i_row) * D + d1, cb);
+            }
+            if (kept && scale != old) {
+                const float ratio = __fdiv_rn(old, scale);
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
-                    float v[4];
+                    float2 v[2];
                     uint32_t one[1];
-                    q8_values(ca[i], v);
+                    q8_values(ka[i], reinterpret_cast<float(&)[4]>(v));
                     q8_codes(v, ratio, one);
-                    ca[i] = one[0];
-                    q8_values(cb[i], v);
+                    ka[i] = one[0];
+                    q8_values(kb[i], reinterpret_cast<float(&)[4]>(v));
                     q8_codes(v, ratio, one);
-                    cb[i] = one[0];
+                    kb[i] = one[0];
                 }
+                q8_store_codes(page + i_row * D + d0, ka);
+                q8_store_codes(page + i_row * D + d1, kb);
             }
-            if (fresh || (kept && scale != old)) {
-                q8_store_codes(to + d0, ca);
-                q8_store_codes(to + d1, cb);
-            }
-            if (tid == 0 && scale != old) scales[block0 + step] = scale;
-            a = an, b = bn, old = old_n;
-#pragma unroll
-            for (int i = 0; i < W; ++i) ca[i] = can[i], cb[i] = cbn[i];
+            if (tid == 0 && scale != old) scales[block0 + h] = scale;
         }
     }
 }
@@ -474,33 +738,88 @@ __global__ void __launch_bounds__(kReadThreads) q8_read_kernel(const Q8ReadParam
 
 // ---- Launches and checks.
 
-template <typename... A>
-static cudaError_t launch_step(void (*kernel)(A...), dim3 grid, int threads, cudaStream_t stream,
-                               const A&... args) {
+template <typename... A, typename... B>
+static cudaError_t launch_step_smem(void (*kernel)(A...), dim3 grid, int threads, int smem,
+                                    cudaStream_t stream, const B&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    return cudaLaunchKernelEx(&cfg, kernel, A(args)...);
+}
+
+template <typename... A>
+static cudaError_t launch_step(void (*kernel)(A...), dim3 grid, int threads, cudaStream_t stream,
+                               const A&... args) {
+    return launch_step_smem(kernel, grid, threads, 0, stream, args...);
+}
+
+// Tokens a group of the ring kernel holds in rows of `heads` heads; 0: not two.
+template <int D, typename T>
+static int ring_stages(int heads) {
+    const long long token = (long long)heads * D * (int)sizeof(T);
+    const long long room = 227 * 1024 - (long long)sizeof(RingShared<D>) * kRingGroups - 256;
+    if (heads == 0 || room < 2 * token * kRingGroups) return 0;
+    const long long want = (kRingFill + token * kRingGroups / 2) / (token * kRingGroups);
+    return (int)std::max(2ll, std::min<long long>({want, room / (token * kRingGroups), kRingStages}));
+}
+
+template <int D, typename T, bool ALL>
+static cudaError_t launch_ring(const AppendParams& p, cudaStream_t stream) {
+    const int heads = p.Hq + (ALL ? 2 * p.Hkv : 0), stages = ring_stages<D, T>(heads);
+    const int token = heads * D * (int)sizeof(T), smem = stages * token * kRingGroups;
+    // The kernel's shared-memory limit, raised once per device, and the device's SMs.
+    static std::atomic<int> sms[64];
+    int dev = 0, n = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) n = sms[dev].load();
+    if (n == 0) {
+        e = cudaFuncSetAttribute(append_ring_kernel<D, T, ALL>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 227 * 1024 - (int)sizeof(RingShared<D>) * kRingGroups - 256);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) sms[dev].store(n);
+    }
+    const int ctas = std::min(n, (p.n + kRingGroups - 1) / kRingGroups);
+    return launch_step_smem(append_ring_kernel<D, T, ALL>, dim3(ctas), kRingGroups * kRingThreads,
+                            smem, stream, p, stages, token);
 }
 
 template <int D, typename T>
 static cudaError_t launch_append(const AppendParams& p, bool q8, cudaStream_t stream) {
     constexpr int L = RowLanes<D, T>::kLanes;
+    const int heads = p.Hq + (q8 ? 0 : 2 * p.Hkv);
+    const bool ring = (long long)p.n * heads * D * (int)sizeof(T) >= (q8 ? kRingBytesQ8 : kRingBytes) &&
+                      ring_stages<D, T>(heads) > 0;
     if (!q8) {
+        if (ring) return launch_ring<D, T, true>(p, stream);
         // Threads for kAppendItems items each.
-        const int items = (p.Hq + 2 * p.Hkv) * L;
-        const int threads = (items + kAppendItems * 32 - 1) / (kAppendItems * 32) * 32;
+        const int threads = (heads * L + kAppendItems * 32 - 1) / (kAppendItems * 32) * 32;
         return launch_step(append_kernel<D, T>, dim3(p.n), std::min(kAppendThreads, threads),
                            stream, p);
     }
-    return launch_step(q8_append_kernel<D, T>, dim3(p.kv_ctas + (p.Hq > 0 ? p.n : 0)), 16 * L,
-                       stream, p);
+    // (a tile's rows: at most kMaxTileBytes, see append_call)
+    static std::atomic<unsigned long long> raised{0};  // the shared-memory limit, by device
+    const int smem = kPageSize * p.heads * D * (int)sizeof(T);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !(raised.load() >> dev & 1))) {
+        e = cudaFuncSetAttribute(q8_append_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kMaxTileBytes);
+        if (e == cudaSuccess && dev < 64) raised.fetch_or(1ull << dev);
+    }
+    if (e != cudaSuccess) return e;
+    e = launch_step_smem(q8_append_kernel<D, T>, dim3(p.kv_ctas + (heads > 0 && !ring ? p.n : 0)),
+                         16 * L, smem, stream, p);
+    return e == cudaSuccess && ring ? launch_ring<D, T, false>(p, stream) : e;
 }
 
 template <typename T>
@@ -617,6 +936,7 @@ static int append_call(bool q8, int num_tokens, int num_q_heads, int num_kv_head
         const long long tiles = p.tile == 16 ? tiles16 : num_tokens;
         p.heads = (int)std::max(1ll, std::min<long long>(num_kv_heads,
                                                          tiles * 2 * num_kv_heads / kAppendCtas));
+        p.heads = std::min(p.heads, kMaxTileBytes / (kPageSize * head_dim * es));
         p.groups = (num_kv_heads + p.heads - 1) / p.heads;
         const long long ctas = tiles * 2 * p.groups;
         if (ctas + num_tokens > 0x7fffffffll) return PA_ERR_UNSUPPORTED;

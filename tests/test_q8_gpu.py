@@ -142,6 +142,81 @@ def test_append_shapes_in_place(n, hq, hkv, dtype):
     np.testing.assert_array_equal(host(r.tv), r.v)
 
 
+@pytest.mark.parametrize("n", [2048, 2700, 5001])
+@pytest.mark.parametrize("D,rot,dtype,hq,hkv", [(64, 32, "f32", 3, 1), (96, 96, "bf16", 4, 2), (128, 128, "f16", 5, 1),
+                                                (256, 64, "bf16", 2, 1), (128, 128, "f32", 40, 8), (256, 256, "f32", 64, 1),
+                                                (64, 64, "f16", 0, 3)])
+def test_append_many_tokens(n, D, rot, dtype, hq, hkv):
+    """Prompts of so many tokens that CTAs go through several; rows too wide for a ring of them."""
+    if n != 2700 and hq >= 40:
+        pytest.skip("one length is enough")
+    r = Rows(n + D, n, hq, hkv, D, dtype, True, 1e4, rot)
+    pages = n // 16 + 3
+    slots = page_slots(r.g, n, pages, 5)
+    slots[r.g.random(n) < 0.1] = -1
+    q_out = torch.full((n, hq, D), float("nan"), dtype=T[dtype], device="cuda") if hq else None
+    kw = dict(r.kw)
+    if not hq:
+        kw["q_norm"] = None
+    k, tol = r.want(r.k, 1, dtype)
+    kept = slots >= 0
+    kc, vc = (torch.full((pages, hkv, 16, D), 7.0, dtype=T[dtype], device="cuda") for _ in range(2))
+    for place in ("out", "in place"):
+        pa.pa_append(r.tq if hq else None, r.tk, r.tv, i64(slots), i32(r.pos), kc, vc,
+                     q_out=q_out if place == "out" else None, **kw)
+        if hq:
+            r.check_q(q_out if place == "out" else r.tq)
+        got_k, got_v = host(kc), host(vc)
+        s = slots[kept]
+        assert (np.abs(got_k[s // 16, :, s % 16] - k[kept]) <= tol[kept]).all()
+        np.testing.assert_array_equal(got_v[s // 16, :, s % 16], r.v[kept])
+        rest = np.ones((pages, 16), bool)
+        rest[s // 16, s % 16] = False
+        assert (got_k.transpose(0, 2, 1, 3)[rest] == 7).all() and (got_v.transpose(0, 2, 1, 3)[rest] == 7).all()
+
+
+@pytest.mark.parametrize("norms", ["both", "q", "k", "none"])
+@pytest.mark.parametrize("n", [40, 2100])
+def test_append_with_either_norm(norms, n):
+    D, hq, hkv = 128, 4, 2
+    r = Rows(n, n, hq, hkv, D, "f16", True, 1e4, 64)
+    for i, name in enumerate("qk"):
+        if norms not in ("both", name):
+            r.w[i] = r.kw[name + "_norm"] = None
+    slots = np.arange(n)
+    pages = n // 16 + 1
+    kc, vc = (torch.zeros(pages, hkv, 16, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    q_out = torch.empty(n, hq, D, dtype=torch.float16, device="cuda")
+    pa.pa_append(r.tq, r.tk, r.tv, i64(slots), i32(r.pos), kc, vc, q_out=q_out, **r.kw)
+    r.check_q(q_out)
+    k, tol = r.want(r.k, 1, "f16")
+    assert (np.abs(host(kc).transpose(0, 2, 1, 3).reshape(-1, hkv, D)[:n] - k) <= tol).all()
+    caches = pa.new_q8_cache(pages, hkv, D)
+    q2 = torch.empty_like(q_out)
+    run_q8_append(r, slots, caches, q2)
+    r.check_q(q2)
+    check_q8(r, slots, caches, zero_cache(pages, hkv, D), zero_cache(pages, hkv, D), exact_k=False)
+
+
+def zero_cache(pages, H, D):
+    c = ref.Cache(pages, H, D)
+    c.codes[...] = 0
+    return c
+
+
+def test_append_keeps_infinities_behind_the_rotated_dims_apart():
+    # dims behind rotary_dim are not mixed: an infinity there stays in its place
+    for n in (3, 2048):
+        r = Rows(n, n, 2, 1, 64, "f32", False, 1e4, 32)
+        r.tq[:, :, 40] = float("inf")
+        kc, vc = (torch.zeros(n // 16 + 1, 1, 16, 64, device="cuda") for _ in range(2))
+        q_out = torch.empty(n, 2, 64, device="cuda")
+        pa.pa_append(r.tq, r.tk, r.tv, i64(np.arange(n)), i32(r.pos), kc, vc, q_out=q_out, **r.kw)
+        got = host(q_out)
+        assert np.isinf(got[..., 40]).all() and np.isfinite(np.delete(got, 40, -1)).all()
+        np.testing.assert_array_equal(np.delete(got[..., 32:], 8, -1), np.delete(r.q[..., 32:], 8, -1))
+
+
 def test_append_far_positions():
     r = Rows(5, 200, 2, 1, 64, "f32", False, 1e4, 64, far=True)
     r.pos[:3] = [2 ** 31 - 1, -2 ** 31, -1]
