@@ -23,6 +23,10 @@ namespace pa {
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyCluster = 8;    // CTAs of a sequence, at most
+// CTAs of 152 SMs at four each.  Up to so many have four 16-byte loads of a row in flight a
+// lane; more of them two, and run seven at a time on an SM (128 sequences of 131072: 28.5
+// and 26.7 us, 64: 16.0 and 16.4).
+constexpr int kVerifyWave = 608;
 constexpr int kVerifyMaxVocab = 1 << 19;  // (sums of 2^19 weights of 1 fit 64 bits)
 
 struct VerifyParams {
@@ -86,7 +90,7 @@ __device__ __forceinline__ unsigned long long verify_warp_sum(unsigned long long
 
 // Rows of weights: p, less q where there is one, and none at `hole`.  (Saturating
 // limits a number to [0, 1], NaN to 0.)
-template <typename T>
+template <typename T, int LOADS>
 struct VerifyRow {
     const T* p;
     const T* q;  // null: p itself
@@ -103,7 +107,7 @@ struct VerifyRow {
     __device__ __forceinline__ unsigned long long sum(int lo, int hi, int lane, bool vec) const {
         VerifySum s;
         int n = 0;
-        constexpr int N = 16 / sizeof(T), U = sizeof(T) == 4 ? 4 : 2;
+        constexpr int N = 16 / sizeof(T), U = LOADS;
         int i = lo;
         if (vec) {  // (lo is a multiple of 8)
             for (; i + 32 * N * U <= hi; i += 32 * N * U) {
@@ -163,8 +167,8 @@ struct VerifyRow {
     }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const VerifyParams p) {
+template <typename T, int LOADS>
+__global__ void __launch_bounds__(kVerifyThreads, (LOADS > 2 ? 4 : 7)) verify_kernel(const VerifyParams p) {
     __shared__ int s_stop[2];                                // j, and the draft there
     __shared__ unsigned long long s_warp[kVerifyWarps];      // sums of the warps' stretches
     __shared__ unsigned long long s_cta[2][kVerifyCluster];  // of the cluster's CTAs (by pass)
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const VerifyP
     }
     __syncthreads();
     const int j = s_stop[0];
-    VerifyRow<T> row;
+    VerifyRow<T, LOADS> row;
     row.p = target + (size_t)j * p.V;
     row.q = j < n && draft ? draft + (size_t)j * p.V : nullptr;
     row.hole = j < n && !draft ? s_stop[1] : -1;
@@ -313,7 +317,8 @@ static cudaError_t launch_verify(const VerifyParams& p, int batch, cudaStream_t 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, verify_kernel<T>, p);
+    return batch * p.cluster <= kVerifyWave ? cudaLaunchKernelEx(&cfg, verify_kernel<T, 4>, p)
+                                            : cudaLaunchKernelEx(&cfg, verify_kernel<T, 2>, p);
 }
 
 }  // namespace pa
@@ -357,9 +362,14 @@ extern "C" int pa_verify_drafts(int batch, int max_drafts, int vocab, int dtype,
     p.V = vocab;
     p.vec = (long long)vocab * es % 16 == 0 &&
             (((uintptr_t)target_probs | (uintptr_t)draft_probs) & 15u) == 0;
-    // CTAs of a sequence: with 2048 elements each at least.
+    // CTAs of a sequence: with 2048 elements each at least, and no more than leave one wave
+    // of CTAs where they have 16384 at most (128 sequences of 32003: by 8 CTAs each 13.7
+    // us, by 4 9.8; of 131072: 28.5 and 30.0).
     p.cluster = 1;
     while (p.cluster < kVerifyCluster && vocab >= p.cluster * 2 * 2048) p.cluster *= 2;
+    while (p.cluster > 1 && (long long)batch * p.cluster > kVerifyWave &&
+           vocab <= p.cluster / 2 * 16384)
+        p.cluster /= 2;
     const int parts = p.cluster * kVerifyWarps;
     p.stretch = ((vocab + parts - 1) / parts + 7) / 8 * 8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
