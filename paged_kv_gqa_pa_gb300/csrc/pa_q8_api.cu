@@ -18,8 +18,13 @@ constexpr int kQ8MaxBatch = 4096;
 constexpr int kQ8MaxQuery = 16;     // query tokens of a sequence
 constexpr int kQ8MinRun = 2;        // pages of a warp, at least
 constexpr int kQ8MaxCluster = 8;    // (the largest that every launch may have)
-constexpr int kQ8ClusterExtra = 12;  // pages of head_dim 128, see pa_q8_plan
-constexpr int kQ8KernelRows = 4;    // partials per sequence beyond which a kernel merges
+// Pages of head_dim 128, see pa_q8_plan (16 sequences of 4096 tokens' window, five queries: 4
+// pages 44.4 us, 12 41.1; with 24, 12 of 10000 tokens each go 48.0 -> 43.8, but 12 of up to
+// 10000 25.7 -> 35.4).
+constexpr int kQ8ClusterExtra = 12;
+// Partials per sequence beyond which a kernel merges (20 sequences of 6000 tokens: 2 50.4 us, 4
+// 45.3; 6 of 20000: 4 46.1, 12 47.5).
+constexpr int kQ8KernelRows = 4;
 
 static bool q8_head_dim_ok(int D) { return D == 64 || D == 96 || D == 128 || D == 256; }
 

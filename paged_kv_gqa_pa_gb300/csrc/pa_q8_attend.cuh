@@ -25,11 +25,17 @@ namespace pa {
 
 #define PA_INLINE_LAMBDA __attribute__((always_inline))
 
-// Pages up to which a sequence goes to one CTA where there is one for each.
+// Pages up to which a plan gives each sequence one CTA, if so many run at once, and no
+// cluster (48 sequences of 24 pages 10.0 us, in ranges 15.1; beyond, see kQ8Whole).
 constexpr int q8_short(int D) { return D == 256 ? 16 : 24; }
 // What a sequence's start and end cost a CTA, in pages: equal ranges are equal
 // in this cost, not in pages.
 constexpr int kQ8Start = 12;
+// Where there is a CTA for each sequence, each has one unless the longest has so many pages
+// more than an equal range costs: that many are as long as cutting and joining.  (48 of 57
+// CTAs a head, head_dim 128, sequences of 560 tokens 18.4 -> 13.1 us, of 2000 39.2 -> 35.2; with
+// 48 pages instead, 30 of up to 1000 tokens 13.1 -> 16.2.)
+constexpr int kQ8Whole = 24;
 // The running maximum (log2 domain) before any score: below every score that
 // counts, and finite, so that a score of -inf is further below it.
 constexpr float kQ8NoMax = -3e38f;
@@ -500,7 +506,10 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         s0 = p.starts ? __ldcg(p.starts + b) : b;
         s1 = p.starts ? __ldcg(p.starts + b + 1) : b + 1;
     };
-    // Returns whether a sequence is longer than q8_short pages.  (one: B <= kThreads,
+    auto range_of = [&](int pages, int sequences) {
+        return max(kWarps, (pages + kQ8Start * sequences + p.X - 1) / p.X);
+    };
+    // Returns whether a sequence is too long for a CTA of its own.  (one: B <= kThreads,
     // and len, s0, s1 are sequence tid's)
     auto scan = [&](bool one, int len, int s0, int s1) {
         const int per = one ? 1 : (p.B + kThreads - 1) / kThreads;
@@ -526,7 +535,13 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         }
         if (lane == 31) s_scan[warp] = inc;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) inc += s_scan[w];
+        long long all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) inc += s_scan[w];
+            all += s_scan[w];
+        }
+        const int whole = range_of((int)all, (int)(all >> 32)) + kQ8Whole;
         int at = (int)(inc - sum), rank = (int)((inc - sum) >> 32);
         for (int b = b0; b < b1; ++b) {
             const int n = s_base[b];
@@ -540,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             s_base[p.B] = (int)inc;
             s_rank[p.B] = (int)(inc >> 32);
         }
-        return __syncthreads_or(longest > q8_short(D)) != 0;
+        return __syncthreads_or(longest > whole) != 0;
     };
     // Sequence of page f: the last b with s_base[b] <= f (behind any empty ones
     // that share that number).
@@ -592,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             return;
         }
         const int cost = total + kQ8Start * s_rank[p.B];
-        range = max(kWarps, (cost + p.X - 1) / p.X);
+        range = range_of(total, s_rank[p.B]);
         from = (int)min((long long)cost, (long long)blockIdx.x * range);
         lo = page_at(from);
         hi = page_at((long long)from + range);

@@ -320,7 +320,9 @@ def q8_decode(q, starts, k_cache, v_cache, k_scales, v_scales, block_tables, con
         if stream is not None:  # what is allocated here is filled on the current stream
             torch.cuda.ExternalStream(st, device=dev).synchronize()
         if max_query_len is None:
-            max_query_len = 1 if starts is None else max(1, int((starts[1:] - starts[:-1]).max()))
+            max_query_len = 1
+            if starts is not None and B > 0:
+                max_query_len = max(1, int((starts[1:] - starts[:-1]).max()))
         plan = pa_q8_plan(B, Hq, hkv, D, PAGE_SIZE, pages, maxp, max_context_len, window,
                           max_query_len, 0, _DTYPE[q.dtype])
         out = torch.zeros((n, Hq, D), dtype=q.dtype, device=q.device)

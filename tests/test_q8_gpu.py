@@ -633,6 +633,15 @@ def test_decode_ranges_cut_anywhere(ctas, D, dtype, queries):
         d.case(ctas=ctas)
 
 
+@pytest.mark.parametrize("longest", [30, 60, 62, 63, 64, 65, 66, 67, 68, 90])
+@pytest.mark.parametrize("queries,window", [(1, 0), (3, 700)])
+def test_decode_sequences_with_a_cta_each(longest, queries, window):
+    # Seven CTAs for six sequences: one each, or, from a longest sequence of about 65 pages
+    # on, equal ranges.
+    lens = [30 * 16, 29 * 16 + 1, 30 * 16, 0, 30 * 16 - 5, 16 * longest]
+    Decode(longest, lens, 4, 1, 64, "f16", T=queries).case(window=window, ctas=7)
+
+
 def test_decode_long_ranges_are_staged_in_stretches():
     # One CTA serves 2600 pages, more than it stages at a time, with sequences that end at,
     # before and behind the borders of the stretches.
@@ -977,6 +986,14 @@ def test_decode_offsets_beyond_32_bits():
     pa.pa_q8_decode(plan, tq, i32(d.starts), cache[0].view(F8), cache[1].view(F8), *scales, i32(ids[None]),
                     i32(d.lens), 0.1, 0, out, lse, ws)
     d.check((host(out), host(lse), pa.pa_get_error(ws)), want)
+
+
+def test_convenience_call_without_sequences():
+    d = Decode(40, [20], 2, 1, 64, "f16")
+    q = torch.empty(0, 2, 64, dtype=torch.float16, device="cuda")
+    for starts in (None, i32(np.zeros(1, np.int32))):
+        out, lse, plan, err = pa.q8_decode(q, starts, *d.device(), i32(d.bt[:0]), i32(d.lens[:0]), 0.1)
+        assert out.shape == (0, 2, 64) and lse.shape == (0, 2) and plan.batch == 0 and err == 0
 
 
 def test_convenience_call():
