@@ -19,7 +19,6 @@
 namespace pa {
 
 constexpr int kAppendThreads = 256;  // at most, of pa_append
-constexpr int kAppendItems = 2;      // items a thread requests before it waits for the angles
 constexpr int kMaxTileBytes = 48 << 10;  // of rows that a CTA holds at a time
 constexpr int kAppendCtas = 608;     // CTAs that fill the GPU: four for each of 152 SMs
 
@@ -106,33 +105,36 @@ __device__ __forceinline__ long long append_slot(const AppendParams& p, long lon
     return bad ? -1 : s;
 }
 
-// What a CTA of a token has in shared memory.
-template <int D>
+// What a CTA of TOKENS tokens has in shared memory.
+template <int D, int TOKENS>
 struct AppendShared {
-    alignas(16) float cos[kMaxRopePairs];
-    alignas(16) float sin[kMaxRopePairs];
+    alignas(16) float cos[TOKENS][D / 2];
+    alignas(16) float sin[TOKENS][D / 2];
     alignas(16) float w[2][D];  // norm weights of q and k
 };
 
-// The q heads of token t, or all its heads (ALL: q's, K's, then V's, into the cache too).
-template <int D, typename T, bool ALL>
-__device__ __forceinline__ void append_token(const AppendParams& p, long long t,
-                                             AppendShared<D>& sh) {
+// The q heads of token t, or all its heads (ALL: q's, K's, then V's, into the cache too), by
+// nt threads, ITEMS of whose items are requested before the wait for the angles; of the CTA's
+// tokens this one has number `part`.
+template <int D, typename T, bool ALL, int ITEMS, int TOKENS>
+__device__ __forceinline__ void append_token(const AppendParams& p, long long t, int part, int tid,
+                                             int nt, AppendShared<D, TOKENS>& sh) {
     using Rw = RowLanes<D, T>;
     using E = RopeElem<T>;
     constexpr int N = Rw::N, ES = Rw::ES, L = Rw::kLanes;
-    const int tid = threadIdx.x, nt = blockDim.x;
-    const int n_rows = p.Hq + (ALL ? 2 * p.Hkv : 0);
-    const int items = n_rows * L;
-    const int c = tid % L;  // (blockDim is a multiple of 32)
+    const bool real = TOKENS == 1 || t < p.n;  // (behind the last token: only the barrier)
+    if (!real) t = 0;
+    const int all_rows = p.Hq + (ALL ? 2 * p.Hkv : 0), n_rows = real ? all_rows : 0;
+    const int items = all_rows * L;
+    const int c = tid % L;  // (nt is a multiple of 32)
     const bool has_lane = c < Rw::kHave;
     const int d0 = Rw::first(c, p.R), d1 = Rw::second(c, p.R);
     const bool turn = c < p.R / (2 * N);
-    const long long slot = ALL ? append_slot(p, p.slots[t], tid == 0) : -1;
-    for (int i0 = 0; i0 < items; i0 += kAppendItems * nt) {
-        uint4 a[kAppendItems], b[kAppendItems];
+    const long long slot = ALL ? append_slot(p, p.slots[t], real && tid == 0) : -1;
+    for (int i0 = 0; i0 < items; i0 += ITEMS * nt) {
+        uint4 a[ITEMS], b[ITEMS];
 #pragma unroll
-        for (int u = 0; u < kAppendItems; ++u) {
+        for (int u = 0; u < ITEMS; ++u) {
             const int h = (i0 + u * nt + tid) / L;
             a[u] = b[u] = make_uint4(0, 0, 0, 0);
             if (has_lane && h < n_rows) {  // (rows that are left out too: nobody waits for the slot)
@@ -151,12 +153,12 @@ __device__ __forceinline__ void append_token(const AppendParams& p, long long t,
             if (p.R > 0) {
                 const int pos = p.positions[t];
                 for (int i = tid; i < p.R / 2; i += nt)
-                    rope_angle(pos, p.freq[i], sh.cos[i], sh.sin[i]);
+                    rope_angle(pos, p.freq[i], sh.cos[part][i], sh.sin[part][i]);
             }
             __syncthreads();
         }
 #pragma unroll
-        for (int u = 0; u < kAppendItems; ++u) {
+        for (int u = 0; u < ITEMS; ++u) {
             const int h = (i0 + u * nt + tid) / L;
             const bool is_q = !ALL || h < p.Hq, is_v = ALL && h >= p.Hq + p.Hkv;
             const bool has = has_lane && h < n_rows && (is_q || slot >= 0);
@@ -171,7 +173,7 @@ __device__ __forceinline__ void append_token(const AppendParams& p, long long t,
             if (turn && !is_v) {
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const float cs = sh.cos[c * N + j], sn = sh.sin[c * N + j];
+                    const float cs = sh.cos[part][c * N + j], sn = sh.sin[part][c * N + j];
                     const float xr = fmaf(x[j], cs, -(y[j] * sn));
                     y[j] = fmaf(y[j], cs, x[j] * sn);
                     x[j] = xr;
@@ -192,13 +194,19 @@ __device__ __forceinline__ void append_token(const AppendParams& p, long long t,
     }
 }
 
-// A CTA for each token.
-template <int D, typename T>
-__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendParams p) {
-    __shared__ AppendShared<D> sh;
+// TOKENS tokens a CTA, nt threads for each.
+template <int D, typename T, int ITEMS, int TOKENS>
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendParams p, const int nt) {
+    __shared__ AppendShared<D, TOKENS> sh;
     allow_dependent_launch();
     wait_for_prerequisite_grid();
-    append_token<D, T, true>(p, blockIdx.x, sh);
+    if (TOKENS == 1) {
+        append_token<D, T, true, ITEMS>(p, blockIdx.x, 0, threadIdx.x, blockDim.x, sh);
+    } else {
+        const int part = threadIdx.x / nt;
+        append_token<D, T, true, ITEMS>(p, (long long)blockIdx.x * TOKENS + part, part,
+                                        threadIdx.x - part * nt, nt, sh);
+    }
 }
 
 // ---- Many tokens: persistent CTAs whose groups of four warps each have a ring of tokens in
@@ -208,8 +216,12 @@ constexpr int kRingGroups = 3;     // groups of a CTA
 constexpr int kRingThreads = 128;  // threads of a group
 constexpr int kRingStages = 8;     // tokens of a group's ring, at most
 constexpr int kRingFill = 96 << 10;  // bytes of the CTA's rings, about
-// Bytes of rows from which the ring pays: in pa_append, and for the q rows of pa_q8_append,
-// where it is one more launch.
+// Bytes of a token's rows from which the ring pays, for a token costs its group about 1 us
+// whatever its size (16384 tokens of 6 KB 53.4 us, directly 39.4; 8000 of 12 KB 36.3 and
+// 43.6), and bytes of all rows (1024 tokens of 16 KB 8.3 us, directly 10.1; 4 MB 5.8 and 4.5).
+// For the q rows of pa_q8_append it is one more launch (2048 tokens of 16 KB 25.0 us, directly
+// 23.3; 4096 equal).
+constexpr int kRingToken = 8 << 10;
 constexpr long long kRingBytes = 12 << 20, kRingBytesQ8 = 48 << 20;
 
 // What turns a row's pairs, weights included: (x, y) becomes (x a + y b, y c + x d) times
@@ -472,14 +484,14 @@ __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes), 64 / RowLanes<D
     using E = RopeElem<T>;
     constexpr int N = Rw::N, ES = Rw::ES, L = Rw::kLanes, W = N / 4, F = N / 2;
     constexpr int kWarpsHere = 16 * L / 32;
-    __shared__ AppendShared<D> sh;
+    __shared__ AppendShared<D, 1> sh;
     __shared__ uint32_t s_max[2][kWarpsHere];
     __shared__ unsigned long long s_freq[kMaxRopePairs];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     allow_dependent_launch();
     wait_for_prerequisite_grid();
     if ((int)blockIdx.x >= p.kv_ctas) {
-        append_token<D, T, false>(p, blockIdx.x - p.kv_ctas, sh);
+        append_token<D, T, false, 1>(p, blockIdx.x - p.kv_ctas, 0, tid, blockDim.x, sh);
         return;
     }
     const int is_v = blockIdx.x & 1, group = (blockIdx.x >> 1) % p.groups;
@@ -797,14 +809,23 @@ template <int D, typename T>
 static cudaError_t launch_append(const AppendParams& p, bool q8, cudaStream_t stream) {
     constexpr int L = RowLanes<D, T>::kLanes;
     const int heads = p.Hq + (q8 ? 0 : 2 * p.Hkv);
-    const bool ring = (long long)p.n * heads * D * (int)sizeof(T) >= (q8 ? kRingBytesQ8 : kRingBytes) &&
+    const long long token = (long long)heads * D * (int)sizeof(T);
+    const bool ring = token >= kRingToken && p.n * token >= (q8 ? kRingBytesQ8 : kRingBytes) &&
                       ring_stages<D, T>(heads) > 0;
     if (!q8) {
         if (ring) return launch_ring<D, T, true>(p, stream);
-        // Threads for kAppendItems items each.
-        const int threads = (heads * L + kAppendItems * 32 - 1) / (kAppendItems * 32) * 32;
-        return launch_step(append_kernel<D, T>, dim3(p.n), std::min(kAppendThreads, threads),
-                           stream, p);
+        auto direct = [&](auto kernel, int items, int tokens) {
+            const int nt = std::min(kAppendThreads, (heads * L + items * 32 - 1) / (items * 32) * 32);
+            return launch_step(kernel, dim3((p.n + tokens - 1) / tokens), nt * tokens, stream, p, nt);
+        };
+        // Few tokens: more threads for each.  Many: three items a thread, and two tokens a CTA
+        // where a warp is enough for one (16384 tokens of 16 + 2 x 4 heads: D 128 two items
+        // 44.5 us, three 39.4, in pairs 42.5; D 64 28.1, 23.7, 23.3; 512 tokens of 32 + 2 x 8
+        // heads, D 128: two 5.2, three 5.8).
+        if (p.n <= kAppendCtas) return direct(append_kernel<D, T, 2, 1>, 2, 1);
+        if (heads * L <= 2 * 32) return direct(append_kernel<D, T, 2, 2>, 2, 2);
+        if (heads * L <= 3 * 32) return direct(append_kernel<D, T, 3, 2>, 3, 2);
+        return direct(append_kernel<D, T, 3, 1>, 3, 1);
     }
     // (a tile's rows: at most kMaxTileBytes, see append_call)
     static std::atomic<unsigned long long> raised{0};  // the shared-memory limit, by device

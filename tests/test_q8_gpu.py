@@ -142,13 +142,23 @@ def test_append_shapes_in_place(n, hq, hkv, dtype):
     np.testing.assert_array_equal(host(r.tv), r.v)
 
 
+@pytest.mark.parametrize("n", [609, 1301])
+@pytest.mark.parametrize("D,rot,dtype,hq,hkv", [(64, 64, "f16", 8, 8), (96, 48, "f16", 8, 2), (64, 16, "bf16", 1, 1),
+                                                (64, 64, "f32", 32, 4), (96, 96, "bf16", 48, 8),
+                                                (128, 64, "f16", 32, 8), (256, 256, "bf16", 16, 2)])
+def test_append_some_hundred_tokens(n, D, rot, dtype, hq, hkv):
+    """Tokens of one warp each, two to a CTA, the last one alone; tokens of 8 KB and more,
+    through rings of them."""
+    test_append_many_tokens(n, D, rot, dtype, hq, hkv)
+
+
 @pytest.mark.parametrize("n", [2048, 2700, 5001])
 @pytest.mark.parametrize("D,rot,dtype,hq,hkv", [(64, 32, "f32", 3, 1), (96, 96, "bf16", 4, 2), (128, 128, "f16", 5, 1),
                                                 (256, 64, "bf16", 2, 1), (128, 128, "f32", 40, 8), (256, 256, "f32", 64, 1),
                                                 (64, 64, "f16", 0, 3)])
 def test_append_many_tokens(n, D, rot, dtype, hq, hkv):
     """Prompts of so many tokens that CTAs go through several; rows too wide for a ring of them."""
-    if n != 2700 and hq >= 40:
+    if n > 2000 and n != 2700 and hq >= 40:
         pytest.skip("one length is enough")
     r = Rows(n + D, n, hq, hkv, D, dtype, True, 1e4, rot)
     pages = n // 16 + 3
