@@ -20,6 +20,12 @@ namespace pa {
 
 constexpr int kAppendThreads = 256;  // at most, of pa_append
 constexpr int kMaxTileBytes = 48 << 10;  // of rows that a CTA holds at a time
+constexpr int kAppendTiles = 38;     // tiles of 16 rows, times KV heads and two, from which there are any
+// Runs of a tile from which they are served side by side (a step of 64 sequences, 32 + 2 x 8
+// heads of 128, with the q rows and read back: 6.9 -> 6.1 us, of 776 with 16 + 2 x 4 14.1 -> 9.2,
+// of 6615 with 48 + 2 x 8 of 64 194 -> 58.3; two runs of a prompt's chunks are faster one after
+// the other, 7707 rows 72.5 and 79.7).
+constexpr int kSideBySide = 3;
 constexpr int kAppendCtas = 608;     // CTAs that fill the GPU: four for each of 152 SMs
 
 struct AppendParams {
@@ -471,8 +477,9 @@ __device__ __forceinline__ void q8_store_codes(unsigned char* p, const uint32_t 
 }
 
 // The first kv_ctas CTAs go by (tile of rows, group of KV heads, K or V): in its tile a
-// CTA finds the rows that begin a run (rows at consecutive slots of a page).  For each
-// run and head a thread has its two pieces of a new row, and of a row that was there
+// CTA finds the rows that begin a run (rows at consecutive slots of a page).  Several runs
+// of a row each are served side by side, see below.  Otherwise, for each
+// run and head, a thread has its two pieces of a new row, and of a row that was there
 // before, if there are so many.  The largest magnitude goes through the CTA, the scale
 // follows, codes are stored.  The rows of the tile come by bulk copies, asked for beside
 // the slots; those of a run that goes on behind the tile (it is the tile's last) take the
@@ -486,6 +493,7 @@ __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes), 64 / RowLanes<D
     constexpr int kWarpsHere = 16 * L / 32;
     __shared__ AppendShared<D, 1> sh;
     __shared__ uint32_t s_max[2][kWarpsHere];
+    __shared__ float s_row[2][kPageSize];  // rows' largest magnitudes, by turns of heads
     __shared__ unsigned long long s_freq[kMaxRopePairs];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     allow_dependent_launch();
@@ -559,6 +567,132 @@ __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes), 64 / RowLanes<D
     bool behind = last_end > p.tile;
     if (!arrived()) return;
     if (!leads) return;
+    // A row of the run (x, y) normalised and rotated.
+    float2 cs[F], sn[F];
+    auto angles = [&](int pos) {
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            rope_angle(pos, s_freq[c * N + 2 * i], cs[i].x, sn[i].x);
+            rope_angle(pos, s_freq[c * N + 2 * i + 1], cs[i].y, sn[i].y);
+        }
+    };
+    float2 x[F], y[F];
+    auto load_row = [&](const unsigned char* from, bool fresh) {  // (the whole warp)
+        float(&xs)[N] = reinterpret_cast<float(&)[N]>(x);
+        float(&ys)[N] = reinterpret_cast<float(&)[N]>(y);
+        uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+        if (fresh) {
+            xa = *reinterpret_cast<const uint4*>(from + d0 * ES);
+            xb = *reinterpret_cast<const uint4*>(from + d1 * ES);
+        }
+        E::load(xa, xs);
+        E::load(xb, ys);
+        if (norm) Rw::normalise(xs, ys, sh.w[1], d0, d1, fresh, p.eps);
+        if (turn && fresh) {
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                const float2 minus = make_float2(-sn[i].x, -sn[i].y);
+                const float2 xr = __ffma2_rn(x[i], cs[i], __fmul2_rn(y[i], minus));
+                y[i] = __ffma2_rn(y[i], cs[i], __fmul2_rn(x[i], sn[i]));
+                x[i] = xr;
+            }
+        }
+    };
+    auto largest_here = [&]() {  // (NaN does not count)
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+            most = fmaxf(fmaxf(most, fmaxf(fabsf(x[i].x), fabsf(x[i].y))),
+                         fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
+        return most;
+    };
+    auto no_infinities = [&]() {
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            if (fabsf(x[i].x) > FLT_MAX) x[i].x = NAN;
+            if (fabsf(x[i].y) > FLT_MAX) x[i].y = NAN;
+            if (fabsf(y[i].x) > FLT_MAX) y[i].x = NAN;
+            if (fabsf(y[i].y) > FLT_MAX) y[i].y = NAN;
+        }
+    };
+    auto store_row = [&](unsigned char* to, float scale) {
+        const float inv = __frcp_rn(scale);
+        uint32_t ca[W], cb[W];
+        q8_codes(x, inv, ca);
+        q8_codes(y, inv, cb);
+        q8_store_codes(to + d0, ca);
+        q8_store_codes(to + d1, cb);
+    };
+    auto recode = [&](uint32_t (&k)[W], float ratio) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            float2 v[2];
+            uint32_t one[1];
+            q8_values(k[i], reinterpret_cast<float(&)[4]>(v));
+            q8_codes(v, ratio, one);
+            k[i] = one[0];
+        }
+    };
+    const uint32_t within = behind ? leads & ~(1u << last) : leads;
+    if (__popc(within) >= kSideBySide) {
+        // Several runs that end in the tile (a step's rows, one or a few of each sequence): the
+        // lanes of a row serve it, and a share of the rows that were in its page before.
+        const int j = i_row + 1;
+        const uint32_t upto = leads & ((2u << j) - 1);
+        const int begin = upto ? 31 - __clz(upto) : 0;  // where its run begins
+        const bool mine = (within >> begin & 1) && (begin == j || (on >> j & 1));
+        const bool fresh = have && mine, alone = (on >> 1 & within) == 0;  // (alone: in every run)
+        const long long first = __shfl_sync(0xffffffffu, slot, begin);
+        const int cnt = __ffs(~(on >> (begin + 1)));
+        const int r0 = mine ? (int)(first % kPageSize) : 0;
+        const size_t block0 = mine ? (size_t)(first / kPageSize) * p.Hkv : 0;
+        if (turn && fresh) angles(first_pos);
+        float next = r0 > 0 ? scales[block0 + h0] : 0.f;
+#pragma unroll 1
+        for (int h = h0; h < h1; ++h) {
+            const float was = next;
+            if (r0 > 0 && h + 1 < h1) next = scales[block0 + h + 1];
+            unsigned char* page = cache + (block0 + h) * (size_t)(kPageSize * D);
+            load_row(tile_smem + i_row * row_bytes + (h - h0) * (D * ES), fresh);
+            float most;
+#pragma unroll 1
+            for (bool again = false;; again = true) {
+                most = fresh ? largest_here() : 0.f;
+#pragma unroll
+                for (int m = 1; m < L; m <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
+                if (again || !__any_sync(0xffffffffu, most > FLT_MAX)) break;
+                no_infinities();
+            }
+            if (!alone) {
+                float* of_rows = s_row[h & 1];
+                if (c == 0) of_rows[i_row] = most;
+                __syncthreads();
+                if (mine)
+                    for (int i = begin - 1; i < begin - 1 + cnt; ++i) most = fmaxf(most, of_rows[i]);
+            }
+            const float old = was > 0.f && was <= FLT_MAX ? was : 0.f;
+            const float scale = fmaxf(old, q8_scale_for(most));
+            if (!mine) continue;
+            if (have) store_row(page + (r0 + j - begin) * D, scale);
+            if (scale == old) continue;
+            if (c == 0 && j == begin) scales[block0 + h] = scale;
+            const float ratio = __fdiv_rn(old, scale);
+            if (!have) continue;
+#pragma unroll 1
+            for (int r = j - begin; r < r0; r += cnt) {
+                uint32_t ka[W], kb[W];
+                q8_load_codes(ka, page + r * D + d0);
+                q8_load_codes(kb, page + r * D + d1);
+                recode(ka, ratio);
+                recode(kb, ratio);
+                q8_store_codes(page + r * D + d0, ka);
+                q8_store_codes(page + r * D + d1, kb);
+            }
+        }
+        if (!behind) return;
+        leads = 1u << last;
+        __syncthreads();  // (every thread has read the rows whose places the last run's take)
+    }
     if (behind && (leads & (leads - 1)) == 0) {
         if (warp == 0) fetch(p.tile, last_end);
         if (!arrived()) return;
@@ -579,15 +713,7 @@ __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes), 64 / RowLanes<D
         const bool fresh = have && i_row < cnt, kept = have && i_row < r0;
         const size_t block0 = (size_t)(first / kPageSize) * p.Hkv;
         const unsigned char* src = tile_smem + (j - 1 + i_row) % kPageSize * row_bytes;
-        float2 cs[F], sn[F];
-        if (turn && fresh) {
-            const int pos = j == 1 ? first_pos : p.positions[run + i_row];
-#pragma unroll
-            for (int i = 0; i < F; ++i) {
-                rope_angle(pos, s_freq[c * N + 2 * i], cs[i].x, sn[i].x);
-                rope_angle(pos, s_freq[c * N + 2 * i + 1], cs[i].y, sn[i].y);
-            }
-        }
+        if (turn && fresh) angles(j == 1 ? first_pos : p.positions[run + i_row]);
         for (int h = h0; h < h1; ++h) {
             unsigned char* page = cache + (block0 + h) * (size_t)(kPageSize * D);
             uint32_t ka[W] = {}, kb[W] = {};
@@ -596,32 +722,9 @@ __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes), 64 / RowLanes<D
                 q8_load_codes(kb, page + i_row * D + d1);
             }
             const float was = r0 > 0 ? scales[block0 + h] : 0.f;
-            uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
-            if (fresh) {
-                xa = *reinterpret_cast<const uint4*>(src + (h - h0) * (D * ES) + d0 * ES);
-                xb = *reinterpret_cast<const uint4*>(src + (h - h0) * (D * ES) + d1 * ES);
-            }
-            float2 x[F], y[F];
-            float(&xs)[N] = reinterpret_cast<float(&)[N]>(x);
-            float(&ys)[N] = reinterpret_cast<float(&)[N]>(y);
-            E::load(xa, xs);
-            E::load(xb, ys);
-            if (norm) Rw::normalise(xs, ys, sh.w[1], d0, d1, fresh, p.eps);
-            if (turn && fresh) {
-#pragma unroll
-                for (int i = 0; i < F; ++i) {
-                    const float2 minus = make_float2(-sn[i].x, -sn[i].y);
-                    const float2 xr = __ffma2_rn(x[i], cs[i], __fmul2_rn(y[i], minus));
-                    y[i] = __ffma2_rn(y[i], cs[i], __fmul2_rn(x[i], sn[i]));
-                    x[i] = xr;
-                }
-            }
-            auto largest = [&]() {  // (NaN does not count)
-                float most = 0.f;
-#pragma unroll
-                for (int i = 0; i < F; ++i)
-                    most = fmaxf(fmaxf(most, fmaxf(fabsf(x[i].x), fabsf(x[i].y))),
-                                 fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
+            load_row(src + (h - h0) * (D * ES), fresh);
+            auto largest = [&]() {
+                const float most = largest_here();
                 // over the CTA, as bits: numbers from 0 on are in the order of their bits
                 uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(fresh ? most : 0.f));
                 if (lane == 0) s_max[turn_of][warp] = all;
@@ -632,38 +735,16 @@ __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes), 64 / RowLanes<D
             };
             uint32_t all = largest();
             if (all == 0x7F800000u) {  // an infinity somewhere: NaN in its place, and again
-#pragma unroll
-                for (int i = 0; i < F; ++i) {
-                    if (fabsf(x[i].x) > FLT_MAX) x[i].x = NAN;
-                    if (fabsf(x[i].y) > FLT_MAX) x[i].y = NAN;
-                    if (fabsf(y[i].x) > FLT_MAX) y[i].x = NAN;
-                    if (fabsf(y[i].y) > FLT_MAX) y[i].y = NAN;
-                }
+                no_infinities();
                 all = largest();
             }
             const float old = was > 0.f && was <= FLT_MAX ? was : 0.f;
             const float scale = fmaxf(old, q8_scale_for(__uint_as_float(all)));
-            if (fresh) {
-                const float inv = __frcp_rn(scale);
-                uint32_t ca[W], cb[W];
-                q8_codes(x, inv, ca);
-                q8_codes(y, inv, cb);
-                q8_store_codes(page + (r0 + i_row) * D + d0, ca);
-                q8_store_codes(page + (r0 + i_row) * D + d1, cb);
-            }
+            if (fresh) store_row(page + (r0 + i_row) * D, scale);
             if (kept && scale != old) {
                 const float ratio = __fdiv_rn(old, scale);
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    float2 v[2];
-                    uint32_t one[1];
-                    q8_values(ka[i], reinterpret_cast<float(&)[4]>(v));
-                    q8_codes(v, ratio, one);
-                    ka[i] = one[0];
-                    q8_values(kb[i], reinterpret_cast<float(&)[4]>(v));
-                    q8_codes(v, ratio, one);
-                    kb[i] = one[0];
-                }
+                recode(ka, ratio);
+                recode(kb, ratio);
                 q8_store_codes(page + i_row * D + d0, ka);
                 q8_store_codes(page + i_row * D + d1, kb);
             }
@@ -949,11 +1030,11 @@ static int append_call(bool q8, int num_tokens, int num_q_heads, int num_kv_head
                sizeof(unsigned long long) * (rotary_dim / 2));
     }
     if (q8) {
-        // Tiles of 16 rows where they fill the GPU (a prompt's tile then is a run or two,
-        // and no CTA starts for nothing), else of one row; as many heads in one CTA as
+        // Tiles of 16 rows but for the smallest calls (300 rows of 8 + 2 heads of 96: from 152
+        // CTAs on 6.2 us, from 38 5.4), whose runs get a CTA each; as many heads in one CTA as
         // leave kAppendCtas of them, so that angles are worked out once for several.
         const long long tiles16 = ((long long)num_tokens + 15) / 16;
-        p.tile = tiles16 * 2 * num_kv_heads >= kAppendCtas ? 16 : 1;
+        p.tile = tiles16 * 2 * num_kv_heads >= kAppendTiles ? 16 : 1;
         const long long tiles = p.tile == 16 ? tiles16 : num_tokens;
         p.heads = (int)std::max(1ll, std::min<long long>(num_kv_heads,
                                                          tiles * 2 * num_kv_heads / kAppendCtas));

@@ -377,6 +377,40 @@ def test_q8_append_sizes(hkv, n, order):
     assert (want_k != rk.codes).any() and (want_v != rv.codes).any()
 
 
+@pytest.mark.parametrize("D,dtype", [(64, "f16"), (64, "f32"), (96, "bf16"), (128, "f16"), (128, "f32"),
+                                     (256, "bf16"), (256, "f32")])
+@pytest.mark.parametrize("hkv,most", [(1, 1), (2, 3), (3, 6), (20, 1), (9, 20)])
+def test_q8_append_steps_of_many_sequences(D, dtype, hkv, most):
+    """Tiles of several runs, of one row each or a few, beside rows that are left out; runs that
+    go on behind their tile or in the next page; infinities and NaN in some of the rows."""
+    n = 40 if hkv == 20 else 333
+    r = Rows(D + most, n, 2, hkv, D, dtype, True, 1e4, D)
+    g = r.g
+    slots, page = [], 0
+    while len(slots) < n:
+        at = int(g.integers(0, 16)) + np.arange(int(g.integers(1, most + 1)))
+        slots += list((page + at // 16) * 16 + at % 16)
+        page += int(at[-1]) // 16 + 1
+        if g.random() < 0.1:
+            slots.append(-1)
+    slots = np.array(slots[:n])
+    perm = g.permutation(page + 2)
+    slots = np.where(slots < 0, -1, perm[slots // 16] * 16 + slots % 16)
+    for value in (np.inf, -np.inf, np.nan):
+        i, h, d = g.integers(0, n, 12), g.integers(0, hkv, 12), g.integers(0, D, 12)
+        r.v[i, h, d] = value
+        r.tv[torch.from_numpy(i).cuda(), torch.from_numpy(h).cuda(), torch.from_numpy(d).cuda()] = value
+    r.v[n // 2] = 0.0
+    r.tv[n // 2] = 0.0
+    rk, rv = ref.Cache(page + 2, hkv, D), ref.Cache(page + 2, hkv, D)
+    for c in (rk, rv):
+        c.append(rows(g, ((page + 2) * 16, hkv, D), dtype) * 0.25, np.arange((page + 2) * 16))
+    caches = (f8(rk.codes), f8(rv.codes), torch.from_numpy(rk.scales).float().cuda(),
+              torch.from_numpy(rv.scales).float().cuda())
+    run_q8_append(r, slots, caches)
+    check_q8(r, slots, caches, rk, rv, exact_k=False)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 def test_q8_append_special_values(dtype):
     """Infinities and NaN, zeros of both signs, values at the borders of scales and codes, the
