@@ -20,6 +20,9 @@ namespace pa {
 
 constexpr int kAppendThreads = 256;  // at most, of pa_append
 constexpr int kMaxTileBytes = 48 << 10;  // of rows that a CTA holds at a time
+// Tokens whose q a CTA beside 8-bit runs serves, at most (16384 tokens of 8 + 2 x 2 heads of 64,
+// appended and read back: 1 26.1 us, 4 18.5, 8 the same).
+constexpr int kQTokens = 4;
 constexpr int kAppendTiles = 38;     // tiles of 16 rows, times KV heads and two, from which there are any
 // Runs of a tile from which they are served side by side (a step of 64 sequences, 32 + 2 x 8
 // heads of 128, with the q rows and read back: 6.9 -> 6.1 us, of 776 with 16 + 2 x 4 14.1 -> 9.2,
@@ -44,6 +47,7 @@ struct AppendParams {
     // 8-bit cache: CTAs in front that serve runs of rows, rows of such a CTA's tile, KV
     // heads that it goes through and groups of them
     int kv_ctas, tile, heads, groups;
+    int q_shift, q_tokens;  // of the other CTAs: log2 of the threads for a token's q, tokens
     unsigned long long freq[kMaxRopePairs];
 };
 
@@ -156,7 +160,7 @@ __device__ __forceinline__ void append_token(const AppendParams& p, long long t,
         if (i0 == 0) {  // (while the rows are on their way)
             Rw::stage(p.q_norm, sh.w[0]);
             if (ALL) Rw::stage(p.k_norm, sh.w[1]);
-            if (p.R > 0) {
+            if (p.R > 0 && real) {
                 const int pos = p.positions[t];
                 for (int i = tid; i < p.R / 2; i += nt)
                     rope_angle(pos, p.freq[i], sh.cos[part][i], sh.sin[part][i]);
@@ -483,7 +487,8 @@ __device__ __forceinline__ void q8_store_codes(unsigned char* p, const uint32_t 
 // before, if there are so many.  The largest magnitude goes through the CTA, the scale
 // follows, codes are stored.  The rows of the tile come by bulk copies, asked for beside
 // the slots; those of a run that goes on behind the tile (it is the tile's last) take the
-// places of rows before it, which are done with.  The other CTAs serve a token's q each.
+// places of rows before it, which are done with.  The other CTAs serve the q of a token or
+// a few.
 template <int D, typename T>
 __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes), 64 / RowLanes<D, T>::kLanes)
     q8_append_kernel(const AppendParams p) {
@@ -491,7 +496,7 @@ __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes), 64 / RowLanes<D
     using E = RopeElem<T>;
     constexpr int N = Rw::N, ES = Rw::ES, L = Rw::kLanes, W = N / 4, F = N / 2;
     constexpr int kWarpsHere = 16 * L / 32;
-    __shared__ AppendShared<D, 1> sh;
+    __shared__ AppendShared<D, kQTokens> sh;
     __shared__ uint32_t s_max[2][kWarpsHere];
     __shared__ float s_row[2][kPageSize];  // rows' largest magnitudes, by turns of heads
     __shared__ unsigned long long s_freq[kMaxRopePairs];
@@ -499,7 +504,11 @@ __global__ void __launch_bounds__(16 * (RowLanes<D, T>::kLanes), 64 / RowLanes<D
     allow_dependent_launch();
     wait_for_prerequisite_grid();
     if ((int)blockIdx.x >= p.kv_ctas) {
-        append_token<D, T, false, 1>(p, blockIdx.x - p.kv_ctas, 0, tid, blockDim.x, sh);
+        const int part = tid >> p.q_shift, nt = 1 << p.q_shift;
+        const long long t = (long long)(blockIdx.x - p.kv_ctas) * p.q_tokens + part;
+        // (threads that are left over: a token behind the last)
+        append_token<D, T, false, 1>(p, part < p.q_tokens ? t : p.n, min(part, p.q_tokens - 1),
+                                     tid & (nt - 1), nt, sh);
         return;
     }
     const int is_v = blockIdx.x & 1, group = (blockIdx.x >> 1) % p.groups;
@@ -919,8 +928,15 @@ static cudaError_t launch_append(const AppendParams& p, bool q8, cudaStream_t st
         if (e == cudaSuccess && dev < 64) raised.fetch_or(1ull << dev);
     }
     if (e != cudaSuccess) return e;
-    e = launch_step_smem(q8_append_kernel<D, T>, dim3(p.kv_ctas + (heads > 0 && !ring ? p.n : 0)),
-                         16 * L, smem, stream, p);
+    AppendParams with_q = p;
+    with_q.q_shift = 5;
+    while (2 << with_q.q_shift <= 16 * L && 1 << with_q.q_shift < heads * L) ++with_q.q_shift;
+    int q_ctas = 0;
+    if (heads > 0 && !ring) {
+        with_q.q_tokens = std::min(kQTokens, 16 * L >> with_q.q_shift);
+        q_ctas = (p.n + with_q.q_tokens - 1) / with_q.q_tokens;
+    }
+    e = launch_step_smem(q8_append_kernel<D, T>, dim3(p.kv_ctas + q_ctas), 16 * L, smem, stream, with_q);
     return e == cudaSuccess && ring ? launch_ring<D, T, false>(p, stream) : e;
 }
 

@@ -411,6 +411,19 @@ def test_q8_append_steps_of_many_sequences(D, dtype, hkv, most):
     check_q8(r, slots, caches, rk, rv, exact_k=False)
 
 
+@pytest.mark.parametrize("n", [1, 3, 50, 1001])
+@pytest.mark.parametrize("D,dtype,hq", [(128, "f16", 1), (128, "bf16", 6), (128, "f16", 9), (256, "f32", 3), (64, "bf16", 5),
+                                        (96, "f32", 4), (256, "f16", 17)])
+def test_q8_append_queries_of_few_heads(n, D, dtype, hq):
+    """q of several tokens to a CTA, of one, of threads that are left over."""
+    r = Rows(n + hq, n, hq, 1, D, dtype, True, 1e4, D // 2)
+    pages = n // 16 + 2
+    caches = pa.new_q8_cache(pages, 1, D)
+    for q_out in (torch.full((n, hq, D), float("nan"), dtype=T[dtype], device="cuda"), r.tq):
+        run_q8_append(r, np.arange(n), caches, q_out=q_out)
+        r.check_q(q_out)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 def test_q8_append_special_values(dtype):
     """Infinities and NaN, zeros of both signs, values at the borders of scales and codes, the
