@@ -160,7 +160,7 @@ int pa_q8_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
  * Precision: the codes of K and V and q are exact in the products (bf16 rows of q are
  * scaled by a power of two), scores, maxima and sums fp32; the weights are rounded to
  * fp16's 11 bits for the product with V and normalised by the sum of the rounded
- * weights.
+ * weights; lse has the sum of the others.
  * workspace as for pa_q4_decode.
  */
 int pa_q8_decode(const pa_q8_plan_t* plan, int num_rows, const void* q, const int32_t* starts,

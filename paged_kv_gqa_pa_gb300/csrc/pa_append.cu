@@ -6,6 +6,14 @@
 // partners (i and i + R / 2), or that lie side by side behind dim R; the lanes of a
 // row, a power of two of them, sum its squares by shuffles.  Everything between
 // load and store stays in registers.
+//
+// Three kernels put rows away.  Few tokens, or small ones: threads for each token, whose loads
+// go out before the angles are worked out (64 tokens of 32 + 2 x 8 heads of 128 3.5 us, the
+// launch and three dependent reads; 16384 of 16 + 2 x 4 39.4, 0.75 of the copy rate: bound by
+// instructions).  Many large ones: rings in shared memory (16384 tokens of 24 + 2 x 4 heads of
+// 256, bf16: 84.6 us, 0.94 of the copy rate).  8 bits: tiles of rows (the same tokens and their
+// read back 113 us, about 63 of them q's rows, 31 the runs', which are bound by instructions:
+// norm, angles, the largest, codes; 19 the reading, bound by latency).
 #include <float.h>
 
 #include <algorithm>
@@ -204,7 +212,8 @@ __device__ __forceinline__ void append_token(const AppendParams& p, long long t,
     }
 }
 
-// TOKENS tokens a CTA, nt threads for each.
+// TOKENS tokens a CTA, nt threads for each.  (Four CTAs an SM: 512 tokens of 32 + 2 x 8 heads
+// 5.15 us, five, with fewer registers, 5.53.)
 template <int D, typename T, int ITEMS, int TOKENS>
 __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendParams p, const int nt) {
     __shared__ AppendShared<D, TOKENS> sh;
@@ -222,6 +231,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendP
 // ---- Many tokens: persistent CTAs whose groups of four warps each have a ring of tokens in
 // shared memory, filled by bulk copies.
 
+// (16384 tokens of 16 KB: 3 groups with 96 KB on their way 85 us, 4 groups with 128 KB 92, with
+// 256 KB 94: more on their way is slower.)
 constexpr int kRingGroups = 3;     // groups of a CTA
 constexpr int kRingThreads = 128;  // threads of a group
 constexpr int kRingStages = 8;     // tokens of a group's ring, at most

@@ -8,6 +8,20 @@
 //   lse = ln 2 (m + log2 sum p)
 // page by page with a running maximum m; the codes of K and V become fp16 (every
 // e4m3 value is one) in registers in front of the mma.sync m16n8k16.
+//
+// Tokens are the products' rows, so a step with one query row wastes no more than seven of
+// eight columns, and a page of 16 tokens is one tile.  A warp takes whole pages, one after the
+// other of its CTA's range, with a ring of its own (a tensor copy for K and one for V, whose
+// swizzle makes every ldmatrix free of conflicts), an own maximum and own accumulators: no
+// barrier until the sequence ends.  V's codes come out of ldmatrix.trans with two tokens' bytes
+// of a dim pair in a word, one byte_perm from what the product takes.
+//
+// Bound by: the copies, where there is one tile of rows (4 sequences of 100000 tokens, 24/4
+// heads, D 256: 127 us, 0.95 of the copy rate; 16 of 8192 with two queries, 32/8, D 128: 49.2,
+// 0.81); with more the latency of a warp's page (four tiles of rows, eight queries: 91.8 us,
+// 0.44), whose accumulators leave two warps a scheduler; in short steps the start, of about
+// 1.3 us, and the joining of a sequence's states (16 of a 4096 window, five queries: 42.0 us
+// of a floor of 20).  Slots of a warp's ring, 2, 3, 4: 64 ragged sequences 47.8, 48.8, 48.9 us.
 #pragma once
 
 #include <cuda.h>
@@ -29,7 +43,8 @@ namespace pa {
 // cluster (48 sequences of 24 pages 10.0 us, in ranges 15.1; beyond, see kQ8Whole).
 constexpr int q8_short(int D) { return D == 256 ? 16 : 24; }
 // What a sequence's start and end cost a CTA, in pages: equal ranges are equal
-// in this cost, not in pages.
+// in this cost, not in pages.  (6, 12, 20: 64 ragged sequences 49.3, 48.8, 49.0 us, 16 with
+// five queries 44.9, 41.1, 41.1.)
 constexpr int kQ8Start = 12;
 // Where there is a CTA for each sequence, each has one unless the longest has so many pages
 // more than an equal range costs: that many are as long as cutting and joining.  (48 of 57
@@ -66,7 +81,7 @@ struct Q8AttendParams {
     void* out;
     float* lse;
     float* ws_o;    // [groups][X][2] partial outputs, normalised, [unit][lane][4]
-    float* ws_ml;   // [groups][X][2][8 NT][2] their maximum (log2 domain) and exp-sum
+    float* ws_ml;   // [groups][X][2][8 NT][2] their maximum (log2 domain) and exp-sum (lse's)
     int* ws_info;   // for the merge kernel: cost of a range, then s_base, s_rank, s_row [B + 1]
     unsigned* counters;  // [groups][B] partials left so far
     unsigned* err;
@@ -99,7 +114,7 @@ struct Q8Cfg {
     // Page ids and scales that a CTA stages at a time.
     static constexpr int kStaged = NT == 2 && D == 256 ? 256 : 512;
     static constexpr int kSmemBytes = 1024 + kRingBytes + kXBytes + kQBytes + kStaged * 12 +
-                                      kWarps * kRows * 8 + kWarps * kStages * 8;
+                                      kWarps * kRows * 12 + kRows * 4 + kWarps * kStages * 8;
     // CTAs per SM by registers.
     static constexpr int kMinBlocks = D == 256 || NT > 2 ? 2 : 3;
     static constexpr int kStaticBytes = kRows * 8 + 128;  // (beside the dynamic ones)
@@ -466,7 +481,9 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
     uint2* s_q = reinterpret_cast<uint2*>(xbuf + Cfg::kXBytes / 16);  // [tile][chunk][lane]
     float2* s_sc = reinterpret_cast<float2*>(s_q + Cfg::kQBytes / 8);  // K's and V's scale
     float2* s_ml = s_sc + Cfg::kStaged;                                // [warp][row] m, sum
-    uint64_t* bars = reinterpret_cast<uint64_t*>(s_ml + kWarps * Cfg::kRows);
+    float* s_l0 = reinterpret_cast<float*>(s_ml + kWarps * Cfg::kRows);  // [warp][row] lse's sum
+    float2* s_c = reinterpret_cast<float2*>(s_l0 + kWarps * Cfg::kRows);  // [row pair] see crow
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s_c + Cfg::kRows / 2);
     float* s_qmax = reinterpret_cast<float*>(xbuf);  // [warp][row] (while xbuf is idle)
     int* s_pid = reinterpret_cast<int*>(bars + kWarps * NS);
     int* s_base = s_pid + Cfg::kStaged;  // (s_pid: first row of the page in the cache's maps)
@@ -699,8 +716,10 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
     uint2 qf[Cfg::kQShared ? NT * QL : QL];
     float acc[NT][NC][4];  // O^T: dims 16 c + 2 g (0, 1) and the next (2, 3) of rows 2 t, 2 t + 1
     float m[NT][2];        // running maximum (log2 domain) of rows 2 t, 2 t + 1 of a tile
-    float l[NT][2];        // sums of this lane's weights
+    float l[NT][2];        // sums of this lane's weights as the products have them, in fp16,
+    float l0[NT][2];       // and as they are: outputs are divided by the one, lse is of the other
     float crow[NT][2];     // what a row's products are multiplied by, beside the page's scale
+                           // (kQShared: in s_c, for want of registers)
     float vref;            // acc counts in units of it
     int seq_L = 0, seq_end0 = 0, seq_rows = 0, row0 = 0;
     bool dead = false;     // a copy timed out
@@ -792,6 +811,10 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                 for (int i = 0; i < QL; ++i)
                     if (warp + i * kWarps < NC)
                         s_q[(n * NC + warp + i * kWarps) * 32 + lane] = qf[n * QL + i];
+            if (warp == 0 && g == 0) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s_c[4 * n + t] = make_float2(crow[n][0], crow[n][1]);
+            }
             __syncthreads();
         }
 #pragma unroll
@@ -802,6 +825,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                 for (int i = 0; i < 4; ++i) acc[n][c][i] = 0.f;
             m[n][0] = m[n][1] = kQ8NoMax;
             l[n][0] = l[n][1] = 0.f;
+            l0[n][0] = l0[n][1] = 0.f;
         }
         vref = 0.f;
         bad = dead;
@@ -913,7 +937,8 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         float e[NT][4], most = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float k0 = sc.x * crow[n][0], k1 = sc.x * crow[n][1];
+            const float2 by = Cfg::kQShared ? s_c[4 * n + t] : make_float2(crow[n][0], crow[n][1]);
+            const float k0 = sc.x * by.x, k1 = sc.x * by.y;
 #pragma unroll
             for (int i = 0; i < 4; ++i) e[n][i] = fmaf(s[n][i], i & 1 ? k1 : k0, -m[n][i & 1]);
         }
@@ -934,7 +959,8 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     // (again from the products: against no maximum yet, e has lost them)
-                    const float k = sc.x * crow[n][i];
+                    const float2 by = Cfg::kQShared ? s_c[4 * n + t] : make_float2(crow[n][0], crow[n][1]);
+                    const float k = sc.x * (i ? by.y : by.x);
                     const float xa = e[n][i] == -INFINITY ? -INFINITY : s[n][i] * k;
                     const float xb = e[n][i + 2] == -INFINITY ? -INFINITY : s[n][i + 2] * k;
                     float x = fmaxf(xa, xb);
@@ -947,6 +973,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                     e[n][i] = xa - top;
                     e[n][i + 2] = xb - top;
                     l[n][i] *= f;
+                    l0[n][i] *= f;
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         acc[n][c][i] *= f;
@@ -972,8 +999,10 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         uint32_t b0[NT], b1[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint32_t ha = q8_pack(ex2(e[n][0]), ex2(e[n][1]));
-            const uint32_t hb = q8_pack(ex2(e[n][2]), ex2(e[n][3]));
+            const float p0 = ex2(e[n][0]), p1 = ex2(e[n][1]), p2 = ex2(e[n][2]), p3 = ex2(e[n][3]);
+            const uint32_t ha = q8_pack(p0, p1), hb = q8_pack(p2, p3);
+            l0[n][0] += p0 + p2;
+            l0[n][1] += p1 + p3;
             const float2 fa = q8_unpack(ha), fb = q8_unpack(hb);
             l[n][0] += fa.x + fb.x;
             l[n][1] += fa.y + fb.y;
@@ -1032,9 +1061,11 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                for (int k = 4; k < 32; k <<= 1)
+                for (int k = 4; k < 32; k <<= 1) {
                     l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], k);
-                if (bad) l[n][i] = NAN;
+                    l0[n][i] += __shfl_xor_sync(0xffffffffu, l0[n][i], k);
+                }
+                if (bad) l[n][i] = l0[n][i] = NAN;
             }
         __syncthreads();  // the last use of xbuf and s_ml is over
         if (g == 0) {
@@ -1042,12 +1073,15 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
+                {
                     s_ml[warp * Cfg::kRows + 8 * n + 2 * t + i] = make_float2(m[n][i], l[n][i]);
+                    s_l0[warp * Cfg::kRows + 8 * n + 2 * t + i] = l0[n][i];
+                }
         }
         __syncthreads();
         // A lane for each row: maximum and sum over the warps, and this warp's factor.
         // (A sum of 0: the warp had no page.  NaN is kept.)
-        float top = -INFINITY, sum = 0.f, own = 0.f;
+        float top = -INFINITY, sum = 0.f, sum0 = 0.f, own = 0.f;
         {
             float2 ml[kWarps];
 #pragma unroll
@@ -1059,17 +1093,18 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             for (int w = 0; w < kWarps; ++w) {
                 const float f = ml[w].y == 0.f ? 0.f : (ml[w].y != ml[w].y ? NAN : ex2(ml[w].x - top));
                 sum += f * ml[w].y;
+                sum0 += f * s_l0[w * Cfg::kRows + min(lane, Cfg::kRows - 1)];
                 if (w == warp) own = f == 0.f ? 0.f : f * vref;
             }
         }
         const float inv = q8_inverse(sum);
         if (warp == 0 && lane < seq_rows) {
             if (kCluster)
-                s_sum[lane] = make_float2(top, sum);
+                s_sum[lane] = make_float2(top, sum0);
             else if (!cut)
-                q8_store_lse(p, row0, h0, lane, top, sum);
+                q8_store_lse(p, row0, h0, lane, top, sum0);
             else
-                reinterpret_cast<float2*>(p.ws_ml)[wrow * Cfg::kRows + lane] = make_float2(top, sum);
+                reinterpret_cast<float2*>(p.ws_ml)[wrow * Cfg::kRows + lane] = make_float2(top, sum0);
         }
         // Tile by tile the warps' shares meet in shared memory; a warp adds up units of it.
         // (Rolled: this runs once a sequence, from instructions that have to be fetched.)

@@ -699,6 +699,20 @@ def test_decode_sequences_with_a_cta_each(longest, queries, window):
     Decode(longest, lens, 4, 1, 64, "f16", T=queries).case(window=window, ctas=7)
 
 
+@pytest.mark.parametrize("D,dtype", DIMS)
+@pytest.mark.parametrize("queries", [1, 3, 8])
+@pytest.mark.parametrize("cluster", [None, 0])
+def test_decode_lse_is_of_the_unrounded_weights(D, dtype, queries, cluster):
+    # The bound less what rounding the weights to 11 bits would add, with 2^-24 for each of the
+    # additions a weight goes through.
+    d = Decode(45 + queries, [3, 40, 700, 2100, 5000], 4, 1, D, dtype, T=queries)
+    _, lse, _ = d.run(D ** -0.5, cluster=cluster)
+    _, want, _, ltol = d.want(D ** -0.5, 0)
+    room = ltol - 2.0 ** -11 + 2.0 ** -24 * (16 + 5000 / 8)
+    fin = np.isfinite(want)
+    assert fin.any() and (np.abs(lse[fin] - want[fin]) <= room[fin]).all()
+
+
 def test_decode_long_ranges_are_staged_in_stretches():
     # One CTA serves 2600 pages, more than it stages at a time, with sequences that end at,
     # before and behind the borders of the stretches.
