@@ -37,7 +37,10 @@ EXPORTED = ("pa_plan", "pa_plan_ex", "pa_decode", "pa_decode_partitions", "pa_me
             "pa_decode_static",
             # include/pa_q4.h (q4.py)
             "pa_q4_page_bytes", "pa_q4_write", "pa_q4_read", "pa_q4_plan", "pa_q4_decode",
-            "pa_extend_tables", "pa_rope_axes")
+            "pa_extend_tables", "pa_rope_axes",
+            # include/pa_q8.h (q8.py)
+            "pa_append", "pa_q8_append", "pa_q8_read", "pa_q8_plan", "pa_q8_decode",
+            "pa_verify_drafts")
 
 
 class pa_plan_t(ctypes.Structure):
