@@ -8,8 +8,10 @@
 // all its threads within that warp's stretch.  Sums are of whole numbers, so no order
 // changes them.
 //
-// Bound by memory: one row of the target's probabilities, and one of the draft's where
-// a draft was not accepted, are read once.
+// Bound by memory where rows are many and long: one row of the target's probabilities, and
+// one of the draft's where a draft was not accepted, are read once (128 sequences of 131072 in
+// fp32 26.7 us of a floor of 19); else by a fixed part of 5 to 6 us, the launch, the gather of
+// the drafts' probabilities, the exchange of sums and the search (1 of 32003: 5.3 us).
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -27,6 +29,10 @@ constexpr int kVerifyCluster = 8;    // CTAs of a sequence, at most
 // lane; more of them two, and run seven at a time on an SM (128 sequences of 131072: 28.5
 // and 26.7 us, 64: 16.0 and 16.4).
 constexpr int kVerifyWave = 608;
+// Up to so many run two at a time on an SM with eight loads in flight (8 sequences of 131072 8.2
+// -> 6.8 us, 23 of 199880 14.8 -> 12.4, 32 of 131072 11.9 -> 10.4; 38 of 128000, 304 CTAs, whose
+// clusters no longer fit at once, 10.4 -> 14.3).
+constexpr int kVerifyFew = 256;
 constexpr int kVerifyMaxVocab = 1 << 19;  // (sums of 2^19 weights of 1 fit 64 bits)
 
 struct VerifyParams {
@@ -168,7 +174,8 @@ struct VerifyRow {
 };
 
 template <typename T, int LOADS>
-__global__ void __launch_bounds__(kVerifyThreads, (LOADS > 2 ? 4 : 7)) verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVerifyThreads, (LOADS > 4 ? 2 : LOADS > 2 ? 4 : 7))
+    verify_kernel(const VerifyParams p) {
     __shared__ int s_stop[2];                                // j, and the draft there
     __shared__ unsigned long long s_warp[kVerifyWarps];      // sums of the warps' stretches
     __shared__ unsigned long long s_cta[2][kVerifyCluster];  // of the cluster's CTAs (by pass)
@@ -317,6 +324,7 @@ static cudaError_t launch_verify(const VerifyParams& p, int batch, cudaStream_t 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    if (batch * p.cluster <= kVerifyFew) return cudaLaunchKernelEx(&cfg, verify_kernel<T, 8>, p);
     return batch * p.cluster <= kVerifyWave ? cudaLaunchKernelEx(&cfg, verify_kernel<T, 4>, p)
                                             : cudaLaunchKernelEx(&cfg, verify_kernel<T, 2>, p);
 }

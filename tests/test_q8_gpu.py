@@ -1198,7 +1198,8 @@ def check_verify(c, dtype, offset=0):
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("B,V,drafts", [(1, 1, 1), (3, 2, 2), (40, 17, 3), (7, 1000, 8), (5, 4096, 4),
-                                        (4, 8195, 32), (3, 32003, 4), (2, 131072, 5), (1, 524288, 1)])
+                                        (4, 8195, 32), (3, 32003, 4), (2, 131072, 5), (1, 524288, 1),
+                                        (3, 32002, 3), (40, 16388, 2), (200, 9002, 2)])
 def test_verify(B, V, drafts, dtype):
     if dtype != "f32" and V > 100000:
         pytest.skip("one type is enough")
