@@ -31,7 +31,8 @@ constexpr int kMaxTileBytes = 48 << 10;  // of rows that a CTA holds at a time
 // Tokens whose q a CTA beside 8-bit runs serves, at most (16384 tokens of 8 + 2 x 2 heads of 64,
 // appended and read back: 1 26.1 us, 4 18.5, 8 the same).
 constexpr int kQTokens = 4;
-constexpr int kAppendTiles = 38;     // tiles of 16 rows, times KV heads and two, from which there are any
+// Tiles have 16 rows where that makes so many of them, times KV heads, times two; see append_call.
+constexpr int kAppendTiles = 38;
 // Runs of a tile from which they are served side by side (a step of 64 sequences, 32 + 2 x 8
 // heads of 128, with the q rows and read back: 6.9 -> 6.1 us, of 776 with 16 + 2 x 4 14.1 -> 9.2,
 // of 6615 with 48 + 2 x 8 of 64 194 -> 58.3; two runs of a prompt's chunks are faster one after
@@ -493,7 +494,7 @@ __device__ __forceinline__ void q8_store_codes(unsigned char* p, const uint32_t 
 
 // The first kv_ctas CTAs go by (tile of rows, group of KV heads, K or V): in its tile a
 // CTA finds the rows that begin a run (rows at consecutive slots of a page).  Several runs
-// of a row each are served side by side, see below.  Otherwise, for each
+// that end in the tile are served side by side, see below.  Otherwise, for each
 // run and head, a thread has its two pieces of a new row, and of a row that was there
 // before, if there are so many.  The largest magnitude goes through the CTA, the scale
 // follows, codes are stored.  The rows of the tile come by bulk copies, asked for beside
