@@ -4,7 +4,7 @@
 // For sequence b and the R = G T_b query rows (G heads, T_b tokens) of a KV
 // head's chunk, in NT tiles of 8 rows:
 //   S^T[16 tokens x 8] = K[16 x D] Q^T, p = 2^(scale log2(e) k_scale S - m),
-//   O^T[D x 8] += V^T[D x 16] (v_scale P)^T, out = O / sum p,
+//   O^T[D x 8] += V^T[D x 16] (v_scale P)^T in two parts, out = O / sum p,
 //   lse = ln 2 (m + log2 sum p)
 // page by page with a running maximum m; the codes of K and V become fp16 (every
 // e4m3 value is one) in registers in front of the mma.sync m16n8k16.
@@ -18,9 +18,9 @@
 //
 // Bound by: the copies, where there is one tile of rows (4 sequences of 100000 tokens, 24/4
 // heads, D 256: 127 us, 0.95 of the copy rate; 16 of 8192 with two queries, 32/8, D 128: 49.2,
-// 0.81); with more the latency of a warp's page (four tiles of rows, eight queries: 91.8 us,
-// 0.44), whose accumulators leave two warps a scheduler; in short steps the start, of about
-// 1.3 us, and the joining of a sequence's states (16 of a 4096 window, five queries: 42.0 us
+// 0.81); with more the latency of a warp's page (four tiles of rows, eight queries: 103.5 us,
+// 0.39), whose accumulators leave two warps a scheduler; in short steps the start, of about
+// 1.3 us, and the joining of a sequence's states (16 of a 4096 window, five queries: 47.0 us
 // of a floor of 20).  Slots of a warp's ring, 2, 3, 4: 64 ragged sequences 47.8, 48.8, 48.9 us.
 #pragma once
 
@@ -81,7 +81,7 @@ struct Q8AttendParams {
     void* out;
     float* lse;
     float* ws_o;    // [groups][X][2] partial outputs, normalised, [unit][lane][4]
-    float* ws_ml;   // [groups][X][2][8 NT][2] their maximum (log2 domain) and exp-sum (lse's)
+    float* ws_ml;   // [groups][X][2][8 NT][2] their maximum (log2 domain) and exp-sum
     int* ws_info;   // for the merge kernel: cost of a range, then s_base, s_rank, s_row [B + 1]
     unsigned* counters;  // [groups][B] partials left so far
     unsigned* err;
@@ -114,7 +114,7 @@ struct Q8Cfg {
     // Page ids and scales that a CTA stages at a time.
     static constexpr int kStaged = NT == 2 && D == 256 ? 256 : 512;
     static constexpr int kSmemBytes = 1024 + kRingBytes + kXBytes + kQBytes + kStaged * 12 +
-                                      kWarps * kRows * 12 + kRows * 4 + kWarps * kStages * 8;
+                                      kWarps * kRows * 8 + kRows * 4 + kWarps * kStages * 8;
     // CTAs per SM by registers.
     static constexpr int kMinBlocks = D == 256 || NT > 2 ? 2 : 3;
     static constexpr int kStaticBytes = kRows * 8 + 128;  // (beside the dynamic ones)
@@ -186,12 +186,6 @@ __device__ __forceinline__ uint32_t q8_high(uint32_t x) {
         : "=r"(y)
         : "r"(x));
     return y;
-}
-
-__device__ __forceinline__ uint32_t q8_hmul2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
 }
 
 // 0x80 in every byte that is the code of a NaN (0x7F, 0xFF).
@@ -481,8 +475,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
     uint2* s_q = reinterpret_cast<uint2*>(xbuf + Cfg::kXBytes / 16);  // [tile][chunk][lane]
     float2* s_sc = reinterpret_cast<float2*>(s_q + Cfg::kQBytes / 8);  // K's and V's scale
     float2* s_ml = s_sc + Cfg::kStaged;                                // [warp][row] m, sum
-    float* s_l0 = reinterpret_cast<float*>(s_ml + kWarps * Cfg::kRows);  // [warp][row] lse's sum
-    float2* s_c = reinterpret_cast<float2*>(s_l0 + kWarps * Cfg::kRows);  // [row pair] see crow
+    float2* s_c = s_ml + kWarps * Cfg::kRows;                          // [row pair] see crow
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_c + Cfg::kRows / 2);
     float* s_qmax = reinterpret_cast<float*>(xbuf);  // [warp][row] (while xbuf is idle)
     int* s_pid = reinterpret_cast<int*>(bars + kWarps * NS);
@@ -716,8 +709,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
     uint2 qf[Cfg::kQShared ? NT * QL : QL];
     float acc[NT][NC][4];  // O^T: dims 16 c + 2 g (0, 1) and the next (2, 3) of rows 2 t, 2 t + 1
     float m[NT][2];        // running maximum (log2 domain) of rows 2 t, 2 t + 1 of a tile
-    float l[NT][2];        // sums of this lane's weights as the products have them, in fp16,
-    float l0[NT][2];       // and as they are: outputs are divided by the one, lse is of the other
+    float l[NT][2];        // sums of this lane's weights
     float crow[NT][2];     // what a row's products are multiplied by, beside the page's scale
                            // (kQShared: in s_c, for want of registers)
     float vref;            // acc counts in units of it
@@ -825,7 +817,6 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                 for (int i = 0; i < 4; ++i) acc[n][c][i] = 0.f;
             m[n][0] = m[n][1] = kQ8NoMax;
             l[n][0] = l[n][1] = 0.f;
-            l0[n][0] = l0[n][1] = 0.f;
         }
         vref = 0.f;
         bad = dead;
@@ -973,7 +964,6 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                     e[n][i] = xa - top;
                     e[n][i + 2] = xb - top;
                     l[n][i] *= f;
-                    l0[n][i] *= f;
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         acc[n][c][i] *= f;
@@ -994,46 +984,63 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         }
         const float ratio = sc.y == vref ? 1.f : __fdividef(sc.y, vref);
         const bool direct = ratio >= kQ8LeastRatio;
-        const uint32_t r2 = direct ? q8_pack(ratio, ratio) : 0x3C003C00u;
-        // Weights; P^T's fragments are S^T's, each 8 x 8 block transposed.
-        uint32_t b0[NT], b1[NT];
+        const float on_weights = direct ? ratio : 1.f;
+        // Weights, times the page's ratio, as two fp16 numbers each, a head and a rest: 22 bits, and
+        // 2^-33 of the greatest at least.  P^T's fragments are S^T's, each 8 x 8 block transposed.
+        // (Heads alone, 11 bits, move rows across roundings' borders; with one or two tiles of
+        // rows the rests cost nothing, with three five queries of 16 sequences behind a window
+        // of 4096 go 41.7 -> 47.0 us, with four eight of 8192 91.5 -> 103.5: 8 cycles a product.)
+        uint32_t b0[NT][2], b1[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float p0 = ex2(e[n][0]), p1 = ex2(e[n][1]), p2 = ex2(e[n][2]), p3 = ex2(e[n][3]);
-            const uint32_t ha = q8_pack(p0, p1), hb = q8_pack(p2, p3);
-            l0[n][0] += p0 + p2;
-            l0[n][1] += p1 + p3;
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = ex2(e[n][i]);
+            l[n][0] += w[0] + w[2];
+            l[n][1] += w[1] + w[3];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] *= on_weights;
+            const uint32_t ha = q8_pack(w[0], w[1]), hb = q8_pack(w[2], w[3]);
             const float2 fa = q8_unpack(ha), fb = q8_unpack(hb);
-            l[n][0] += fa.x + fb.x;
-            l[n][1] += fa.y + fb.y;
-            b0[n] = q8_movmatrix(q8_hmul2(ha, r2));
-            b1[n] = q8_movmatrix(q8_hmul2(hb, r2));
+            b0[n][0] = q8_movmatrix(ha);
+            b1[n][0] = q8_movmatrix(hb);
+            b0[n][1] = q8_movmatrix(q8_pack(w[0] - fa.x, w[1] - fa.y));
+            b1[n][1] = q8_movmatrix(q8_pack(w[2] - fb.x, w[3] - fb.y));
         }
         // V: tokens 2 t, 2 t + 1 and 8 on, dims 2 g and 2 g + 1 of a chunk.
         auto products = [&](auto straight) PA_INLINE_LAMBDA {
             constexpr bool STRAIGHT = decltype(straight)::value;
 #pragma unroll
             for (int c = 0; c < NC; c += 2) {
-                uint32_t x[4];
+                uint32_t x[4], a[2][4];
                 q8_ldmatrix_trans(x, at + PB + q8_chunk<D>(lm_row, c + lm_half));
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t ya = __byte_perm(x[2 * k], 0, 0x3120);
                     const uint32_t yb = __byte_perm(x[2 * k + 1], 0, 0x3120);
-                    const uint32_t a0 = q8_low(ya), a1 = q8_high(ya);
-                    const uint32_t a2 = q8_low(yb), a3 = q8_high(yb);
+                    a[k][0] = q8_low(ya), a[k][1] = q8_high(ya);
+                    a[k][2] = q8_low(yb), a[k][3] = q8_high(yb);
+                }
+                if constexpr (STRAIGHT) {  // (rests first: two products of one sum lie far apart)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if constexpr (STRAIGHT) {
-                            q8_mma(acc[n][c + k], a0, a1, a2, a3, b0[n], b1[n]);
-                        } else {
+                    for (int h = 1; h >= 0; --h)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                q8_mma(acc[n][c + k], a[k][0], a[k][1], a[k][2], a[k][3], b0[n][h], b1[n][h]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
                             float d[4];
-                            q8_mma0(d, a0, a1, a2, a3, b0[n], b1[n]);
+                            q8_mma0(d, a[k][0], a[k][1], a[k][2], a[k][3], b0[n][1], b1[n][1]);
+                            q8_mma(d, a[k][0], a[k][1], a[k][2], a[k][3], b0[n][0], b1[n][0]);
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 acc[n][c + k][i] = fmaf(ratio, d[i], acc[n][c + k][i]);
                         }
-                    }
                 }
             }
         };
@@ -1061,11 +1068,8 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                for (int k = 4; k < 32; k <<= 1) {
-                    l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], k);
-                    l0[n][i] += __shfl_xor_sync(0xffffffffu, l0[n][i], k);
-                }
-                if (bad) l[n][i] = l0[n][i] = NAN;
+                for (int k = 4; k < 32; k <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], k);
+                if (bad) l[n][i] = NAN;
             }
         __syncthreads();  // the last use of xbuf and s_ml is over
         if (g == 0) {
@@ -1073,15 +1077,12 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                {
                     s_ml[warp * Cfg::kRows + 8 * n + 2 * t + i] = make_float2(m[n][i], l[n][i]);
-                    s_l0[warp * Cfg::kRows + 8 * n + 2 * t + i] = l0[n][i];
-                }
         }
         __syncthreads();
         // A lane for each row: maximum and sum over the warps, and this warp's factor.
         // (A sum of 0: the warp had no page.  NaN is kept.)
-        float top = -INFINITY, sum = 0.f, sum0 = 0.f, own = 0.f;
+        float top = -INFINITY, sum = 0.f, own = 0.f;
         {
             float2 ml[kWarps];
 #pragma unroll
@@ -1093,18 +1094,17 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             for (int w = 0; w < kWarps; ++w) {
                 const float f = ml[w].y == 0.f ? 0.f : (ml[w].y != ml[w].y ? NAN : ex2(ml[w].x - top));
                 sum += f * ml[w].y;
-                sum0 += f * s_l0[w * Cfg::kRows + min(lane, Cfg::kRows - 1)];
                 if (w == warp) own = f == 0.f ? 0.f : f * vref;
             }
         }
         const float inv = q8_inverse(sum);
         if (warp == 0 && lane < seq_rows) {
             if (kCluster)
-                s_sum[lane] = make_float2(top, sum0);
+                s_sum[lane] = make_float2(top, sum);
             else if (!cut)
-                q8_store_lse(p, row0, h0, lane, top, sum0);
+                q8_store_lse(p, row0, h0, lane, top, sum);
             else
-                reinterpret_cast<float2*>(p.ws_ml)[wrow * Cfg::kRows + lane] = make_float2(top, sum0);
+                reinterpret_cast<float2*>(p.ws_ml)[wrow * Cfg::kRows + lane] = make_float2(top, sum);
         }
         // Tile by tile the warps' shares meet in shared memory; a warp adds up units of it.
         // (Rolled: this runs once a sequence, from instructions that have to be fetched.)
