@@ -13,8 +13,9 @@
  * A code c of KV head h in page p stands for k_scales[p][h] * c.  e4m3 is the
  * 8-bit float with 4 exponent and 3 mantissa bits, largest value 448, NaN 0x7F and
  * 0xFF, no infinities (torch.float8_e4m3fn).  pa_q8_decode takes any
- * positive scales up to 2^126; those that pa_q8_append makes are powers of two, so that a
- * scale costs no precision and raising it later is a shift of the exponent.
+ * positive scales up to 2^126 with which V's values are finite in fp32; those that
+ * pa_q8_append makes are powers of two, so that a scale costs no precision and raising it
+ * later is a shift of the exponent.
  */
 #ifndef PA_GB300_Q8_H
 #define PA_GB300_Q8_H
@@ -158,7 +159,9 @@ int pa_q8_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
  * than max_query_len apart too, and for starts that do not ascend or lie outside
  * [0, num_rows], where it is not known which rows the sequence has: none is written).
  * Precision: the codes of K and V and q are exact in the products (bf16 rows of q are
- * scaled by a power of two), scores, maxima and sums fp32.  In the product with V a
+ * scaled by a power of two), scores, maxima and sums fp32.  Scores are these products times
+ * one fp32 factor, the call's scale times log2(e), K's scale and q's power of two: a factor
+ * that overflows makes its rows NaN, a score that does to -inf weighs nothing.  In the product with V a
  * weight, times its page's V scale relative to the greatest met, is two fp16 numbers, a
  * head and a rest (22 bits; what is below 2^-33 of the row's greatest weight is nothing);
  * products are summed in fp32 and normalised by the fp32 sum of the weights, which lse

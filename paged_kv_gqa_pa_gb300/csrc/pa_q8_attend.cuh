@@ -280,12 +280,12 @@ __device__ __forceinline__ size_t q8_out_row(const Q8AttendParams& p, int row0, 
 // Unit u of the rows that begin at row0, head h0.
 template <int D, int NT>
 __device__ __forceinline__ void q8_store_unit(const Q8AttendParams& p, int row0, int h0, int u,
-                                              int lane, float4 o, float inv) {
+                                              int lane, float4 o) {
     uint32_t* at = reinterpret_cast<uint32_t*>(
         reinterpret_cast<__half*>(p.out) +
         q8_out_row(p, row0, h0, q8_unit_row<D, NT>(u, lane)) * D + q8_unit_dim<D, NT>(u, lane));
-    at[0] = q8_out2(p.bf16, o.x * inv, o.y * inv);
-    at[8] = q8_out2(p.bf16, o.z * inv, o.w * inv);
+    at[0] = q8_out2(p.bf16, o.x, o.y);
+    at[8] = q8_out2(p.bf16, o.z, o.w);
 }
 
 __device__ __forceinline__ void q8_store_lse(const Q8AttendParams& p, int row0, int h0, int r,
@@ -326,7 +326,8 @@ __device__ __forceinline__ float2 q8_ld_peer2(uint32_t addr) {
     return v;
 }
 
-// A log-sum-exp merge: N more partials (a sum of 0: none; NaN is kept).
+// A log-sum-exp merge: N more partials (a sum of 0: none; NaN is kept).  o is an average
+// throughout, so that it is no larger than the largest of V, which may be next to fp32's end.
 struct Q8Merge {
     float top, sum;
     float4 o;
@@ -336,16 +337,22 @@ struct Q8Merge {
         float most = top;
 #pragma unroll
         for (int i = 0; i < N; ++i) most = fmaxf(most, ml[i].x);
-        const float f = top == -INFINITY ? 0.f : ex2(top - most);
-        sum *= f;
-        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+        float w[N];
+        const float before = top == -INFINITY ? 0.f : sum * ex2(top - most);
+        sum = before;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float l = ml[i].y;
-            const float w = l == 0.f ? 0.f : (l != l ? NAN : ex2(ml[i].x - most) * l);
-            if (w == 0.f) continue;
-            sum += w;
-            o.x += w * v[i].x, o.y += w * v[i].y, o.z += w * v[i].z, o.w += w * v[i].w;
+            w[i] = l == 0.f ? 0.f : (l != l ? NAN : ex2(ml[i].x - most) * l);
+            sum += w[i];
+        }
+        const float inv = q8_inverse(sum), f = before * inv;
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (w[i] == 0.f) continue;
+            w[i] *= inv;
+            o.x += w[i] * v[i].x, o.y += w[i] * v[i].y, o.z += w[i] * v[i].z, o.w += w[i] * v[i].w;
         }
         top = most;
     }
@@ -382,7 +389,7 @@ __device__ __forceinline__ void q8_finish_unit(const Q8AttendParams& p, int row0
                                                int h0, int u, int lane, const Q8Merge& m) {
     const int r = q8_unit_row<D, NT>(u, lane);
     if (r >= nrows) return;
-    q8_store_unit<D, NT>(p, row0, h0, u, lane, m.o, q8_inverse(m.sum));
+    q8_store_unit<D, NT>(p, row0, h0, u, lane, m.o);
     if (u % Q8Cfg<D, NT>::kTileUnits < 2 && lane < 4) q8_store_lse(p, row0, h0, r, m.top, m.sum);
 }
 
@@ -423,15 +430,12 @@ __global__ void __launch_bounds__(kQ8MergeWarps * 32) q8_merge_kernel(const Q8At
     s_o[warp][lane] = r.o;
     __syncthreads();
     if (warp != 0) return;
-    // (what the warps hold are sums of weighted outputs: as outputs of weight 1)
     float2 ml[kQ8MergeWarps];
     float4 v[kQ8MergeWarps];
 #pragma unroll
     for (int w = 0; w < kQ8MergeWarps; ++w) {
         ml[w] = s_ml[w][lane];
         v[w] = s_o[w][lane];
-        const float inv = q8_inverse(ml[w].y);
-        v[w].x *= inv, v[w].y *= inv, v[w].z *= inv, v[w].w *= inv;
     }
     Q8Merge all;
     all.add(ml, v);
@@ -973,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         }
         // The page's V scale against the reference, which only rises.
         if (!(sc.y <= vref)) {
-            const float f = __fdividef(vref, sc.y);
+            const float f = vref == 0.f ? 0.f : __fdividef(vref, sc.y);
             vref = sc.y;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -1080,8 +1084,9 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                     s_ml[warp * Cfg::kRows + 8 * n + 2 * t + i] = make_float2(m[n][i], l[n][i]);
         }
         __syncthreads();
-        // A lane for each row: maximum and sum over the warps, and this warp's factor.
-        // (A sum of 0: the warp had no page.  NaN is kept.)
+        // A lane for each row: maximum and sum over the warps, and this warp's factor, its share
+        // of a weight of 1: times the greatest V scale only then, for that may be next to fp32's
+        // end.  (A sum of 0: the warp had no page.  NaN is kept.)
         float top = -INFINITY, sum = 0.f, own = 0.f;
         {
             float2 ml[kWarps];
@@ -1094,10 +1099,10 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             for (int w = 0; w < kWarps; ++w) {
                 const float f = ml[w].y == 0.f ? 0.f : (ml[w].y != ml[w].y ? NAN : ex2(ml[w].x - top));
                 sum += f * ml[w].y;
-                if (w == warp) own = f == 0.f ? 0.f : f * vref;
+                if (w == warp) own = f;
             }
+            own *= q8_inverse(sum);
         }
-        const float inv = q8_inverse(sum);
         if (warp == 0 && lane < seq_rows) {
             if (kCluster)
                 s_sum[lane] = make_float2(top, sum);
@@ -1121,15 +1126,14 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                     const int c = u >> 1 << 1, k = u & 1;
                     const float f = k ? f1 : f0;
                     xbuf[(u * kWarps + warp) * 32 + lane] =
-                        make_float4(acc[i][c][k] * f, acc[i][c][2 + k] * f, acc[i][c + 1][k] * f,
-                                    acc[i][c + 1][2 + k] * f);
+                        make_float4(acc[i][c][k] * f * vref, acc[i][c][2 + k] * f * vref,
+                                    acc[i][c + 1][k] * f * vref, acc[i][c + 1][2 + k] * f * vref);
                 }
             }
             __syncthreads();
 #pragma unroll 1
             for (int u = warp; u < Cfg::kTileUnits; u += kWarps) {
                 const int r = 8 * n + 2 * t + (u & 1), un = n * Cfg::kTileUnits + u;
-                const float iv = __shfl_sync(0xffffffffu, inv, r);
                 if (r >= seq_rows) continue;
                 float4 o = xbuf[u * kWarps * 32 + lane];
 #pragma unroll
@@ -1137,15 +1141,12 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
                     const float4 v = xbuf[(u * kWarps + w) * 32 + lane];
                     o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
                 }
-                if (!cut && !kCluster) {
-                    q8_store_unit<D, NT>(p, row0, h0, un, lane, o, iv);
-                } else {
-                    o.x *= iv, o.y *= iv, o.z *= iv, o.w *= iv;
-                    if (kCluster)  // (the ring is idle: this is the range's end)
-                        reinterpret_cast<float4*>(ring)[un * 32 + lane] = o;
-                    else
-                        reinterpret_cast<float4*>(p.ws_o)[(wrow * Cfg::kUnits + un) * 32 + lane] = o;
-                }
+                if (!cut && !kCluster)
+                    q8_store_unit<D, NT>(p, row0, h0, un, lane, o);
+                else if (kCluster)  // (the ring is idle: this is the range's end)
+                    reinterpret_cast<float4*>(ring)[un * 32 + lane] = o;
+                else
+                    reinterpret_cast<float4*>(p.ws_o)[(wrow * Cfg::kUnits + un) * 32 + lane] = o;
             }
         }
         if (cut && !tail && !p.merge_kernel) {

@@ -1,11 +1,12 @@
 """GPU tests of include/pa_q8.h at what its first tests left open: outputs off by no more than
-their own rounding."""
+their own rounding and V scales at the ends of their range."""
 import numpy as np
 import pytest
+import torch
 
 import paged_kv_gqa_pa_gb300 as pa
 from paged_kv_gqa_pa_gb300 import build as pa_build
-from test_q8_gpu import DIMS, Decode, rounded
+from test_q8_gpu import DIMS, Decode, T, host, i32, rounded, to_t
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,45 @@ def test_decode_rows_are_off_by_their_own_rounding(D, dtype, queries, cluster, s
     want, tol = narrow(d, 1.0)
     over = np.abs(out - want) - tol - half_step(np.abs(want) + tol, dtype)
     assert not (over > 0).any(), f"{np.mean(over > 0):.2e} of the elements"
+
+
+# ---------------------------------------------------------------- attention: V scales of any size
+
+@pytest.mark.parametrize("form", ["whole", "cut", "merged", "cluster"])
+@pytest.mark.parametrize("low,high", [(100, 100), (120, 120), (126, 126), (100, 126), (-120, -120),
+                                      (-126, -126), (-140, -128), (-149, -110)])
+@pytest.mark.parametrize("queries", [1, 4])
+@pytest.mark.parametrize("D", [64, 256])
+def test_decode_v_scales_of_any_size(D, queries, low, high, form):
+    """Scales of 2^low to 2^high, subnormal ones among them, where every value of V is finite."""
+    lens = [40, 300, 1, 17] if form == "whole" else [900, 300, 1500, 20]
+    d = Decode([D, queries, high + 200], lens, 4, 2, D, "bf16", T=queries)
+    x = d.codes[1]  # codes of at most 1.75 either way
+    d.codes[1] = np.where(x & 127 == 127, 127, (x & 0x80) | (0x20 + (x & 0x1F)) - ((x & 0x1F) == 0x1F))
+    d.scales[1] = 2.0 ** d.g.integers(low, high + 1, d.scales[1].shape)
+    assert (d.scales[1] > 0).all()
+    if form == "merged":  # (so many CTAs for the sequences that a kernel of its own merges)
+        p = d.plan()
+        p.cluster, p.ctas_per_group, p.workspace_bytes = 0, 60, 1 << 27
+        ws = torch.zeros(1 << 27, dtype=torch.uint8, device="cuda")
+        tq = to_t(d.q, "bf16")
+        out, lse = torch.full_like(tq, 3.0), torch.empty(tq.shape[0], 4, device="cuda")
+        pa.pa_q8_decode(p, tq, i32(d.starts), *d.device(), i32(d.bt), i32(d.lens), 0.1, 0, out, lse, ws)
+        got = host(out), host(lse), pa.pa_get_error(ws)
+    else:
+        p = d.plan()
+        assert form != "cluster" or p.cluster > 1
+        got = d.run(0.1, **{"whole": dict(cluster=0, ctas=4), "cut": dict(ctas=7), "cluster": {}}[form])
+    d.check(got, d.want(0.1, 0))
+
+
+@pytest.mark.parametrize("first", ["zero", "subnormal", "least", "one"])
+@pytest.mark.parametrize("queries", [1, 4])
+def test_decode_v_scales_that_rise(first, queries):
+    """A page of scale 0, subnormal or least in front of ordinary ones, in every warp."""
+    d = Decode([7, queries], [600, 90], 4, 1, 128, "bf16", T=queries)
+    for b, n in ((0, 38), (1, 6)):
+        d.scales[1, d.bt[b, :n // 2], 0] = {"zero": 0.0, "subnormal": 2.0 ** -140, "least": 2.0 ** -120,
+                                           "one": 1.0}[first]
+    d.case(0.1)
+    d.case(0.1, ctas=1)
