@@ -1,12 +1,13 @@
 """GPU tests of include/pa_q8.h at what its first tests left open: outputs off by no more than
-their own rounding and V scales at the ends of their range."""
+their own rounding, V scales at the ends of their range and scores that overflow."""
 import numpy as np
 import pytest
 import torch
 
 import paged_kv_gqa_pa_gb300 as pa
+from paged_kv_gqa_pa_gb300 import binding, q8
 from paged_kv_gqa_pa_gb300 import build as pa_build
-from test_q8_gpu import DIMS, Decode, T, host, i32, rounded, to_t
+from test_q8_gpu import DIMS, Decode, Rows, T, host, i32, i64, rounded, to_t
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +128,66 @@ def test_decode_v_scales_that_rise(first, queries):
                                            "one": 1.0}[first]
     d.case(0.1)
     d.case(0.1, ctas=1)
+
+
+# ---------------------------------------------------------------- attention: scores that overflow
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("queries", [1, 4])
+@pytest.mark.parametrize("cluster", [None, 0])
+def test_decode_scores_beyond_fp32_by_sign(dtype, queries, cluster):
+    """Scores that overflow to -inf weigh nothing, those to +inf make their rows NaN, and the rows of
+    the other heads stay what they are."""
+    L, Hq, D = 700, 5, 128
+    # (the factor of the products, K's scale times the call's in the log2 domain, is finite)
+    big, scale, small = (2.0 ** 14, 2.0 ** 8, 0.0) if dtype == "f16" else (2.0 ** 44, 2.0 ** -22, 2.0 ** -77)
+    d = Decode([queries, 3], [L, 50], Hq, 1, D, dtype, T=queries, new=[queries, 1])
+    k = d.codes[0]
+    d.codes[0] = np.where(k & 127 == 127, 127, (k & 0x80) | (0x28 + (k & 7)))  # 0.25 to 0.47 either way
+    gone = np.zeros(L, bool)
+    gone[d.g.permutation(L)[:300]] = True
+    gone[16:16 * 9] = True  # whole pages
+    gone[0] = gone[L - queries:] = False
+    pos = np.arange(L)
+    cells = d.bt[0][pos // 16], 0, pos % 16
+    d.codes[0][cells + (5,)] = np.where(gone, 0xFE, 0)  # -448, 0
+    d.codes[0][cells + (9,)] = 0xFE
+    d.scales[0] = 2.0 ** 100
+    d.q[:] = 0.0
+    d.q[:, 0, 5] = d.q[:, 2, 9] = big
+    d.q[:, 1, 5] = -big
+    d.q[:, 3, 3] = small
+    out, lse, err = d.run(scale, cluster=cluster)
+    assert err == 0
+    w, wl, tol, ltol = d.want(scale, 0)
+    row = slice(0, queries)
+    assert np.isnan(out[row, 1]).all() and np.isnan(lse[row, 1]).all()
+    assert (out[row, 2] == 0).all() and np.isneginf(lse[row, 2]).all()
+    for h in (3, 4):
+        assert (np.abs(out[row, h] - w[row, h]) <= tol[row, h]).all()
+        assert (np.abs(lse[row, h] - wl[row, h]) <= ltol[row, h]).all()
+    # head 0: equal weights of what is not gone, sums in fp32
+    v = d.values()[1][cells]
+    for t in range(queries):
+        see = ~gone & (pos < L - queries + 1 + t)
+        mean, room = v[see].mean(0), 2.0 ** -16 * np.abs(v[see]).mean(0)
+        assert (np.abs(out[t, 0] - mean) <= room + half_step(np.abs(mean) + room, dtype)).all()
+        assert abs(lse[t, 0] - np.log(see.sum())) <= 2.0 ** -16
+
+
+# ---------------------------------------------------------------- norm weights without q
+
+def test_append_without_q_does_not_use_its_norm():
+    """With no q heads q_norm is not used, wherever it points and whatever eps is."""
+    n, hkv, D = 20, 2, 64
+    r = Rows(3, n, 0, hkv, D, "f16", False, 0.0, D)
+    caches = [torch.zeros(2, hkv, 16, D, dtype=torch.float16, device="cuda") for _ in range(2)]
+    slots, w = i64(np.arange(n)), torch.ones(D + 1, dtype=torch.float16, device="cuda")
+    s = r.tk.stride(0)
+    st = q8._lib().pa_append(n, 0, hkv, D, D, 16, 2, 0, 0.0, -1.0, None, 0, r.tk.data_ptr(), s,
+                             r.tv.data_ptr(), s, w[1:].data_ptr(), None, None, slots.data_ptr(), None, 0,
+                             caches[0].data_ptr(), caches[1].data_ptr(), None,
+                             torch.cuda.current_stream().cuda_stream)
+    assert st == binding.PA_OK
+    for c, want in zip(caches, (r.k, r.v)):
+        np.testing.assert_array_equal(host(c).transpose(0, 2, 1, 3).reshape(-1, hkv, D)[:n], want)
