@@ -1,13 +1,16 @@
 """GPU tests of include/pa_q8.h at what its first tests left open: outputs off by no more than
-their own rounding, V scales at the ends of their range and scores that overflow."""
+their own rounding, V scales at the ends of their range, scores that overflow and q beside 8-bit
+rows through the rings."""
 import numpy as np
 import pytest
 import torch
 
 import paged_kv_gqa_pa_gb300 as pa
+import q8_reference as ref
 from paged_kv_gqa_pa_gb300 import binding, q8
 from paged_kv_gqa_pa_gb300 import build as pa_build
-from test_q8_gpu import DIMS, Decode, Rows, T, host, i32, i64, rounded, to_t
+from test_q8_gpu import (DIMS, Decode, Rows, T, check_q8, host, i32, i64, page_slots, rounded,
+                         run_q8_append, to_t)
 
 pytestmark = pytest.mark.gpu
 
@@ -173,6 +176,37 @@ def test_decode_scores_beyond_fp32_by_sign(dtype, queries, cluster):
         mean, room = v[see].mean(0), 2.0 ** -16 * np.abs(v[see]).mean(0)
         assert (np.abs(out[t, 0] - mean) <= room + half_step(np.abs(mean) + room, dtype)).all()
         assert abs(lse[t, 0] - np.log(see.sum())) <= 2.0 ** -16
+
+
+# ---------------------------------------------------------------- q beside 8-bit rows, by rings
+
+@pytest.mark.parametrize("D,rot,dtype,hq,n,norm", [(256, 128, "bf16", 32, 3100, True), (256, 256, "f16", 17, 5800, False),
+                                                   (128, 64, "f32", 40, 2461, True), (96, 96, "f16", 48, 5470, True),
+                                                   (64, 32, "bf16", 65, 6060, True)])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_q8_append_many_large_q_rows(D, rot, dtype, hq, n, norm, inplace):
+    """q of 8 KB a token and more, 48 MB in all: it goes through the rings, by a launch of its own."""
+    es = 4 if dtype == "f32" else 2
+    assert hq * D * es >= 8 << 10 and n * hq * D * es >= 48 << 20
+    hkv, pages = 2, n // 16 + 2
+    r = Rows([D, n], n, hq, hkv, D, dtype, norm, 1e4, rot)
+    slots = page_slots(r.g, n, pages, 5)
+    slots[n // 2] = -1 if slots[n // 2] % 16 == 15 else slots[n // 2]
+    caches = pa.new_q8_cache(pages, hkv, D)
+    rk, rv = ref.Cache(pages, hkv, D), ref.Cache(pages, hkv, D)
+    rk.codes[...] = rv.codes[...] = 0
+    q_out = r.tq if inplace else torch.full((n + 2, hq, D), 3.0, dtype=T[dtype], device="cuda")
+    run_q8_append(r, slots, caches, q_out if inplace else q_out[1:-1])
+    if not inplace:
+        assert (q_out[0] == 3).all() and (q_out[-1] == 3).all()
+        q_out = q_out[1:-1]
+    for lo in range(0, n, 512):  # (the reference's fp64 rows a share at a time)
+        x = r.q[lo:lo + 512]
+        w = ref.turned(x, r.w[0], r.pos[lo:lo + 512], r.eps, r.theta, rot)
+        tol = ref.turned_tolerance(x, r.w[0], w, r.eps, r.theta, rot, dtype)
+        assert (np.abs(host(q_out[lo:lo + 512]) - w) <= tol).all()
+    np.testing.assert_array_equal(host(r.tv), r.v)
+    check_q8(r, slots, caches, rk, rv, exact_k=False)
 
 
 # ---------------------------------------------------------------- norm weights without q
