@@ -1,6 +1,6 @@
 """GPU tests of include/pa_q8.h at what its first tests left open: outputs off by no more than
-their own rounding, V scales at the ends of their range, scores that overflow and q beside 8-bit
-rows through the rings."""
+their own rounding, V scales at the ends of their range, scores that overflow, q beside 8-bit
+rows through the rings and verification of more sequences than one wave holds."""
 import numpy as np
 import pytest
 import torch
@@ -9,8 +9,8 @@ import paged_kv_gqa_pa_gb300 as pa
 import q8_reference as ref
 from paged_kv_gqa_pa_gb300 import binding, q8
 from paged_kv_gqa_pa_gb300 import build as pa_build
-from test_q8_gpu import (DIMS, Decode, Rows, T, check_q8, host, i32, i64, page_slots, rounded,
-                         run_q8_append, to_t)
+from test_q8_gpu import (DIMS, Decode, Rows, T, check_q8, check_verify, host, i32, i64,
+                         page_slots, rounded, run_q8_append, to_t, verify_case)
 
 pytestmark = pytest.mark.gpu
 
@@ -207,6 +207,26 @@ def test_q8_append_many_large_q_rows(D, rot, dtype, hq, n, norm, inplace):
         assert (np.abs(host(q_out[lo:lo + 512]) - w) <= tol).all()
     np.testing.assert_array_equal(host(r.tv), r.v)
     check_q8(r, slots, caches, rk, rv, exact_k=False)
+
+
+# ---------------------------------------------------------------- verification of many sequences
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("B,V,drafts,ctas", [(160, 33000, 1, 640), (80, 70000, 2, 640), (155, 32771, 2, 620),
+                                             (310, 20000, 2, 620), (610, 1500, 2, 610)])
+def test_verify_more_sequences_than_a_wave(B, V, drafts, ctas, dtype):
+    """More CTAs than one wave of 608: rows with few loads in flight, with and without clusters."""
+    c = 1
+    while c < 8 and V >= c * 2 * 2048:
+        c *= 2
+    while c > 1 and B * c > 608 and V <= c // 2 * 16384:
+        c //= 2
+    assert B * c == ctas > 608
+    case = verify_case([V, B], B, V, drafts, dtype, ragged=True)
+    check_verify(case, dtype)
+    check_verify(case, dtype, offset=1)
+    case["draft"], case["num"] = None, None
+    check_verify(case, dtype)
 
 
 # ---------------------------------------------------------------- norm weights without q
