@@ -998,7 +998,9 @@ static int append_call(bool q8, int num_tokens, int num_q_heads, int num_kv_head
                        float* k_scales, float* v_scales, uint32_t* device_error, void* stream) {
     const int st = check_rows(num_tokens, num_kv_heads, head_dim, page_size, num_pages, dtype);
     if (st == PA_ERR_INVALID_ARG) return st;
-    const bool rotate = theta != 0.f, norm = q_norm || k_norm, has_q = num_q_heads > 0;
+    const bool rotate = theta != 0.f, has_q = num_q_heads > 0;
+    if (!has_q) q_norm = nullptr;
+    const bool norm = q_norm || k_norm;
     if (num_q_heads < 0 || !(theta >= 0.f) || theta == INFINITY ||
         (rotate && (rotary_dim <= 0 || rotary_dim > head_dim)) ||
         (norm && (!(eps >= 0.f) || eps == INFINITY)))
@@ -1033,7 +1035,7 @@ static int append_call(bool q8, int num_tokens, int num_q_heads, int num_kv_head
     p.q = static_cast<const unsigned char*>(q);
     p.k = static_cast<const unsigned char*>(k);
     p.v = static_cast<const unsigned char*>(v);
-    p.q_norm = has_q ? static_cast<const unsigned char*>(q_norm) : nullptr;
+    p.q_norm = static_cast<const unsigned char*>(q_norm);
     p.k_norm = static_cast<const unsigned char*>(k_norm);
     p.q_out = static_cast<unsigned char*>(q_out);
     p.k_cache = static_cast<unsigned char*>(k_cache);
