@@ -38,7 +38,8 @@ extern "C" {
  *     y = x * w / sqrt(mean(x^2) + eps)      with a norm weight w, else y = x
  *     dims i and i + R/2, i < R/2, R = rotary_dim, turned by
  *         positions[t] * theta^(-2 i / R)    (dims R .. D - 1 as they are)
- * v is copied.  All of it is fp32 (angles as in pa_rope_axes), rounded once.
+ * v is copied.  All of it is fp32 (angles, from frequencies of 64 bits, with cosines and
+ * sines within 2^-23.6), rounded once.
  *   q, k, v      T [num_tokens, Hq or Hkv, D], T = fp16, bf16 or fp32; consecutive
  *                tokens *_stride elements apart (columns of a fused projection's
  *                rows), 16-byte aligned, strides multiples of 16 bytes

@@ -14,7 +14,8 @@ namespace pa {
 const unsigned long long* rope_frequency_table(float theta, int R);
 
 // Cosine and sine of position * frequency.  The product modulo 2^64 is the angle
-// modulo one turn; its top 32 bits, as a signed fraction, go to fp32 and sincospif.
+// modulo one turn; its top 32 bits, as a signed fraction, go to fp32 and sincospif.  (pa_rope.cu's;
+// pa_append.cu has one that is off by half as much.)
 __device__ __forceinline__ void rope_angle(int pos, unsigned long long freq, float& cs, float& sn) {
     const unsigned long long turns = (unsigned long long)(long long)pos * freq;
     sincospif((float)(int)(turns >> 32) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31: half turns

@@ -1,6 +1,7 @@
 """GPU tests of include/pa_q8.h at what its first tests left open: outputs off by no more than
 their own rounding, V scales at the ends of their range, scores that overflow, q beside 8-bit
-rows through the rings and verification of more sequences than one wave holds."""
+rows through the rings, verification of more sequences than one wave holds, angles and q_norm
+without q."""
 import numpy as np
 import pytest
 import torch
@@ -227,6 +228,38 @@ def test_verify_more_sequences_than_a_wave(B, V, drafts, ctas, dtype):
     check_verify(case, dtype, offset=1)
     case["draft"], case["num"] = None, None
     check_verify(case, dtype)
+
+
+# ---------------------------------------------------------------- angles
+
+@pytest.mark.parametrize("n,hq,hkv", [(300, 2, 1), (1500, 1, 2), (900, 30, 1)])  # (threads; rings)
+@pytest.mark.parametrize("theta,rot,far", [(1e4, 128, False), (1e4, 128, True), (5e5, 64, True)])
+def test_append_cosines_and_sines_are_fp32s(n, hq, hkv, theta, rot, far):
+    """Rows (1 .. 1, 0 .. 0) become cosines and sines.  Of a position's 64-bit turn the top 32 bits
+    count (2^-32 of a turn), at most an eighth of a turn either way goes to fp32 (2^-28 of a turn, half a
+    step), and the functions have a unit in the last place next to 1, 2^-24.  (Exactly: the steps
+    of an angle x of at most a quarter half turn in fp32 leave the cosine, for z = x^2 <= 2^-4 and
+    its series 1 + z Q with 4 <= |Q| < 8, half a step of the sum, 2^-25, of Q and of its constant,
+    2^-4 2^-22 and 2^-4 1.5e-7, and of z, 2^-29 |Q|: 6.3e-8, with sin(pi / 4) of the angle's 2.5e-8
+    together 8.1e-8 of the 8.4e-8 here; the sine's are smaller.)"""
+    g = np.random.default_rng([n, rot])
+    pos = (g.integers(-2 ** 31, 2 ** 31 - 1, n) if far else g.integers(0, 100000, n)).astype(np.int32)
+    half, pages = rot // 2, n // 16 + 1
+    x = torch.zeros(n, hq + 2 * hkv, 128, device="cuda")
+    x[..., :half] = 1.0
+    q_out = torch.empty(n, hq, 128, device="cuda")
+    kc, vc = (torch.zeros(pages, hkv, 16, 128, device="cuda") for _ in range(2))
+    pa.pa_append(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], i64(np.arange(n)), i32(pos), kc, vc,
+                 q_out=q_out, theta=theta, rotary_dim=rot)
+    # (64 bits and more: a position of 2^31 has 31 of a double's 53 in front of the point)
+    f = np.longdouble(theta) ** (-2 * np.arange(half, dtype=np.longdouble) / rot)
+    ang = pos.astype(np.longdouble)[:, None] * f
+    want = np.concatenate([np.cos(ang), np.sin(ang)], 1)[:, None]
+    room = 2 * np.pi * (2.0 ** -28 + 2.0 ** -32) + 2.0 ** -24
+    k = kc.transpose(1, 2).reshape(-1, hkv, 128)[:n]
+    for got in (q_out, k):
+        assert np.abs(host(got)[..., :rot] - want).max() <= room
+        assert (host(got)[..., rot:] == 0).all()
 
 
 # ---------------------------------------------------------------- norm weights without q
