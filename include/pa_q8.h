@@ -202,6 +202,9 @@ int pa_q8_decode(const pa_q8_plan_t* plan, int num_rows, const void* q, const in
  * draft outside [0, V) is not accepted (PA_DEVERR_BAD_TOKEN); a number of drafts is
  * limited to [0, max_drafts] (PA_DEVERR_BAD_TOKEN).
  * max_drafts 0 to 32, V 1 to 524288.
+ * (A loop with pa_extend_tables: its next call counts pages by the tokens that are kept,
+ * so the caller gives back those that only drafts that were not accepted had begun, entries
+ * ceil(kept / 16) .. ceil(context_len / 16) - 1 of a sequence's row.)
  */
 #define PA_VERIFY_MAX_DRAFTS 32
 int pa_verify_drafts(int batch, int max_drafts, int vocab, int dtype, const void* target_probs,

@@ -1,17 +1,17 @@
 """GPU tests of include/pa_q8.h at what its first tests left open: outputs off by no more than
 their own rounding, V scales at the ends of their range, scores that overflow, q beside 8-bit
-rows through the rings, verification of more sequences than one wave holds, angles and q_norm
-without q."""
+rows through the rings, verification of more sequences than one wave holds, angles, q_norm
+without q and the pages of drafts that were not accepted."""
 import numpy as np
 import pytest
 import torch
 
 import paged_kv_gqa_pa_gb300 as pa
 import q8_reference as ref
-from paged_kv_gqa_pa_gb300 import binding, q8
+from paged_kv_gqa_pa_gb300 import binding, q4, q8
 from paged_kv_gqa_pa_gb300 import build as pa_build
-from test_q8_gpu import (DIMS, Decode, Rows, T, check_q8, check_verify, host, i32, i64,
-                         page_slots, rounded, run_q8_append, to_t, verify_case)
+from test_q8_gpu import (DIMS, Decode, Rows, T, check_q8, check_verify, code_bytes, host, i32,
+                         i64, page_slots, rounded, run_q8_append, to_t, verify_case)
 
 pytestmark = pytest.mark.gpu
 
@@ -278,3 +278,68 @@ def test_append_without_q_does_not_use_its_norm():
     assert st == binding.PA_OK
     for c, want in zip(caches, (r.k, r.v)):
         np.testing.assert_array_equal(host(c).transpose(0, 2, 1, 3).reshape(-1, hkv, D)[:n], want)
+
+
+# ---------------------------------------------------------------- pages of drafts that were not accepted
+
+def free_list(past_lens, block_tables, num_pages):
+    """The pages that no token in past_lens lies in, on the device; behind them ids of no page."""
+    held = torch.arange(block_tables.shape[1], device="cuda") < ((past_lens + 15) // 16)[:, None]
+    free = torch.ones(num_pages + 1, dtype=torch.bool, device="cuda")
+    free[torch.where(held, block_tables, num_pages).long()] = False
+    ids = torch.arange(num_pages, dtype=torch.int32, device="cuda")
+    return torch.where(free[:-1], ids, num_pages).sort().values.int()
+
+
+@pytest.mark.parametrize("give_back", [True, False])
+def test_pages_of_drafts_that_were_not_accepted(give_back):
+    """The loop over tables, rows, attention and verification, drafts mostly not accepted: with the
+    pages that only they had begun given back the pool lasts, without them it runs out."""
+    g = np.random.default_rng(6)
+    B, Hq, Hkv, D, maxp, pages, drafts, V, steps = 4, 4, 2, 64, 8, 36, 4, 60, 100
+    scale, n = D ** -0.5, B * (drafts + 1)
+    caches = pa.new_q8_cache(pages, Hkv, D)
+    plan = pa.pa_q8_plan(B, Hq, Hkv, D, 16, pages, maxp, maxp * 16, max_query_len=drafts + 1)
+    ws = pa.new_workspace(plan, "cuda")
+    table, past, ctx = i32(np.full((B, maxp), -1)), i32(np.zeros(B)), i32(np.zeros(B))
+    new, starts, pos, taken = i32(np.full(B, drafts + 1)), i32(np.zeros(B + 1)), i32(np.zeros(n)), i32([0])
+    slots = torch.zeros(n, dtype=torch.int64, device="cuda")
+    free = torch.arange(pages, dtype=torch.int32, device="cuda")
+    err = i32(np.zeros(64))
+    accepted, tokens = i32(np.zeros(B)), i32(np.zeros((B, drafts + 1)))
+    hp = np.zeros(B, np.int64)
+    for step in range(steps):
+        if hp.max() + drafts + 1 > maxp * 16:
+            break
+        r = Rows([5, step], n, Hq, Hkv, D, "f16", False, 0.0, D)
+        q, out, lse = r.tq.contiguous(), torch.zeros(n, Hq, D, dtype=T["f16"], device="cuda"), torch.zeros(n, Hq, device="cuda")
+        pa.pa_extend_tables(past, new, free, pages, table, ctx, starts, slots, pos, taken, err)
+        pa.pa_q8_append(q, r.tk, r.tv, slots, pos, *caches)
+        pa.pa_q8_decode(plan, q, starts, *caches, table, ctx, scale, 0, out, lse, ws)
+        c = verify_case([8, step], B, V, drafts, "f32", near=3.0)
+        args = [to_t(c["target"], "f32"), to_t(c["draft"], "f32"), i32(c["tok"]), None,
+                torch.from_numpy(c["accept"]).cuda(), torch.from_numpy(c["sample"]).cuda()]
+        pa.pa_verify_drafts(*args, accepted, tokens)
+        bad = pa.pa_get_error_ex(err)
+        if bad:
+            break
+        # every token's row is where the table says, and no page belongs to two sequences
+        bt = table.cpu().numpy()
+        lens = hp + drafts + 1
+        np.testing.assert_array_equal(ctx.cpu().numpy(), lens)
+        at = (hp[:, None] + np.arange(drafts + 1)).ravel()
+        want = bt[np.arange(B).repeat(drafts + 1), at // 16].astype(np.int64) * 16 + at % 16
+        np.testing.assert_array_equal(slots.cpu().numpy(), want)
+        held = np.concatenate([bt[b, :-(-lens[b] // 16)] for b in range(B)])
+        assert len(set(held)) == len(held) and (held >= 0).all() and (held < pages).all()
+        k, v = (ref.E4M3[code_bytes(x)] * host(y)[..., None, None] for x, y in ((caches[0], caches[2]), (caches[1], caches[3])))
+        w, wl, tol, ltol = ref.decode(host(q), k, v, bt, lens, np.arange(B + 1) * (drafts + 1), scale, 0, "f16")
+        assert (np.abs(host(out) - w) <= tol).all() and (np.abs(host(lse) - wl) <= ltol).all()
+        past.add_(accepted + 1)
+        hp = hp + accepted.cpu().numpy() + 1
+        np.testing.assert_array_equal(past.cpu().numpy(), hp)
+        free = free_list(past, table, pages) if give_back else free[int(taken):]
+    if give_back:
+        assert bad == 0 and pa.pa_get_error(ws) == 0 and hp.max() > 100
+    else:
+        assert bad == q4.PA_DEVERR_NO_PAGES and hp.max() < 100
