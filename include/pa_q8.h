@@ -160,13 +160,14 @@ int pa_q8_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int p
  * than max_query_len apart too, and for starts that do not ascend or lie outside
  * [0, num_rows], where it is not known which rows the sequence has: none is written).
  * Precision: the codes of K and V and q are exact in the products (bf16 rows of q are
- * scaled by a power of two), scores, maxima and sums fp32.  Scores are these products times
- * one fp32 factor, the call's scale times log2(e), K's scale and q's power of two: a factor
- * that overflows makes its rows NaN, a score that does to -inf weighs nothing.  In the product with V a
- * weight, times its page's V scale relative to the greatest met, is two fp16 numbers, a
- * head and a rest (22 bits; what is below 2^-33 of the row's greatest weight is nothing);
- * products are summed in fp32 and normalised by the fp32 sum of the weights, which lse
- * has too.
+ * scaled by a power of two; elements below 2^-28 of their row's largest are rounded, by at
+ * most 2^-39 of it), scores, maxima and sums fp32.  Scores are these products times one
+ * fp32 factor, the call's scale times log2(e), K's scale and q's power of two: a factor
+ * that overflows makes its rows NaN, a score that does to -inf weighs nothing.  In the
+ * product with V a weight, times its page's V scale relative to the greatest met, is two
+ * fp16 numbers, a head and a rest (22 bits; what is below 2^-33 of the row's greatest
+ * weight is nothing); products are summed in fp32 and normalised by the fp32 sum of the
+ * weights, which lse has too.
  * workspace as for pa_q4_decode.
  */
 int pa_q8_decode(const pa_q8_plan_t* plan, int num_rows, const void* q, const int32_t* starts,

@@ -29,7 +29,7 @@ namespace pa {
 constexpr int kAppendThreads = 256;  // at most, of pa_append
 constexpr int kMaxTileBytes = 48 << 10;  // of rows that a CTA holds at a time
 // Tokens whose q a CTA beside 8-bit runs serves, at most (16384 tokens of 8 + 2 x 2 heads of 64,
-// appended and read back: 1 26.1 us, 4 18.5, 8 the same).
+// appended and read back: 1 26.1 us, 4 18.2, 8 the same).
 constexpr int kQTokens = 4;
 // Tiles have 16 rows where that makes so many of them, times KV heads, times two; see append_call.
 constexpr int kAppendTiles = 38;

@@ -48,7 +48,7 @@ constexpr int q8_short(int D) { return D == 256 ? 16 : 24; }
 constexpr int kQ8Start = 12;
 // Where there is a CTA for each sequence, each has one unless the longest has so many pages
 // more than an equal range costs: that many are as long as cutting and joining.  (48 of 57
-// CTAs a head, head_dim 128, sequences of 560 tokens 18.4 -> 13.1 us, of 2000 39.2 -> 35.2; with
+// CTAs a head, head_dim 128, sequences of 560 tokens 18.4 -> 13.1 us, of 2000 39.2 -> 35.6; with
 // 48 pages instead, 30 of up to 1000 tokens 13.1 -> 16.2.)
 constexpr int kQ8Whole = 24;
 // The running maximum (log2 domain) before any score: below every score that
@@ -63,7 +63,7 @@ constexpr float kQ8Room = 8.f, kQ8Most = 15.f;
 constexpr float kQ8LeastRatio = 0x1p-8f;
 constexpr int kQ8MaxRows = 32;  // query rows of a CTA (NT tiles of 8)
 
-constexpr int q8_max_rows(int D) { return D == 256 ? 16 : 32; }
+constexpr int q8_max_rows(int D) { return D == 256 ? 16 : kQ8MaxRows; }
 
 struct Q8Maps {
     CUtensorMap k, v;
@@ -739,9 +739,9 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
             }
         }
     };
-    // bf16 rows become fp16 exactly: times the power of two that brings the row's
-    // largest element to 2^14 .. 2^15, where fp16 has 28 octaves of normal numbers
-    // below it (elements further below lose bits that are 2^-39 of the largest).
+    // bf16 rows become fp16 by the power of two that brings the row's largest element to
+    // 2^14 .. 2^15: exactly, where an element is within 28 octaves of it (so far down fp16
+    // has normal numbers); smaller ones are rounded to multiples of 2^-38 of it at most.
     auto begin_sequence = [&]() PA_INLINE_LAMBDA {
         seq_L = s_len[b];
         row0 = s_row[b];
