@@ -35,8 +35,9 @@ constexpr int kQTokens = 4;
 constexpr int kAppendTiles = 38;
 // Runs of a tile from which they are served side by side (a step of 64 sequences, 32 + 2 x 8
 // heads of 128, with the q rows and read back: 6.9 -> 6.1 us, of 776 with 16 + 2 x 4 14.1 -> 9.2,
-// of 6615 with 48 + 2 x 8 of 64 194 -> 58.3; two runs of a prompt's chunks are faster one after
-// the other, 7707 rows 72.5 and 79.7).
+// of 6615 with 48 + 2 x 8 of 64 194 -> 61; two runs of a prompt's chunks are faster one after
+// the other, 7707 rows 72.5 and 79.7).  That path's registers cost the others: 4093 rows of
+// 16 + 2 x 4 heads of 96 in chunks, with their read back, 14.4 -> 16.0 us.
 constexpr int kSideBySide = 3;
 constexpr int kAppendCtas = 608;     // CTAs that fill the GPU: four for each of 152 SMs
 

@@ -21,8 +21,8 @@ constexpr int kQ8MaxQuery = 16;     // query tokens of a sequence
 constexpr int kQ8MinRun = 2;
 constexpr int kQ8MaxCluster = 8;    // (the largest that every launch may have)
 // Pages of head_dim 128, see pa_q8_plan (16 sequences of 4096 tokens' window, five queries: 4
-// pages 44.4 us, 12 41.1; with 24, 12 of 10000 tokens each go 48.0 -> 43.8, but 12 of up to
-// 10000 25.7 -> 35.4).
+// pages 48.0 us, 12 46.9; with 24, 12 of 10000 tokens each go 48.0 -> 44.4, but 12 of up to
+// 10000 25.7 -> 37.2).
 constexpr int kQ8ClusterExtra = 12;
 // Partials per sequence beyond which a kernel merges (20 sequences of 6000 tokens: 2 50.4 us, 4
 // 45.3; 6 of 20000: 4 46.1, 12 47.5).

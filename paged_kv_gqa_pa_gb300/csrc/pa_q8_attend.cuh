@@ -18,9 +18,9 @@
 //
 // Bound by: the copies, where there is one tile of rows (4 sequences of 100000 tokens, 24/4
 // heads, D 256: 127 us, 0.95 of the copy rate; 16 of 8192 with two queries, 32/8, D 128: 49.2,
-// 0.81); with more the latency of a warp's page (four tiles of rows, eight queries: 103.5 us,
+// 0.81); with more the latency of a warp's page (four tiles of rows, eight queries: 102.6 us,
 // 0.39), whose accumulators leave two warps a scheduler; in short steps the start, of about
-// 1.3 us, and the joining of a sequence's states (16 of a 4096 window, five queries: 47.0 us
+// 1.3 us, and the joining of a sequence's states (16 of a 4096 window, five queries: 46.9 us
 // of a floor of 20).  Slots of a warp's ring, 2, 3, 4: 64 ragged sequences 47.8, 48.8, 48.9 us.
 #pragma once
 
@@ -43,8 +43,8 @@ namespace pa {
 // cluster (48 sequences of 24 pages 10.0 us, in ranges 15.1; beyond, see kQ8Whole).
 constexpr int q8_short(int D) { return D == 256 ? 16 : 24; }
 // What a sequence's start and end cost a CTA, in pages: equal ranges are equal
-// in this cost, not in pages.  (6, 12, 20: 64 ragged sequences 49.3, 48.8, 49.0 us, 16 with
-// five queries 44.9, 41.1, 41.1.)
+// in this cost, not in pages.  (6, 12, 20: 64 ragged sequences 47.7, 47.4, 47.6 us, 16 with
+// five queries 48.7, 46.9, 46.9.)
 constexpr int kQ8Start = 12;
 // Where there is a CTA for each sequence, each has one unless the longest has so many pages
 // more than an equal range costs: that many are as long as cutting and joining.  (48 of 57
@@ -991,9 +991,10 @@ __global__ void __launch_bounds__(kThreads, (Q8Cfg<D, NT>::kMinBlocks))
         const float on_weights = direct ? ratio : 1.f;
         // Weights, times the page's ratio, as two fp16 numbers each, a head and a rest: 22 bits, and
         // 2^-33 of the greatest at least.  P^T's fragments are S^T's, each 8 x 8 block transposed.
-        // (Heads alone, 11 bits, move rows across roundings' borders; with one or two tiles of
-        // rows the rests cost nothing, with three five queries of 16 sequences behind a window
-        // of 4096 go 41.7 -> 47.0 us, with four eight of 8192 91.5 -> 103.5: 8 cycles a product.)
+        // (Heads alone, 11 bits, move rows across roundings' borders.  The rests cost nothing with
+        // one tile of rows; with two 32 ragged sequences of four queries, head_dim 96, go 24.5 ->
+        // 26.5 us, 16 of two, 128, stay at 49.1; with three 16 of five behind a window of 4096 go
+        // 41.8 -> 46.9, with four 16 of eight 91.6 -> 102.6: 8 cycles a product.)
         uint32_t b0[NT][2], b1[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
